@@ -20,6 +20,8 @@ __all__ = [
     "dspark_version", "dspark_status_string",
     "dspark_draft_workspace_size", "dspark_draft_sample",
     "dspark_verify_workspace_size", "dspark_verify", "dspark_verify_check",
+    "dspark_kv_write", "dspark_kv_read", "dspark_paged_attention_workspace_size", "dspark_paged_attention",
+    "dspark_prompt_attention_workspace_size", "dspark_prompt_attention",
     "dspark_schedule", "dspark_debug_random_words", "dspark_debug_gumbel", "dspark_debug_bias_gemm",
     "dspark_profile_enable", "dspark_profile_collect", "dspark_profile_read", "dspark_profile_reset",
 ]
@@ -34,13 +36,17 @@ DSPARK_ERR_SCRATCH = -6
 DSPARK_NOALLOC_SCRATCH_BYTES = 8 << 20  # the allocation-free draft's fixed scratch (include/dspark.h)
 DSPARK_BF16 = 0
 DSPARK_F32 = 1
+DSPARK_F16 = 2
+DSPARK_E4M3 = 3
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdspark.so")
 
 _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
 _c_u64 = ctypes.c_uint64
+_c_i64 = ctypes.c_int64
 _c_size = ctypes.c_size_t
+_c_float = ctypes.c_float
 _f64p = ctypes.POINTER(ctypes.c_double)
 _i32p = ctypes.POINTER(ctypes.c_int32)
 
@@ -110,6 +116,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                _c_int, _c_int, _c_int, _c_int,
                                _c_void_p, _c_void_p, _c_size, _c_void_p], _c_int),
+        "dspark_kv_write": ([_c_void_p, _c_void_p, _c_i64, _c_i64, _c_int, _c_void_p, _c_int, _c_void_p, _c_void_p,
+                             _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int,
+                             _c_int, _c_int, _c_void_p], _c_int),
+        "dspark_kv_read": ([_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_void_p, _c_int,
+                            _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_int,
+                            _c_void_p], _c_int),
+        "dspark_paged_attention_workspace_size": ([_c_int] * 4, _c_size),
+        "dspark_paged_attention": ([_c_void_p, _c_i64, _c_int, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p,
+                                    _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_int, _c_int, _c_int, _c_float, _c_int, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_size, _c_void_p], _c_int),
+        "dspark_prompt_attention_workspace_size": ([_c_int] * 6, _c_size),
+        "dspark_prompt_attention": ([_c_void_p, _c_void_p, _c_void_p, _c_i64, _c_i64, _c_i64, _c_int, _c_void_p,
+                                     _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_int,
+                                     _c_void_p, _c_void_p, _c_void_p, _c_size, _c_void_p], _c_int),
         "dspark_schedule": ([_f64p, _c_int, _c_int, _f64p, _c_int, _i32p, _f64p, _f64p, _i32p], _c_int),
         "dspark_history_capacity": ([_i32p, _i32p, _c_int, _c_int, _c_int, ctypes.POINTER(ctypes.c_int64)], _c_int),
         "dspark_schedule_capacity": ([_f64p, _c_int, _c_int, ctypes.c_int64, _i32p, _f64p, _i32p], _c_int),
@@ -499,6 +520,233 @@ def dspark_sts_fit(conf, n_accept, grid, *, ell=None, n_bins: int = 15, ece_grid
                             _ptr(out["tau"]), _ptr(out["ece"]), _ptr(out.get("ece_grid")), _ptr(ws), ws.numel(),
                             _stream_ptr(stream))
     _check(st, "dspark_sts_fit")
+    return out
+
+
+# ---------------------------------------------------------------- cache and attention
+
+_row_types = None
+
+
+def _types():
+    global _row_types
+    if _row_types is None:
+        torch = _torch()
+        _row_types = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16, torch.float32: DSPARK_F32,
+                      torch.float8_e4m3fn: DSPARK_E4M3}
+    return _row_types
+
+
+def _rows(t, name, dtype, heads, device):
+    """Checks packed rows [n, heads, D] of one type whose heads lie densely in
+    each row (a slice of a wider row is fine); returns the row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [rows, {'heads' if heads is None else heads}, D]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n and ((s2 != 1 and d > 1) or (s1 != d and h > 1)):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return s0 if n > 1 else h * d
+
+
+def _row_dtype(t, name):
+    dt = _types().get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float16")
+    return dt
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, device):
+    """Checks a paged cache; returns (dtype, n_pages, n_kv_heads, page_size, D)."""
+    torch = _torch()
+    dt = _types().get(k_cache.dtype)
+    if dt is None:
+        raise TypeError(f"k_cache: dtype {k_cache.dtype}, expected bfloat16, float16 or float8_e4m3fn")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache: [n_pages, n_kv_heads, page_size, D]")
+    _need(k_cache, "k_cache", k_cache.dtype, None, device)
+    _need(v_cache, "v_cache", k_cache.dtype, k_cache.shape, device)
+    if dt == DSPARK_E4M3:
+        _need(k_scale, "k_scale", torch.uint8, k_cache.shape[:3], device)
+        _need(v_scale, "v_scale", torch.uint8, k_cache.shape[:3], device)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale/v_scale: only with a float8_e4m3fn cache")
+    return (dt,) + tuple(k_cache.shape)
+
+
+def _requests(row_offsets, n_rows, page_table, device):
+    """Checks the request arrays; returns (B, max_pages)."""
+    torch = _torch()
+    if page_table.dim() != 2:
+        raise ValueError("page_table: [B, max_pages]")
+    B = page_table.shape[0]
+    _need(page_table, "page_table", torch.int32, None, device)
+    if row_offsets is not None:
+        _need(row_offsets, "row_offsets", torch.int32, (B + 1,), device)
+    elif n_rows != B:
+        raise ValueError(f"row_offsets: needed for {n_rows} rows of {B} requests")
+    return B, page_table.shape[1]
+
+
+def _call_on(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current, on `stream` or its current stream."""
+    torch = _torch()
+    if device.index is None or device.index == torch.cuda.current_device():
+        return fn(*args, _stream_ptr(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_ptr(stream))
+
+
+def dspark_kv_write(k, v, k_cache, v_cache, cache_len, page_table, *, row_offsets=None, k_scale=None, v_scale=None,
+                    stream=None) -> None:
+    """Writes rows k, v [n, Hkv, D] (bfloat16 or float16; slices of wider rows
+    are fine) into the paged cache [n_pages, Hkv, page_size, D] of the same type
+    or float8_e4m3fn (then with k_scale, v_scale [n_pages, Hkv, page_size] uint8):
+    row i of request b, rows row_offsets[b] .. row_offsets[b + 1] - 1 (None: one
+    row a request), goes to position cache_len[b] + i of page_table [B, max_pages]."""
+    lib = load_library()
+    dev = k_cache.device
+    cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dt = _row_dtype(k, "k")
+    ks, vs = _rows(k, "k", k.dtype, Hkv, dev), _rows(v, "v", k.dtype, Hkv, dev)
+    n = k.shape[0]
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError(f"k/v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [rows, {Hkv}, {D}]")
+    B, max_pages = _requests(row_offsets, n, page_table, dev)
+    _need(cache_len, "cache_len", _torch().int32, (B,), dev)
+    st = _call_on(dev, stream, lib.dspark_kv_write, _ptr(k), _ptr(v), ks, vs, dt, _ptr(row_offsets), n,
+                  _ptr(cache_len), _ptr(page_table), B, max_pages, Hkv, D, _ptr(k_cache), _ptr(v_cache),
+                  _ptr(k_scale), _ptr(v_scale), cdt, n_pages, ps)
+    _check(st, "dspark_kv_write")
+
+
+def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=None, first=None, k_scale=None,
+                   v_scale=None, dtype=None, out: dict | None = None, stream=None) -> dict:
+    """Reads rows back: row i of request b is the token at position first[b] + i
+    (None: 0).  Returns {"k", "v"} [n_rows, Hkv, D] of `dtype` (None: the cache's
+    type, bfloat16 for a float8_e4m3fn cache); rows of no request keep what
+    ``out`` holds (a new result holds zeros there)."""
+    torch = _torch()
+    lib = load_library()
+    dev = k_cache.device
+    cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if dtype is None:
+        dtype = torch.bfloat16 if cdt == DSPARK_E4M3 else k_cache.dtype
+    dt = _types().get(dtype)
+    if dt is None:
+        raise TypeError(f"dtype: {dtype}, expected bfloat16 or float16")
+    B, max_pages = _requests(row_offsets, n_rows, page_table, dev)
+    if first is not None:
+        _need(first, "first", torch.int32, (B,), dev)
+    if out is None:
+        out = {n: torch.zeros((n_rows, Hkv, D), dtype=dtype, device=dev) for n in ("k", "v")}
+    for n in ("k", "v"):
+        _need(out[n], n, dtype, (n_rows, Hkv, D), dev)
+    st = _call_on(dev, stream, lib.dspark_kv_read, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), cdt,
+                  n_pages, ps, _ptr(row_offsets), n_rows, _ptr(first), _ptr(page_table), B, max_pages, Hkv, D,
+                  _ptr(out["k"]), _ptr(out["v"]), dt)
+    _check(st, "dspark_kv_read")
+    return out
+
+
+def _attention_outputs(q, lse, out):
+    torch = _torch()
+    if out is None:
+        # rows of no request stay zero
+        out = {"out": torch.zeros(q.shape, dtype=q.dtype, device=q.device)}
+        if lse:
+            out["lse"] = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
+    _need(out["out"], "out", q.dtype, q.shape, q.device)
+    if "lse" in out:
+        _need(out["lse"], "lse", torch.float32, q.shape[:2], q.device)
+    return out
+
+
+def dspark_paged_attention_workspace_size(max_rows: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return load_library().dspark_paged_attention_workspace_size(max_rows, n_heads, n_kv_heads, head_dim)
+
+
+def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_offsets=None, k_scale=None,
+                           v_scale=None, scale: float | None = None, causal: bool = True, lse: bool = False,
+                           max_rows: int | None = None, out: dict | None = None, workspace=None,
+                           stream=None) -> dict:
+    """Attention of each request's rows q [n, Hq, D] over its tokens in the paged
+    cache (see dspark_kv_write, which must have written the rows' own keys and
+    values).  max_rows: rows a request usually has at most (None: the average,
+    rounded up); scale: None = D^-1/2.  Returns {"out"[, "lse"], "workspace"};
+    pass ``out`` (a previous result) to reuse its buffers."""
+    lib = load_library()
+    dev = k_cache.device
+    cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dt = _row_dtype(q, "q")
+    qs = _rows(q, "q", q.dtype, None, dev)
+    n, Hq = q.shape[:2]
+    if q.shape[2] != D:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, heads, {D}]")
+    B, max_pages = _requests(row_offsets, n, page_table, dev)
+    _need(cache_len, "cache_len", _torch().int32, (B,), dev)
+    out = _attention_outputs(q, lse, out)
+    if max_rows is None:
+        max_rows = max(1, -(-n // B))
+    nbytes = lib.dspark_paged_attention_workspace_size(max_rows, Hq, Hkv, D)
+    if nbytes:  # 0: the call reports why
+        out["workspace"] = _workspace(nbytes, dev, workspace if workspace is not None else out.get("workspace"))
+    ws = out.get("workspace")
+    st = _call_on(dev, stream, lib.dspark_paged_attention, _ptr(q), qs, dt, _ptr(row_offsets), n, int(max_rows),
+                  _ptr(cache_len), _ptr(page_table), B, max_pages, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache),
+                  _ptr(k_scale), _ptr(v_scale), cdt, n_pages, ps, D ** -0.5 if scale is None else float(scale),
+                  int(bool(causal)), _ptr(out["out"]), _ptr(out.get("lse")), _ptr(ws),
+                  0 if ws is None else ws.numel())
+    _check(st, "dspark_paged_attention")
+    return out
+
+
+def dspark_prompt_attention_workspace_size(B: int, n_rows: int, n_kv_rows: int, n_heads: int, n_kv_heads: int,
+                                           head_dim: int) -> int:
+    return load_library().dspark_prompt_attention_workspace_size(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim)
+
+
+def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: float | None = None,
+                            causal: bool = True, lse: bool = False, out: dict | None = None, workspace=None,
+                            stream=None) -> dict:
+    """Attention over packed whole prompts: q [n, Hq, D], k and v [n_kv, Hkv, D]
+    (bfloat16 or float16; slices of a fused projection are fine), sequence b the
+    rows row_offsets[b] .. row_offsets[b + 1] - 1 of q and kv_offsets[b] ..
+    kv_offsets[b + 1] - 1 of k and v (None: the same rows).  Its query rows are
+    the last positions of its keys.  Returns {"out"[, "lse"], "workspace"}."""
+    torch = _torch()
+    lib = load_library()
+    dev = q.device
+    dt = _row_dtype(q, "q")
+    qs = _rows(q, "q", q.dtype, None, dev)
+    n, Hq, D = q.shape
+    ks, vs = _rows(k, "k", q.dtype, None, dev), _rows(v, "v", q.dtype, None, dev)
+    n_kv, Hkv = k.shape[:2]
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError(f"k/v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [rows, heads, {D}]")
+    B = row_offsets.numel() - 1
+    _need(row_offsets, "row_offsets", torch.int32, (B + 1,), dev)
+    if kv_offsets is not None:
+        _need(kv_offsets, "kv_offsets", torch.int32, (B + 1,), dev)
+    elif n_kv != n:
+        raise ValueError(f"kv_offsets: needed for {n} query rows and {n_kv} key rows")
+    out = _attention_outputs(q, lse, out)
+    nbytes = lib.dspark_prompt_attention_workspace_size(B, n, n_kv, Hq, Hkv, D)
+    if nbytes:  # 0: the call reports why
+        out["workspace"] = _workspace(nbytes, dev, workspace if workspace is not None else out.get("workspace"))
+    ws = out.get("workspace")
+    st = _call_on(dev, stream, lib.dspark_prompt_attention, _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, dt,
+                  _ptr(row_offsets), n, _ptr(kv_offsets), n_kv, B, Hq, Hkv, D,
+                  D ** -0.5 if scale is None else float(scale), int(bool(causal)), _ptr(out["out"]),
+                  _ptr(out.get("lse")), _ptr(ws), 0 if ws is None else ws.numel())
+    _check(st, "dspark_prompt_attention")
     return out
 
 

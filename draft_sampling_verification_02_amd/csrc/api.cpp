@@ -594,3 +594,241 @@ int dspark_profile_reset(void) {
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- attention
+
+namespace {
+
+bool head_dim_supported(int d) { return d == 64 || d == 128 || d == 256; }
+
+bool row_stride_ok(int64_t stride, int heads, int head_dim) {
+    return stride >= int64_t(heads) * head_dim && stride <= DSPARK_MAX_ROW_STRIDE && stride % 8 == 0;
+}
+
+// Sizes and types of a cache call, in the order their errors are reported.
+int cache_geometry(int dtype, const int32_t *row_offsets, int n_rows, int B, int max_pages, int n_kv_heads, int head_dim,
+                   int cache_dtype, int n_pages, int page_size) {
+    if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || (!row_offsets && n_rows != B))
+        return DSPARK_ERR_ARG;
+    if (n_kv_heads < 1 || n_kv_heads > DSPARK_MAX_HEADS || head_dim < 1 || n_pages < 1 || max_pages < 1 || page_size < 1)
+        return DSPARK_ERR_ARG;
+    if (int64_t(max_pages) * page_size > DSPARK_MAX_CACHE_TOKENS) return DSPARK_ERR_ARG;
+    if ((dtype != DSPARK_BF16 && dtype != DSPARK_F16 && dtype != DSPARK_F32 && dtype != DSPARK_E4M3) ||
+        (cache_dtype != DSPARK_BF16 && cache_dtype != DSPARK_F16 && cache_dtype != DSPARK_F32 &&
+         cache_dtype != DSPARK_E4M3))
+        return DSPARK_ERR_ARG;
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F16) return DSPARK_ERR_UNSUPPORTED;
+    if (cache_dtype != dtype && cache_dtype != DSPARK_E4M3) return DSPARK_ERR_UNSUPPORTED;
+    if (!head_dim_supported(head_dim)) return DSPARK_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return DSPARK_ERR_UNSUPPORTED;
+    return DSPARK_OK;
+}
+
+int cache_buffers(const void *k_cache, const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
+                  int cache_dtype) {
+    if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return DSPARK_ERR_ARG;
+    if (cache_dtype == DSPARK_E4M3 && (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)))
+        return DSPARK_ERR_ARG;
+    return DSPARK_OK;
+}
+
+// Query heads against key-value heads, and the rows they make.
+int head_geometry(int n_rows, int n_heads, int n_kv_heads) {
+    if (n_heads < 1 || n_heads > DSPARK_MAX_HEADS || n_kv_heads < 1 || n_heads % n_kv_heads != 0) return DSPARK_ERR_ARG;
+    if (int64_t(n_rows) * n_heads > INT32_MAX) return DSPARK_ERR_ARG;
+    return DSPARK_OK;
+}
+
+bool scale_ok(float scale) { return scale > 0.f && scale <= 3.4e38f; }
+
+}  // namespace
+
+extern "C" {
+
+int dspark_kv_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int dtype,
+                    const int32_t *row_offsets, int n_rows, const int32_t *cache_len, const int32_t *page_table, int B,
+                    int max_pages, int n_kv_heads, int head_dim, void *k_cache, void *v_cache, uint8_t *k_scale,
+                    uint8_t *v_scale, int cache_dtype, int n_pages, int page_size, void *stream) {
+    int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
+                            page_size);
+    if (st != DSPARK_OK) return st;
+    if (n_rows == 0) return DSPARK_OK;
+    if (!k || !v || !cache_len || !page_table || !aligned16(k) || !aligned16(v)) return DSPARK_ERR_ARG;
+    if (!row_stride_ok(k_stride, n_kv_heads, head_dim) || !row_stride_ok(v_stride, n_kv_heads, head_dim))
+        return DSPARK_ERR_ARG;
+    st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
+    if (st != DSPARK_OK) return st;
+    CacheArgs a{};
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.dtype = dtype;
+    a.row_offsets = row_offsets;
+    a.start = cache_len;
+    a.page_table = page_table;
+    a.B = B;
+    a.n_rows = n_rows;
+    a.max_pages = max_pages;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype;
+    a.n_pages = n_pages;
+    a.page_size = page_size;
+    return launch_cache(a, true, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
+int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
+                   int cache_dtype, int n_pages, int page_size, const int32_t *row_offsets, int n_rows,
+                   const int32_t *first, const int32_t *page_table, int B, int max_pages, int n_kv_heads, int head_dim,
+                   void *k_out, void *v_out, int dtype, void *stream) {
+    int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
+                            page_size);
+    if (st != DSPARK_OK) return st;
+    if (n_rows == 0) return DSPARK_OK;
+    if (!k_out || !v_out || !page_table || !aligned16(k_out) || !aligned16(v_out)) return DSPARK_ERR_ARG;
+    st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
+    if (st != DSPARK_OK) return st;
+    CacheArgs a{};
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.dtype = dtype;
+    a.row_offsets = row_offsets;
+    a.start = first;
+    a.page_table = page_table;
+    a.B = B;
+    a.n_rows = n_rows;
+    a.max_pages = max_pages;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.k_cache = const_cast<void *>(k_cache);
+    a.v_cache = const_cast<void *>(v_cache);
+    a.k_scale = const_cast<uint8_t *>(k_scale);
+    a.v_scale = const_cast<uint8_t *>(v_scale);
+    a.cache_dtype = cache_dtype;
+    a.n_pages = n_pages;
+    a.page_size = page_size;
+    return launch_cache(a, false, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
+size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim) {
+    if (max_rows < 1 || head_geometry(0, n_heads, n_kv_heads) != DSPARK_OK || !head_dim_supported(head_dim)) return 0;
+    size_t bytes = 0;
+    paged_carve(nullptr, paged_plan(max_rows, n_heads, n_kv_heads, head_dim, 0), head_dim, &bytes);
+    return bytes;
+}
+
+int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
+                           int max_rows, const int32_t *cache_len, const int32_t *page_table, int B, int max_pages,
+                           int n_heads, int n_kv_heads, int head_dim, const void *k_cache, const void *v_cache,
+                           const uint8_t *k_scale, const uint8_t *v_scale, int cache_dtype, int n_pages, int page_size,
+                           float scale, int causal, void *out, float *lse_out, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
+                            page_size);
+    if (st != DSPARK_OK) return st;
+    st = head_geometry(n_rows, n_heads, n_kv_heads);
+    if (st != DSPARK_OK) return st;
+    if (max_rows < 1 || !scale_ok(scale)) return DSPARK_ERR_ARG;
+    if (n_rows == 0) return DSPARK_OK;
+    if (!q || !cache_len || !page_table || !out || !aligned16(q) || !aligned16(out)) return DSPARK_ERR_ARG;
+    if (!row_stride_ok(q_stride, n_heads, head_dim)) return DSPARK_ERR_ARG;
+    st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
+    if (st != DSPARK_OK) return st;
+    const PagedPlan plan = paged_plan(max_rows, n_heads, n_kv_heads, head_dim, (long long)max_pages * page_size);
+    size_t need = 0;
+    paged_carve(nullptr, plan, head_dim, &need);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
+    const PagedWork w = paged_carve(workspace, plan, head_dim, nullptr);
+    PagedArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.dtype = dtype;
+    a.row_offsets = row_offsets;
+    a.start = cache_len;
+    a.page_table = page_table;
+    a.B = B;
+    a.n_rows = n_rows;
+    a.max_pages = max_pages;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype;
+    a.n_pages = n_pages;
+    a.page_size = page_size;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.out = out;
+    a.lse = lse_out;
+    return launch_paged(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
+size_t dspark_prompt_attention_workspace_size(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads,
+                                              int head_dim) {
+    if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || n_kv_rows < 0 ||
+        n_kv_rows > DSPARK_MAX_ROWS || head_geometry(n_rows, n_heads, n_kv_heads) != DSPARK_OK ||
+        !head_dim_supported(head_dim))
+        return 0;
+    size_t bytes = 0;
+    prompt_carve(nullptr, prompt_plan(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim), n_rows, n_heads, head_dim,
+                 &bytes);
+    return bytes;
+}
+
+int dspark_prompt_attention(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int dtype, const int32_t *row_offsets, int n_rows,
+                            const int32_t *kv_offsets, int n_kv_rows, int B, int n_heads, int n_kv_heads, int head_dim,
+                            float scale, int causal, void *out, float *lse_out, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || n_kv_rows < 0 ||
+        n_kv_rows > DSPARK_MAX_ROWS || !row_offsets || (!kv_offsets && n_kv_rows != n_rows) || head_dim < 1)
+        return DSPARK_ERR_ARG;
+    const int st = head_geometry(n_rows, n_heads, n_kv_heads);
+    if (st != DSPARK_OK) return st;
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F16 && dtype != DSPARK_F32 && dtype != DSPARK_E4M3)
+        return DSPARK_ERR_ARG;
+    if ((dtype != DSPARK_BF16 && dtype != DSPARK_F16) || !head_dim_supported(head_dim)) return DSPARK_ERR_UNSUPPORTED;
+    if (!scale_ok(scale)) return DSPARK_ERR_ARG;
+    if (n_rows == 0) return DSPARK_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out) || !row_stride_ok(q_stride, n_heads, head_dim))
+        return DSPARK_ERR_ARG;
+    if (n_kv_rows > 0 && (!k || !v || !aligned16(k) || !aligned16(v) || !row_stride_ok(k_stride, n_kv_heads, head_dim) ||
+                          !row_stride_ok(v_stride, n_kv_heads, head_dim)))
+        return DSPARK_ERR_ARG;
+    const PromptPlan plan = prompt_plan(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim);
+    size_t need = 0;
+    prompt_carve(nullptr, plan, n_rows, n_heads, head_dim, &need);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
+    const PromptWork w = prompt_carve(workspace, plan, n_rows, n_heads, head_dim, nullptr);
+    PromptArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.dtype = dtype;
+    a.q_offsets = row_offsets;
+    a.kv_offsets = kv_offsets;
+    a.B = B;
+    a.n_rows = n_rows;
+    a.n_kv_rows = n_kv_rows;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.out = out;
+    a.lse = lse_out;
+    return launch_prompt(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
+}  // extern "C"

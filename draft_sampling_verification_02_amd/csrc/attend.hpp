@@ -1,0 +1,170 @@
+// attend.hpp -- building blocks of the attention kernels (paged.hip,
+// prompt.hip): element types, matrix products, transposed LDS reads, direct
+// loads into LDS and the cross-lane maximum and sum of a softmax.
+//
+// Both kernels compute the scores transposed, S^T = K Q^T: the A operand is a
+// block of cache rows (tokens), the B operand the queries, so that a lane owns
+// one query (the accumulator column) and its registers run over tokens.  The
+// exponentials of those registers are then already the B operand of
+// O^T = V^T P^T -- the order of the contraction index is free, so the tokens a
+// lane happens to hold define it -- and the probabilities never leave the
+// registers.  V^T comes from the row-major V tile by transposing LDS reads.
+#pragma once
+
+#include "device_common.hpp"
+
+namespace dspark {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
+
+// Element types of rows and caches: storage is 16 bits, E names the value type.
+struct TypeBf16 {
+    using E = __bf16;
+    using V8 = bf16x8_t;
+};
+struct TypeF16 {
+    using E = _Float16;
+    using V8 = f16x8_t;
+};
+
+__device__ __forceinline__ f32x4_t mma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mma16(f16x8_t a, f16x8_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma32(bf16x8_t a, bf16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mma32(f16x8_t a, f16x8_t b, f32x16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- LDS access
+template <typename T>
+__device__ __forceinline__ T lds_read(uint32_t at) {
+    return *reinterpret_cast<__attribute__((address_space(3))) const T *>(at);
+}
+template <typename T>
+__device__ __forceinline__ void lds_write(uint32_t at, T v) {
+    *reinterpret_cast<__attribute__((address_space(3))) T *>(at) = v;
+}
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void *)p));
+}
+// Transposing reads.  Each group of 16 lanes reads a small matrix and every
+// lane gets one of its 16 columns.  tr16: 4 rows of 16 16-bit values, lane
+// 4 i + c addressing row i, columns 4 c .. 4 c + 3 (8 bytes).  tr8: 8 rows of
+// 16 bytes, lane 2 j + c addressing row j, bytes 8 c .. 8 c + 7.
+__device__ __forceinline__ s16x4_t lds_read_tr16(uint32_t at) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4_t *>(at));
+}
+__device__ __forceinline__ u32x2_t lds_read_tr8(uint32_t at) {
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                           reinterpret_cast<__attribute__((address_space(3))) i32x2_t *>(at)));
+}
+template <typename V8>
+__device__ __forceinline__ V8 join4(s16x4_t a, s16x4_t b) {
+    return __builtin_bit_cast(V8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// Direct global-to-LDS loads, lane i writing 16 (or 4) bytes at lds + 16 i
+// (4 i) from base + voff.  They go through asm because the compiler, told of
+// such a load, makes every later LDS read wait for all of them; here the
+// kernels wait themselves, by count (vm_wait).  The asm has no register
+// outputs.  Extra loads in flight only make the compiler's own counted waits
+// stricter.  M0, the LDS base, is written right before each load; nothing else
+// in these kernels uses it.  lds and base are uniform.
+__device__ __forceinline__ void dma16(uint32_t lds, uint32_t voff, const void *base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(voff), "s"(base)
+                 : "memory");
+}
+// the same with an address a lane
+__device__ __forceinline__ void dma16(uint32_t lds, const void *lane_src) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(lane_src) : "memory");
+}
+__device__ __forceinline__ void dma4(uint32_t lds, const void *lane_src) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(lane_src) : "memory");
+}
+// Waits until at most N of this wave's vector memory operations are in flight.
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+    static_assert(N >= 0 && N < 64, "vmcnt is a 6-bit count");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// Every LDS read of this wave has returned: its buffers may be refilled.
+__device__ __forceinline__ void lds_drain() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
+
+// Workgroup barrier that leaves the direct loads in flight: this wave's LDS
+// accesses are done, and none moves across it.
+__device__ __forceinline__ void wg_barrier() {
+    lds_drain();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(u));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(uint32_t(u >> 32));
+    return reinterpret_cast<const uint8_t *>(uint64_t(hi) << 32 | lo);
+}
+
+// ---------------------------------------------------------------- cross-lane
+// Over lanes l and l ^ 32, and l ^ 16: a swap of register halves leaves the
+// two partners' values in the two results.
+__device__ __forceinline__ float max_x32(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_x32(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max_x16(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_x16(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------- e4m3
+// Eight e4m3 values (two words) as 16-bit floats; every e4m3 value is exact in
+// both types.
+__device__ __forceinline__ void e4m3_to8(u32x2_t w, bf16x8_t &o) {
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], 1.f, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], 1.f, true);
+    const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], 1.f, false);
+    const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], 1.f, true);
+    o = bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ void e4m3_to8(u32x2_t w, f16x8_t &o) {
+    const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[0], 1.f, false);
+    const f16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[0], 1.f, true);
+    const f16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[1], 1.f, false);
+    const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[1], 1.f, true);
+    o = f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// 2^(byte - 127), the power-of-two scale of one (token, head)
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+
+// The natural logsumexp from the running maximum (base-2 units) and sum.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.f ? kNegInf : (m + fast_log2(l)) * kLn2;
+}
+
+}  // namespace dspark

@@ -248,6 +248,76 @@ struct StsArgs {
 };
 hipError_t launch_sts(const StsArgs &a, const StsPlan &p, const StsWork &w, hipStream_t s);
 
+// ---- paged key-value cache and attention --------------------------------
+
+// One cache call: rows [n_rows, Hkv, D] against the slots of a paged cache.
+struct CacheArgs {
+    const void *k, *v;  // write: the rows, row strides in elements
+    long long k_stride, v_stride;
+    void *k_out, *v_out;  // read: the rows, densely packed
+    int dtype;            // of the rows
+    const int32_t *row_offsets;  // [B + 1], or nullptr: one row a request
+    const int32_t *start;        // [B] position of each request's first row, or nullptr (0)
+    const int32_t *page_table;   // [B, max_pages]
+    int B, n_rows, max_pages, n_kv_heads, head_dim;
+    void *k_cache, *v_cache;
+    uint8_t *k_scale, *v_scale;
+    int cache_dtype, n_pages, page_size;
+};
+hipError_t launch_cache(const CacheArgs &a, bool write, hipStream_t s);
+
+// The split of a paged attention call.
+struct PagedPlan {
+    int qblocks;   // 16-query blocks a workgroup holds
+    int grid;      // workgroups
+    int whole;     // 1: a workgroup takes whole (request, head, query group) segments, nothing to join
+};
+// table_tokens: max_pages * page_size, the longest a request can be
+PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, long long table_tokens);
+struct PagedWork {
+    int4 *meta;       // [grid] the segment a workgroup left unfinished at its end
+    float *ml;        // [2 grid, 2, queries] partial maxima and sums
+    float *o;         // [2 grid, queries, D] partial products
+};
+PagedWork paged_carve(void *ws, const PagedPlan &p, int head_dim, size_t *bytes);
+
+struct PagedArgs {
+    const void *q;
+    long long q_stride;
+    int dtype;
+    const int32_t *row_offsets, *start, *page_table;
+    int B, n_rows, max_pages, n_heads, n_kv_heads, head_dim;
+    const void *k_cache, *v_cache;
+    const uint8_t *k_scale, *v_scale;
+    int cache_dtype, n_pages, page_size;
+    float scale;
+    int causal;
+    void *out;
+    float *lse;
+};
+hipError_t launch_paged(const PagedArgs &a, const PagedPlan &p, const PagedWork &w, hipStream_t s);
+
+struct PromptArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    int dtype;
+    const int32_t *q_offsets, *kv_offsets;
+    int B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim;
+    float scale;
+    int causal;
+    void *out;
+    float *lse;
+};
+struct PromptPlan {
+    int waves;  // of a workgroup; each holds 32 queries
+};
+PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim);
+struct PromptWork {
+    float *ml, *o;  // unused while nothing is split
+};
+PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_rows, int n_heads, int head_dim, size_t *bytes);
+hipError_t launch_prompt(const PromptArgs &a, const PromptPlan &p, const PromptWork &w, hipStream_t s);
+
 // ---- diagnostics -----------------------------------------------------
 
 hipError_t launch_debug_words(uint32_t key0, uint32_t key1, uint32_t round32, int stream_id, int k,

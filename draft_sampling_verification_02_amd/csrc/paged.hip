@@ -1,0 +1,688 @@
+// paged.hip -- attention of a few new rows a request over a paged key-value
+// cache (the target forward of a verify step, a decoding step, the parallel
+// stage of a draft).
+//
+// For row i of request b (position start_b + i) and head h:
+//   s_t = scale q . k_t over the visible tokens t (t <= start_b + i if causal,
+//   every token of the request otherwise),
+//   out = sum_t exp(s_t - lse) v_t,  lse = log sum_t exp(s_t).
+// One pass over the cache carries the running maximum and sum; everything is
+// accumulated in 32 bits, and the probabilities are rounded to 16 bits (2^-9
+// relative for bfloat16) only as they enter the V product.
+//
+// What bounds it: the cache is read once, 4 D bytes (2 D + 2 in 8 bits) a
+// token and head against 4 D G flops for G queries -- memory, for any group a
+// request of a round has.  So the kernel is built to keep loads in flight: a
+// workgroup of four independent waves, each streaming its own tiles of 32
+// tokens through a ring of LDS buffers with direct loads (no registers held,
+// no barriers), K refilled as soon as its scores are taken, V as soon as its
+// product is.  G query heads times the request's rows share every tile.
+//
+// Work is the concatenation of all (request, head, query group) segments, cut
+// into units of 128 tokens and dealt to the workgroups in equal contiguous
+// ranges, whatever the requests' lengths (each workgroup finds its range from
+// the lengths on the device, so a captured call follows them).  A range may
+// start or end inside a segment: it then leaves a partial result (maximum, sum,
+// unnormalised product), and paged_join merges a segment's partials in their
+// order, so results do not depend on timing.
+#include "attend.hpp"
+#include "dspark.h"
+#include "internal.hpp"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kPagedWaves = 4;
+constexpr int kPagedThreads = 64 * kPagedWaves;
+constexpr int kTokens = 32;                          // tokens of a wave's tile
+constexpr int kUnit = kTokens * kPagedWaves;         // tokens of a work unit
+constexpr int kMinUnits = 2;                         // units a workgroup takes at least
+constexpr int kPagedGrid = 512;                      // two workgroups a compute unit
+constexpr int kWholeTokens = 512;                    // tables up to this long are not split
+
+typedef __attribute__((address_space(4))) const int32_t *ConstInts;  // read by scalar loads
+
+struct PagedParams {
+    PagedArgs a;
+    PagedWork w;
+    int G, pshift, whole;
+    float c;  // scale * log2(e)
+};
+
+struct Request {
+    int row0, rows;  // its rows of q
+    int past;        // position of the first one
+    int L;           // tokens present (0: the request takes no part)
+    int groups;      // query groups
+    int T;           // units of one segment
+};
+
+template <int QB>
+__device__ __forceinline__ Request request_of(const PagedParams &p, int b) {
+    Request r;
+    const PagedArgs &a = p.a;
+    int r0 = b, r1 = b + 1;
+    if (a.row_offsets) {
+        r0 = min(max(a.row_offsets[b], 0), a.n_rows);
+        r1 = min(max(a.row_offsets[b + 1], 0), a.n_rows);
+    }
+    r.row0 = r0;
+    r.rows = max(r1 - r0, 0);
+    r.past = min(a.start[b], 1 << 30);  // tables end at 2^30 tokens: no sum below overflows
+    const long long cap = (long long)a.max_pages << p.pshift;
+    r.L = r.past < 0 ? 0 : int(min((long long)r.past + r.rows, cap));
+    r.groups = (r.rows * p.G + QB - 1) / QB;
+    r.T = p.whole ? 1 : max(1, (r.L + kUnit - 1) / kUnit);
+    return r;
+}
+__device__ __forceinline__ long long cost_of(const PagedParams &p, const Request &r) {
+    return (long long)r.groups * p.a.n_kv_heads * r.T;
+}
+
+// Layout of a wave's LDS tiles: rows of RB bytes in CPR chunks of 16, chunk c
+// of row r at c ^ k_swizzle(r) (K) or c ^ v_swizzle(r) (V).  K is read 16 rows
+// at one chunk, V transposed 4 rows (16-bit) or 8 rows (8-bit) of each of two
+// lane groups at one 32- or 16-byte column: the swizzles put those in distinct
+// banks.
+template <bool E4, int D>
+struct TileShape {
+    static constexpr int RB = E4 ? D : 2 * D;
+    static constexpr int CPR = RB / 16;
+    static constexpr int BYTES = kTokens * RB;
+    static constexpr int NI = BYTES / 1024;       // load instructions of a tile
+    static constexpr int RPI = 1024 / RB;         // rows one of them covers (at most 16)
+    static constexpr int PER = RB >= 256 ? 1 : 256 / RB;  // rows that span all banks
+    static constexpr int SW = CPR < 16 ? CPR : 16;
+    __device__ static __forceinline__ int k_swizzle(int r) { return (r / PER) & (SW - 1); }
+    __device__ static __forceinline__ int v_swizzle(int r) {
+        if constexpr (E4) {
+            // rows 4 g .. 4 g + 3 and 16 + 4 g .. of two neighbouring g: bits 0-2 and 4
+            constexpr int low = 8 / PER;  // distinct values of the low bits after PER rows share a line
+            return ((r & 7) / PER) | (((r >> 4) & 1) * low);
+        } else {
+            return (((r & 7) / PER) * 2) & (SW - 1);
+        }
+    }
+};
+
+template <typename T, bool E4>
+struct ProbType {
+    using type = T;
+};
+template <typename T>
+struct ProbType<T, true> {
+    // 8-bit caches: the V scales multiply the probabilities, whose range then
+    // needs bfloat16's exponent
+    using type = TypeBf16;
+};
+
+template <typename T, bool E4, int D, int NQ>
+struct PagedShape {
+    using S = TileShape<E4, D>;
+    static constexpr int QB = 16 * NQ;
+    static constexpr int NS = S::RB >= 512 ? 1 : 2;                 // tiles in the ring
+    static constexpr int SCALE = E4 ? 256 : 0;                      // a tile's scales
+    static constexpr int STAGE = 2 * S::BYTES + SCALE;
+    static constexpr int RING = NS * STAGE;                         // bytes of a wave
+    static constexpr int OROW = D + 4;                              // padded floats of a joined row
+    static constexpr int JOIN = kPagedWaves * QB * (OROW + 2) * 4;  // the waves' results
+    static constexpr int QBYTES = QB * D * 2;
+    static constexpr int BODY = RING * kPagedWaves > JOIN ? RING * kPagedWaves : JOIN;
+    static constexpr int LDS = BODY + QBYTES;
+    static constexpr int KL = S::NI + (E4 ? 1 : 0);  // loads of a tile's K (and scales)
+    static constexpr int VL = S::NI;
+    static constexpr int FLY = (NS - 1) * (KL + VL) + VL;  // loads younger than a tile's K when it is taken
+    static constexpr int FLYV = (NS - 1) * (KL + VL) + KL; // and than its V, K being refilled
+    static constexpr int PER_CU = LDS <= 80 * 1024 ? 2 : 1;
+    static_assert(LDS <= 160 * 1024, "LDS of a workgroup");
+};
+
+// Four channels of one output row, normalised: out = o / l (0 where nothing is
+// visible), lse from the maximum and sum.
+template <typename T>
+__device__ __forceinline__ void store_row(const PagedParams &p, int row, int head, int c4, int D, f32x4_t o, float m,
+                                          float l) {
+    using E = typename T::E;
+    typedef E e4_t __attribute__((ext_vector_type(4)));
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at = (long long)row * p.a.n_heads + head;
+    const e4_t x = l == 0.f ? e4_t{} : e4_t{E(o[0] * inv), E(o[1] * inv), E(o[2] * inv), E(o[3] * inv)};
+    *reinterpret_cast<e4_t *>(static_cast<E *>(p.a.out) + at * D + 4 * c4) = x;
+    if (p.a.lse && c4 == 0) p.a.lse[at] = lse_of(m, l);
+}
+
+template <typename T, bool E4, int D, int NQ>
+__global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) void paged_kernel(PagedParams p) {
+    using SH = PagedShape<T, E4, D, NQ>;
+    using S = TileShape<E4, D>;
+    using V8 = typename T::V8;
+    using PT = typename ProbType<T, E4>::type;
+    using P8 = typename PT::V8;
+    using QS = TileShape<false, D>;  // query rows in LDS are laid out as 16-bit K rows
+    constexpr int QB = SH::QB, NS = SH::NS, KS = D / 32, CB = D / 16;
+    constexpr int KSTEP = S::RB / 64;  // 16-byte chunks of a K row a lane reads
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
+    __shared__ long long scan[kPagedWaves];
+    __shared__ long long found[2];
+    __shared__ int found_b;
+
+    const PagedArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const uint32_t lds0 = lds_addr(lds);
+    const uint32_t ring = lds0 + wave * SH::RING;
+    const uint32_t qlds = lds0 + SH::BODY;
+
+    // ---- this workgroup's range of units --------------------------------
+    long long total = 0;
+    long long mine = 0;  // with B <= kPagedThreads: the cost of request tid
+    for (int b = tid; b < a.B; b += kPagedThreads) {
+        mine = cost_of(p, request_of<QB>(p, b));
+        total += mine;
+    }
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) total += __shfl_xor(total, s);
+    if (lane == 0) scan[wave] = total;
+    __syncthreads();
+    total = scan[0] + scan[1] + scan[2] + scan[3];
+    const long long min_units = p.whole ? 1 : kMinUnits;
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, min_units);
+    const long long begin = (long long)blockIdx.x * per;
+    const long long end = min(begin + per, total);
+    if (tid == 0 && !p.whole) p.w.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (begin >= end) return;
+    // the request `begin` falls in
+    {
+        long long before = 0;  // cost of the requests before this chunk
+        for (int b0 = 0; b0 < a.B; b0 += kPagedThreads) {
+            const int b = b0 + tid;
+            const long long cost = a.B <= kPagedThreads ? mine : (b < a.B ? cost_of(p, request_of<QB>(p, b)) : 0);
+            long long inc = cost;
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1) {
+                const long long up = __shfl_up(inc, s);
+                if (lane >= s) inc += up;
+            }
+            __syncthreads();
+            if (lane == 63) scan[wave] = inc;
+            __syncthreads();
+            for (int w = 0; w < wave; ++w) inc += scan[w];
+            const long long chunk = scan[0] + scan[1] + scan[2] + scan[3];
+            inc += before;
+            if (b < a.B && begin < inc && begin >= inc - cost) {
+                found_b = b;
+                found[0] = inc - cost;
+            }
+            before += chunk;
+            if (begin < before) break;
+        }
+        __syncthreads();
+    }
+    int b = uniform(found_b);
+    Request rq = request_of<QB>(p, b);
+    long long at = begin;
+    const long long rest = begin - found[0];  // units into the request
+    int seg = uniform(int(rest / rq.T));      // (head, group) segment of the request
+    int u0 = uniform(int(rest - (long long)seg * rq.T));
+
+    // fixed parts of the load and read addresses
+    uint32_t kvoff[S::NI], vvoff[S::NI];
+#pragma unroll
+    for (int j = 0; j < S::NI; ++j) {
+        const int slot = j * 64 + lane, row = slot / S::CPR, c = slot % S::CPR;
+        const int rin = row - j * S::RPI;  // row of the instruction
+        kvoff[j] = rin * S::RB + ((c ^ S::k_swizzle(row)) * 16);
+        vvoff[j] = rin * S::RB + ((c ^ S::v_swizzle(row)) * 16);
+    }
+
+    // where the wave's lanes read a tile
+    uint32_t kread[KSTEP], vread[2];
+#pragma unroll
+    for (int k = 0; k < KSTEP; ++k) kread[k] = n * S::RB + (((4 * k + g) ^ S::k_swizzle(n)) * 16);
+    // transposing reads: 16-bit, row 4 g + i of a half; 8-bit, rows 4 g + i of both halves
+    const int vrow = E4 ? ((lane >> 1) & 3) + 4 * g + ((lane & 8) ? 16 : 0) : 4 * g + ((lane >> 2) & 3);
+    vread[0] = vrow * S::RB;
+    vread[1] = (vrow + 16) * S::RB;
+    auto v_frag = [&](uint32_t buf, int cb) __device__ {
+        if constexpr (E4) {
+            P8 f;
+            e4m3_to8(lds_read_tr8(buf + vread[0] + ((cb ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1)), f);
+            return f;
+        } else {
+            const uint32_t c = uint32_t(((2 * cb + ((lane >> 1) & 1)) ^ S::v_swizzle(vrow)) * 16 + 8 * (lane & 1));
+            return join4<P8>(lds_read_tr16(buf + vread[0] + c), lds_read_tr16(buf + vread[1] + c));
+        }
+    };
+
+    while (at < end) {
+        // ---- one segment: query group grp of head h of request b ---------
+        const int h = uniform(seg / rq.groups), grp = uniform(seg - h * rq.groups);
+        const int u1 = uniform(int(min((long long)rq.T, u0 + (end - at))));
+        const int tok0 = p.whole ? 0 : u0 * kUnit;
+        const int tok1 = p.whole ? rq.L : min(u1 * kUnit, rq.L);
+        const int nq_all = rq.rows * p.G;  // queries of the request
+        // this wave's tiles: tok0 + (wave + 4 i) * kTokens
+        const int ntile = (max(tok1 - tok0, 0) + kTokens - 1) / kTokens;
+        const int tiles = uniform(ntile > wave ? (ntile - wave + kPagedWaves - 1) / kPagedWaves : 0);
+        const ConstInts table = (ConstInts)(a.page_table + (long long)b * a.max_pages);
+        const int pmask = (1 << p.pshift) - 1;
+
+        auto tile_at = [&](int i) __device__ { return tok0 + (wave + i * kPagedWaves) * kTokens; };
+        // the page of token t (the last page of the table for tokens past it: they are masked)
+        auto page_of = [&](int t) __device__ { return table[min(t >> p.pshift, a.max_pages - 1)]; };
+        auto bad_page = [&](int page) __device__ { return page < 0 || page >= a.n_pages; };
+        // row of the cache where tokens t .. t + 15 start; a page outside the cache reads page 0 and is masked
+        auto row_of = [&](int page, int t) __device__ {
+            return (((long long)(bad_page(page) ? 0 : page) * a.n_kv_heads + h) << p.pshift) + (t & pmask);
+        };
+        auto issue = [&](const void *cache, const uint32_t *off, uint32_t dst, int t, int pa, int pb) __device__ {
+            const uint8_t *ba = static_cast<const uint8_t *>(cache) + row_of(pa, t) * S::RB;
+            const uint8_t *bb = static_cast<const uint8_t *>(cache) + row_of(pb, t + 16) * S::RB;
+#pragma unroll
+            for (int j = 0; j < S::NI; ++j) {
+                const int row = j * S::RPI;  // first row of the load; a load stays in one half, so in one page
+                dma16(dst + j * 1024, off[j], uniform((row < 16 ? ba : bb) + (row & 15) * S::RB));
+            }
+        };
+        auto issue_k = [&](int i, int pa, int pb) __device__ {
+            const int t = tile_at(i);
+            const uint32_t dst = uniform(ring + (i % NS) * SH::STAGE);
+            issue(a.k_cache, kvoff, dst, t, pa, pb);
+            if constexpr (E4) {
+                // bytes 0-31: K scales of the tokens, 32-63: V scales (lane i brings 4 bytes; lanes past 15 repeat)
+                const uint8_t *sc = (lane & 8) ? a.v_scale : a.k_scale;
+                dma4(uniform(dst + 2 * S::BYTES), sc + ((lane & 4) ? row_of(pb, t + 16) : row_of(pa, t)) + 4 * (lane & 3));
+            }
+        };
+        auto issue_v = [&](int i, int pa, int pb) __device__ {
+            issue(a.v_cache, vvoff, uniform(ring + (i % NS) * SH::STAGE + S::BYTES), tile_at(i), pa, pb);
+        };
+
+        // ---- queries into LDS (the workgroup's waves share them), first tiles
+        constexpr int QCH = D / 8;  // 16-byte chunks of a query row
+        for (int j = wave; j < SH::QBYTES / 1024; j += kPagedWaves) {
+            const int slot = j * 64 + lane, row = slot / QCH;
+            const int qi = min(grp * QB + row, nq_all - 1);
+            const int i = qi / p.G;
+            const long long src = (rq.row0 + i) * a.q_stride + (long long)(h * p.G + (qi - i * p.G)) * D +
+                                  (((slot % QCH) ^ QS::k_swizzle(row & 15)) * 8);
+            dma16(uniform(qlds + j * 1024), static_cast<const uint8_t *>(a.q) + 2 * src);
+        }
+        int bad = 0;  // two bits a ring slot: the tile's halves lie on pages outside the cache
+        for (int i = 0; i < NS; ++i)
+            if (i < tiles) {
+                const int pa = page_of(tile_at(i)), pb = page_of(tile_at(i) + 16);
+                issue_k(i, pa, pb);
+                issue_v(i, pa, pb);
+                bad |= (int(bad_page(pa)) | int(bad_page(pb)) << 1) << (2 * i);
+            }
+        int na = 0, nb = 0;  // pages of the next tile to issue
+        if (NS < tiles) {
+            na = page_of(tile_at(NS));
+            nb = page_of(tile_at(NS) + 16);
+        }
+        if (tiles >= NS)
+            vm_wait<NS *(SH::KL + SH::VL)>();
+        else
+            vm_wait<0>();
+        wg_barrier();
+        V8 qf[NQ][KS];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                // the 8 channels lane group g takes at step k (an 8-bit K chunk holds two steps')
+                const int ch = E4 ? 2 * (4 * (k / 2) + g) + (k & 1) : 4 * k + g;
+                qf[q][k] = __builtin_bit_cast(
+                    V8, lds_read<u32x4v_t>(qlds + (16 * q + n) * D * 2 + ((ch ^ QS::k_swizzle(n)) * 16)));
+            }
+        int lim[NQ];  // tokens visible to the lane's query
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            const int qi = grp * QB + 16 * q + n;
+            lim[q] = qi >= nq_all ? 0 : (a.causal ? min(rq.L, rq.past + qi / p.G + 1) : rq.L);
+        }
+        const int lim_min = uniform(a.causal ? min(rq.L, rq.past + (grp * QB) / p.G + 1) : rq.L);
+
+        float m[NQ], l[NQ];
+        f32x4_t o[NQ][CB];
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            m[q] = kNegInf;
+            l[q] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CB; ++c) o[q][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+
+        for (int i = 0; i < tiles; ++i) {
+            const uint32_t buf = ring + (i % NS) * SH::STAGE;
+            const int t = tile_at(i);
+            const int bad_now = (bad >> (2 * (i % NS))) & 3;
+            const bool more = i + NS < tiles;
+            const int pa = na, pb = nb;
+            if (i + NS + 1 < tiles) {
+                na = page_of(tile_at(i + NS + 1));
+                nb = page_of(tile_at(i + NS + 1) + 16);
+            }
+            // ---- scores: s[q][half][r] is token 16 half + 4 g + r, query n
+            if (i + NS - 1 < tiles)
+                vm_wait<SH::FLY>();
+            else
+                vm_wait<0>();
+            f32x4_t s[NQ][2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) s[q][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < KSTEP; ++k) {
+                    const u32x4v_t x = lds_read<u32x4v_t>(buf + 16 * hf * S::RB + kread[k]);
+                    if constexpr (E4) {
+                        V8 lo, hi;
+                        e4m3_to8(u32x2_t{x[0], x[1]}, lo);
+                        e4m3_to8(u32x2_t{x[2], x[3]}, hi);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(lo, qf[q][2 * k], s[q][hf]);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(hi, qf[q][2 * k + 1], s[q][hf]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q)
+                            s[q][hf] = mma16(__builtin_bit_cast(V8, x), qf[q][k], s[q][hf]);
+                    }
+                }
+            }
+            float vs[2][4];
+            if constexpr (E4) {
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint32_t kw = lds_read<uint32_t>(buf + 2 * S::BYTES + 16 * hf + 4 * g);
+                    const uint32_t vw = lds_read<uint32_t>(buf + 2 * S::BYTES + 32 + 16 * hf + 4 * g);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float ks = scale_of((kw >> (8 * r)) & 255);
+                        vs[hf][r] = scale_of((vw >> (8 * r)) & 255);
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) s[q][hf][r] *= ks;
+                    }
+                }
+            }
+            lds_drain();
+            if (more) issue_k(i + NS, pa, pb);
+            bad &= ~(3 << (2 * (i % NS)));
+            if (more) bad |= (int(bad_page(pa)) | int(bad_page(pb)) << 1) << (2 * (i % NS));
+
+            // ---- running maximum, probabilities
+            const bool masked = t + kTokens > lim_min || bad_now != 0;
+            P8 pf[NQ];
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                if (masked) {
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (t + 16 * hf + 4 * g + r >= lim[q] || ((bad_now >> hf) & 1)) s[q][hf][r] = kNegInf;
+                }
+                float mx = fmaxf(fmaxf(fmaxf(s[q][0][0], s[q][0][1]), fmaxf(s[q][0][2], s[q][0][3])),
+                                 fmaxf(fmaxf(s[q][1][0], s[q][1][1]), fmaxf(s[q][1][2], s[q][1][3])));
+                mx = max_x16(max_x32(mx)) * p.c;
+                const float mn = fmaxf(m[q], mx);
+                if (__any(mn > m[q])) {
+                    const float al = fast_exp2(m[q] - (mn == kNegInf ? 0.f : mn));
+                    l[q] *= al;
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) o[q][c] *= al;
+                    m[q] = mn;
+                }
+                const float ms = mn == kNegInf ? 0.f : mn;
+                float pr[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pr[e] = fast_exp2(__builtin_fmaf(s[q][e >> 2][e & 3], p.c, -ms));
+                l[q] += ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
+                if constexpr (E4) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // a masked token's scale may be anything: its product stays zero
+                        const float x = pr[e] * vs[e >> 2][e & 3];
+                        pr[e] = masked && s[q][e >> 2][e & 3] == kNegInf ? 0.f : x;
+                    }
+                }
+                using E = typename PT::E;
+                pf[q] = P8{E(pr[0]), E(pr[1]), E(pr[2]), E(pr[3]), E(pr[4]), E(pr[5]), E(pr[6]), E(pr[7])};
+            }
+
+            // ---- products with V
+            if (more)
+                vm_wait<SH::FLYV>();
+            else if (i + NS - 1 < tiles)
+                vm_wait<(NS - 1) * (SH::KL + SH::VL)>();
+            else
+                vm_wait<0>();
+            const uint32_t vbuf = buf + S::BYTES;
+            bool slow = false;
+            if (masked) {
+                // rows that no query sees (past the request's end, pages outside the cache) may hold anything
+                for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
+                    const int row = slot / S::CPR;
+                    if (t + row >= rq.L || ((bad_now >> (row >> 4)) & 1)) lds_write(vbuf + slot * 16, u32x4v_t{0, 0, 0, 0});
+                }
+                lds_drain();
+                // a row that some queries see and others must not: harmless where it is finite, as the others'
+                // probabilities are zero; 0 * v tells
+                if (t + kTokens > lim_min && lim_min < rq.L) {
+                    const P8 zero = {};
+                    f32x4_t z = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbuf, c), zero, z);
+                    slow = __any(!(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f));
+                }
+            }
+            if (!slow) {
+#pragma unroll
+                for (int c = 0; c < CB; ++c) {
+                    const P8 vf = v_frag(vbuf, c);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) o[q][c] = mma16(vf, pf[q], o[q][c]);
+                }
+            } else {
+                // infinities or NaN in such a row: a token at a time, kept only by the queries that see it
+#pragma unroll 1
+                for (int k = 0; k < kTokens; ++k) {
+                    const int e = (k & 3) + 4 * (k >> 4), tok = t + k;  // token k is element e of lane group (k / 4) % 4
+                    const uint32_t keep = g == ((k >> 2) & 3) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
+                    asm volatile("" : : : "memory");  // the fragments are read again: no registers held for them
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) {
+                        u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, c));
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            const f32x4_t with = mma16(__builtin_bit_cast(P8, one), pf[q], o[q][c]);
+                            if (tok < lim[q]) o[q][c] = with;
+                        }
+                    }
+                }
+            }
+            lds_drain();
+            if (more) issue_v(i + NS, pa, pb);
+        }
+
+        // ---- the waves' results through LDS ------------------------------
+        wg_barrier();
+        const uint32_t jml = lds0 + kPagedWaves * QB * SH::OROW * 4;  // [wave][QB][2]: maximum, sum
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            l[q] = sum_x16(sum_x32(l[q]));
+            const int row = wave * QB + 16 * q + n;
+            if (g == 0) lds_write(jml + row * 8, u32x2_t{__float_as_uint(m[q]), __float_as_uint(l[q])});
+#pragma unroll
+            for (int c = 0; c < CB; ++c) lds_write(lds0 + (row * SH::OROW + 16 * c + 4 * g) * 4, o[q][c]);
+        }
+        wg_barrier();
+        const bool starts = u0 == 0, ends = u1 == rq.T;
+        const long long slot = 2LL * blockIdx.x + (starts ? 1 : 0);
+        for (int e = tid; e < QB * (D / 4); e += kPagedThreads) {
+            const int q = e / (D / 4), c4 = e % (D / 4);
+            const int qi = grp * QB + q;
+            float mw[kPagedWaves], lw[kPagedWaves], mm = kNegInf, ll = 0.f;
+#pragma unroll
+            for (int w = 0; w < kPagedWaves; ++w) {
+                const u32x2_t x = lds_read<u32x2_t>(jml + (w * QB + q) * 8);
+                mw[w] = __uint_as_float(x[0]);
+                lw[w] = __uint_as_float(x[1]);
+                mm = fmaxf(mm, mw[w]);
+            }
+            f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            const float ms = mm == kNegInf ? 0.f : mm;
+#pragma unroll
+            for (int w = 0; w < kPagedWaves; ++w) {
+                const float f = fast_exp2(mw[w] - ms);
+                ll += lw[w] * f;
+                acc += lds_read<f32x4_t>(lds0 + ((w * QB + q) * SH::OROW + 4 * c4) * 4) * f;
+            }
+            if (starts && ends) {
+                if (qi < nq_all) store_row<T>(p, rq.row0 + qi / p.G, h * p.G + qi % p.G, c4, D, acc, mm, ll);
+            } else {
+                *reinterpret_cast<f32x4_t *>(p.w.o + (slot * QB + q) * D + 4 * c4) = acc;
+                if (c4 == 0) {
+                    p.w.ml[slot * 2 * QB + q] = mm;
+                    p.w.ml[slot * 2 * QB + QB + q] = ll;
+                }
+            }
+        }
+        if (starts && !ends && tid == 0)
+            p.w.meta[blockIdx.x] = make_int4(int((rq.T - u1 + per - 1) / per), b, h, grp);
+        wg_barrier();
+
+        at += u1 - u0;
+        u0 = 0;
+        if (++seg >= rq.groups * a.n_kv_heads && at < end) {
+            seg = 0;
+            do rq = request_of<QB>(p, ++b);
+            while (rq.groups == 0 && b + 1 < a.B);
+        }
+    }
+}
+
+// The segments that workgroups left unfinished: workgroup (i, q) merges query
+// q of the segment workgroup i started and its successors went on with, in
+// their order.  Its threads take the partials in turn, D / 4 threads each.
+template <typename T, int D, int QB>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p) {
+    constexpr int TPP = D / 4, LANES = 256 / TPP;  // partials in flight
+    __shared__ float red[LANES][D + 2];
+    const int4 seg = p.w.meta[blockIdx.x];
+    if (seg.x == 0) return;
+    const Request rq = request_of<QB>(p, seg.y);
+    const int q = blockIdx.y, qi = seg.w * QB + q;
+    if (qi >= rq.rows * p.G) return;
+    const int grp = threadIdx.x / TPP, c4 = threadIdx.x % TPP;
+    const int parts = seg.x + 1;
+    // partial j lies in slot 2 i + 1 (the start) or 2 (i + j)
+    auto slot_of = [&](int j) __device__ { return 2LL * (blockIdx.x + j) + (j == 0 ? 1 : 0); };
+    float m = kNegInf, l = 0.f;
+    f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto merge = [&](float m2, float l2, f32x4_t o2) __device__ {
+        const float mn = fmaxf(m, m2), ms = mn == kNegInf ? 0.f : mn;
+        const float f1 = fast_exp2(m - ms), f2 = fast_exp2(m2 - ms);
+        l = l * f1 + l2 * f2;
+        o = o * f1 + o2 * f2;
+        m = mn;
+    };
+    for (int j = grp; j < parts; j += LANES) {
+        const long long s = slot_of(j);
+        merge(p.w.ml[s * 2 * QB + q], p.w.ml[s * 2 * QB + QB + q],
+              *reinterpret_cast<const f32x4_t *>(p.w.o + (s * QB + q) * D + 4 * c4));
+    }
+    if (c4 == 0) {
+        red[grp][D] = m;
+        red[grp][D + 1] = l;
+    }
+    *reinterpret_cast<float2 *>(&red[grp][4 * c4]) = make_float2(o[0], o[1]);
+    *reinterpret_cast<float2 *>(&red[grp][4 * c4 + 2]) = make_float2(o[2], o[3]);
+    __syncthreads();
+    if (grp != 0) return;
+    for (int k = 1; k < LANES && k < parts; ++k)
+        merge(red[k][D], red[k][D + 1], f32x4_t{red[k][4 * c4], red[k][4 * c4 + 1], red[k][4 * c4 + 2], red[k][4 * c4 + 3]});
+    store_row<T>(p, rq.row0 + qi / p.G, seg.z * p.G + qi % p.G, c4, D, o, m, l);
+}
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+template <typename T, bool E4, int D, int NQ>
+hipError_t launch_paged_typed(const PagedParams &pp, const PagedPlan &plan, hipStream_t s) {
+    launch_kernel("paged_attention", paged_kernel<T, E4, D, NQ>, dim3(plan.grid), dim3(kPagedThreads), s, pp);
+    if (!plan.whole)
+        launch_kernel("paged_join", paged_join_kernel<T, D, 16 * NQ>, dim3(plan.grid - 1, 16 * NQ), dim3(256), s, pp);
+    return hipGetLastError();
+}
+
+template <typename T, bool E4, int D>
+hipError_t launch_paged_queries(const PagedParams &pp, const PagedPlan &plan, hipStream_t s) {
+    switch (plan.qblocks) {
+        case 1: return launch_paged_typed<T, E4, D, 1>(pp, plan, s);
+        case 2: return launch_paged_typed<T, E4, D, 2>(pp, plan, s);
+        default:
+            if constexpr (D < 256)
+                return launch_paged_typed<T, E4, D, 4>(pp, plan, s);
+            else
+                return hipErrorInvalidValue;
+    }
+}
+
+template <typename T, bool E4>
+hipError_t launch_paged_dim(const PagedParams &pp, const PagedPlan &plan, hipStream_t s) {
+    switch (pp.a.head_dim) {
+        case 64: return launch_paged_queries<T, E4, 64>(pp, plan, s);
+        case 128: return launch_paged_queries<T, E4, 128>(pp, plan, s);
+        default: return launch_paged_queries<T, E4, 256>(pp, plan, s);
+    }
+}
+
+}  // namespace
+
+// The query blocks cover a request's rows times its group where they fit
+// (16 to 64 queries; 32 at D = 256, whose accumulators are twice as long);
+// more rows take several groups, which read the cache again.
+PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, long long table_tokens) {
+    PagedPlan p{};
+    const long long queries = (long long)max_rows * (n_heads / n_kv_heads);
+    const int most = head_dim >= 256 ? 2 : 4;
+    p.qblocks = queries <= 16 ? 1 : (queries <= 32 || most == 2 ? 2 : 4);
+    p.grid = kPagedGrid;
+    p.whole = table_tokens <= kWholeTokens;
+    return p;
+}
+
+PagedWork paged_carve(void *ws, const PagedPlan &p, int head_dim, size_t *bytes) {
+    Carve c(ws);
+    PagedWork w{};
+    w.meta = c.take<int4>(p.grid);
+    w.ml = c.take<float>(size_t(2) * p.grid * 2 * 16 * p.qblocks);
+    w.o = c.take<float>(size_t(2) * p.grid * 16 * p.qblocks * head_dim);
+    if (bytes) *bytes = (c.off + 255) & ~size_t(255);
+    return w;
+}
+
+hipError_t launch_paged(const PagedArgs &a, const PagedPlan &plan, const PagedWork &w, hipStream_t s) {
+    PagedParams p{};
+    p.a = a;
+    p.w = w;
+    p.G = a.n_heads / a.n_kv_heads;
+    p.pshift = log2_of(a.page_size);
+    p.whole = plan.whole;
+    p.c = a.scale * kLog2e;
+    const bool e4 = a.cache_dtype == DSPARK_E4M3;
+    if (a.dtype == DSPARK_BF16)
+        return e4 ? launch_paged_dim<TypeBf16, true>(p, plan, s) : launch_paged_dim<TypeBf16, false>(p, plan, s);
+    return e4 ? launch_paged_dim<TypeF16, true>(p, plan, s) : launch_paged_dim<TypeF16, false>(p, plan, s);
+}
+
+}  // namespace dspark

@@ -1,0 +1,342 @@
+// prompt.hip -- attention over whole prompts: packed sequences of different
+// lengths, grouped heads, causal or not.
+//
+// For query row i of a sequence with R rows and L keys and head h:
+//   s_t = scale q . k_t over t < L, and t <= L - R + i if causal (the rows are
+//   the last R positions; L = R for a prompt on its own, L > R behind a prefix),
+//   out = sum_t exp(s_t - lse) v_t,  lse = log sum_t exp(s_t).
+// The running maximum and sum of the softmax and the products are held in 32
+// bits; probabilities are rounded to 16 bits as they enter the V product.
+//
+// What bounds it: 4 D flops for every (query, key) pair against 16-bit K and V
+// tiles that a whole workgroup shares -- the matrix units, with the
+// exponentials of the softmax beside them.  A workgroup of up to eight waves
+// takes 32 queries a wave: a query is a (row, head of the group) pair, heads
+// fastest, so that the heads of a group share the K and V tiles and a
+// workgroup covers few rows (the causal diagonal wastes little).  Tiles of 64
+// tokens come in by direct loads through a ring of LDS buffers, one barrier a
+// tile.  Two waves a SIMD: one's softmax runs beside the other's products.
+// Workgroups of one key-value head are neighbours modulo the XCDs where the
+// head count allows it, and the last rows of a sequence, which see the most
+// keys, go first.
+#include "attend.hpp"
+#include "dspark.h"
+#include "internal.hpp"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kKeys = 64;  // tokens of a tile
+
+struct PromptParams {
+    PromptArgs a;
+    int G;
+    float c;  // scale * log2(e)
+};
+
+// Rows of RB = 2 D bytes in LDS, 16-byte chunk c of row r at c ^ k_swizzle(r)
+// (K: 16 rows read at one chunk) or c ^ v_swizzle(r) (V: transposing reads
+// take 4 rows of 64 bytes at a time).
+template <int D>
+struct KeyTile {
+    static constexpr int RB = 2 * D;
+    static constexpr int CPR = RB / 16;
+    static constexpr int BYTES = kKeys * RB;
+    static constexpr int PER = RB >= 256 ? 1 : 256 / RB;
+    static constexpr int SW = CPR < 16 ? CPR : 16;
+    __device__ static __forceinline__ int k_swizzle(int r) { return (r / PER) & (SW - 1); }
+    __device__ static __forceinline__ int v_swizzle(int r) { return (((r & 3) / PER) * 4) & (SW - 1); }
+};
+
+template <int D, int NW>
+struct PromptShape {
+    using S = KeyTile<D>;
+    static constexpr int NT = 64 * NW;
+    static constexpr int QB = 32 * NW;
+    static constexpr int NS = D >= 256 ? 2 : 3;              // tiles in the ring
+    static constexpr int LPT = kKeys * S::CPR / NT;          // loads a thread issues for K (and for V)
+    static constexpr int LDS = NS * 2 * S::BYTES;
+    static constexpr int EU = D >= 256 ? 1 : (NW >= 8 ? 2 : 1);
+    static_assert(LPT * NT == kKeys * S::CPR && LDS <= 160 * 1024, "tile loads");
+};
+
+template <typename T, int D, int NW>
+__global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kernel(PromptParams p) {
+    using SH = PromptShape<D, NW>;
+    using S = KeyTile<D>;
+    using V8 = typename T::V8;
+    using E = typename T::E;
+    constexpr int NS = SH::NS, KS = D / 16, CB = D / 32, TILE = 2 * S::BYTES;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
+    __shared__ int red[NW];
+
+    const PromptArgs &a = p.a;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int n = lane & 31, h = lane >> 5;
+    const uint32_t lds0 = lds_addr(lds);
+    const int kvh = blockIdx.x % a.n_kv_heads;
+    const int slot = int(gridDim.x / a.n_kv_heads) - 1 - int(blockIdx.x / a.n_kv_heads);
+
+    // ---- the sequence and query block of this slot -----------------------
+    // sequence b owns the slots from floor(off_b G / QB) + b on: enough for its
+    // blocks, whatever the lengths, and found without a scan
+    auto first_slot = [&](int b) __device__ {
+        const int off = min(max(a.q_offsets[b], 0), a.n_rows);
+        return int((long long)off * p.G / SH::QB) + b;
+    };
+    int count = 0;
+    for (int b = tid; b < a.B; b += SH::NT) count += first_slot(b) <= slot;
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) count += __shfl_xor(count, s);
+    if (lane == 0) red[wave] = count;
+    __syncthreads();
+    count = 0;
+    for (int w = 0; w < NW; ++w) count += red[w];
+    const int b = uniform(count) - 1;
+    if (b < 0) return;
+    const int q0 = uniform(min(max(a.q_offsets[b], 0), a.n_rows));
+    const int rows = uniform(min(max(a.q_offsets[b + 1], 0), a.n_rows)) - q0;
+    const int block = slot - uniform(first_slot(b));
+    const int nq = rows * p.G;
+    if (rows <= 0 || (long long)block * SH::QB >= nq) return;
+    int k0 = q0, L = rows;
+    if (a.kv_offsets) {
+        k0 = uniform(min(max(a.kv_offsets[b], 0), a.n_kv_rows));
+        L = uniform(max(min(max(a.kv_offsets[b + 1], 0), a.n_kv_rows) - k0, 0));
+    }
+    const int past = L - rows;
+    auto limit_of = [&](int row) __device__ { return a.causal ? max(min(L, past + row + 1), 0) : L; };
+
+    // this wave's queries
+    const int wq0 = block * SH::QB + wave * 32;
+    const int qi = wq0 + n;
+    const int qrow = min(qi, nq - 1) / p.G, qhead = min(qi, nq - 1) - qrow * p.G;
+    const int lim = qi < nq ? limit_of(qrow) : 0;
+    const int wlast = min(wq0 + 31, nq - 1);
+    const int wmin = uniform(wq0 < nq ? limit_of(wq0 / p.G) : 0);
+    const int wmax = uniform(wq0 < nq ? limit_of(wlast / p.G) : 0);
+    const int glast = min(block * SH::QB + SH::QB - 1, nq - 1);
+    const int gmax = uniform(limit_of(glast / p.G));
+    const int ntile = (gmax + kKeys - 1) / kKeys;
+
+    // ---- loads of a tile ---------------------------------------------------
+    uint32_t krow[SH::LPT], kch[SH::LPT], vch[SH::LPT];
+#pragma unroll
+    for (int j = 0; j < SH::LPT; ++j) {
+        const int s = (j * NW + wave) * 64 + lane;
+        krow[j] = s / S::CPR;
+        kch[j] = ((s % S::CPR) ^ S::k_swizzle(krow[j])) * 16;
+        vch[j] = ((s % S::CPR) ^ S::v_swizzle(krow[j])) * 16;
+    }
+    const uint32_t kst = uint32_t(a.k_stride * 2), vst = uint32_t(a.v_stride * 2);
+    auto issue = [&](int j0) __device__ {
+        const int t = j0 * kKeys;
+        const uint32_t dst = lds0 + (j0 % NS) * TILE;
+        const uint8_t *kb = uniform(static_cast<const uint8_t *>(a.k) + 2 * ((long long)(k0 + t) * a.k_stride + kvh * D));
+        const uint8_t *vb = uniform(static_cast<const uint8_t *>(a.v) + 2 * ((long long)(k0 + t) * a.v_stride + kvh * D));
+        const uint32_t top = uint32_t(min(L - 1 - t, kKeys - 1));  // rows past the sequence repeat its last one: masked
+#pragma unroll
+        for (int j = 0; j < SH::LPT; ++j) {
+            const uint32_t r = min(krow[j], top);
+            dma16(uniform(dst + (j * NW + wave) * 1024), r * kst + kch[j], kb);
+        }
+#pragma unroll
+        for (int j = 0; j < SH::LPT; ++j) {
+            const uint32_t r = min(krow[j], top);
+            dma16(uniform(dst + S::BYTES + (j * NW + wave) * 1024), r * vst + vch[j], vb);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < NS - 1; ++j)
+        if (j < ntile) issue(j);
+
+    V8 qf[KS];
+    {
+        const E *src = static_cast<const E *>(a.q) + (long long)(q0 + qrow) * a.q_stride + (kvh * p.G + qhead) * D + 8 * h;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const V8 *>(src + 16 * k);
+    }
+
+    // ---- read addresses ----------------------------------------------------
+    uint32_t kread[KS];
+#pragma unroll
+    for (int k = 0; k < KS; ++k) kread[k] = n * S::RB + (((2 * k + h) ^ S::k_swizzle(n)) * 16);
+    // V^T fragment (32 channels cb, 16 tokens from row r0): rows r0 + 4 h + i and r0 + 8 + 4 h + i
+    const int vrow = 4 * h + ((lane >> 2) & 3);
+    uint32_t vread[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+        vread[c] = vrow * S::RB + (((4 * c + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1);
+    auto v_frag = [&](uint32_t buf, int r0, int c) __device__ {
+        return join4<V8>(lds_read_tr16(buf + r0 * S::RB + vread[c]), lds_read_tr16(buf + (r0 + 8) * S::RB + vread[c]));
+    };
+
+    float m = kNegInf, l = 0.f;
+    f32x16_t o[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) o[c] = f32x16_t{};
+
+    for (int j = 0; j < ntile; ++j) {
+        if (NS > 2 && j + 1 < ntile)
+            vm_wait<(NS - 2) * 2 * SH::LPT>();
+        else
+            vm_wait<0>();
+        wg_barrier();  // tile j is in, and every wave is done with the buffer refilled next
+        if (j + NS - 1 < ntile) issue(j + NS - 1);
+        const int t = j * kKeys;
+        if (t >= wmax) continue;
+        const uint32_t buf = lds0 + (j % NS) * TILE;
+
+        // scores: s[tb][r] is token 32 tb + 8 (r / 4) + 4 h + r % 4, query n
+        f32x16_t s[2];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            s[tb] = f32x16_t{};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) s[tb] = mma32(lds_read<V8>(buf + 32 * tb * S::RB + kread[k]), qf[k], s[tb]);
+        }
+        const bool masked = t + kKeys > wmin;
+        if (masked) {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (t + 32 * tb + 8 * (r >> 2) + 4 * h + (r & 3) >= lim) s[tb][r] = kNegInf;
+        }
+        float mx = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+        for (int r = 1; r < 16; ++r) mx = fmaxf(fmaxf(s[0][r], s[1][r]), mx);
+        mx = max_x32(mx) * p.c;
+        const float mn = fmaxf(m, mx);
+        if (__any(mn > m)) {
+            const float al = fast_exp2(m - (mn == kNegInf ? 0.f : mn));
+            l *= al;
+#pragma unroll
+            for (int c = 0; c < CB; ++c) o[c] *= al;
+            m = mn;
+        }
+        const float ms = mn == kNegInf ? 0.f : mn;
+        V8 pf[4];
+        float sum = 0.f;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = fast_exp2(__builtin_fmaf(s[f >> 1][8 * (f & 1) + i], p.c, -ms));
+            sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            pf[f] = V8{E(e[0]), E(e[1]), E(e[2]), E(e[3]), E(e[4]), E(e[5]), E(e[6]), E(e[7])};
+        }
+        l += sum;
+
+        const uint32_t vbuf = buf + S::BYTES;
+        bool slow = false;
+        if (masked) {
+            // a V row that some queries must not see is harmless where it is
+            // finite, as their probabilities are zero; 0 * v tells
+            f32x16_t z = f32x16_t{};
+            const V8 zero = {};
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int c = 0; c < CB; ++c) z = mma32(v_frag(vbuf, 16 * f, c), zero, z);
+            float any = 0.f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) any += z[r];
+            slow = __any(any != 0.f);
+        }
+        if (!slow) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vbuf, 16 * f, c), pf[f], o[c]);
+        } else {
+            // infinities or NaN in such a row: a token at a time, kept only by the queries that see it
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                    // token 16 f + k is element e of lane half (k / 4) % 2
+                    const int e = (k & 3) + 4 * (k >> 3), tok = t + 16 * f + k;
+                    const uint32_t keep = h == ((k >> 2) & 1) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
+                    asm volatile("" : : : "memory");
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) {
+                        u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, 16 * f, c));
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
+                        const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) o[c][r] = tok < lim ? with[r] : o[c][r];
+                    }
+                }
+        }
+    }
+
+    if (qi >= nq) return;
+    l = sum_x32(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at = (long long)(q0 + qrow) * a.n_heads + kvh * p.G + qhead;
+    typedef E e4_t __attribute__((ext_vector_type(4)));
+    E *dst = static_cast<E *>(a.out) + at * D + 4 * h;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const e4_t x = l == 0.f ? e4_t{}
+                                    : e4_t{E(o[c][r] * inv), E(o[c][r + 1] * inv), E(o[c][r + 2] * inv), E(o[c][r + 3] * inv)};
+            *reinterpret_cast<e4_t *>(dst + 32 * c + 2 * r) = x;
+        }
+    if (a.lse && h == 0) a.lse[at] = lse_of(m, l);
+}
+
+template <typename T, int D, int NW>
+hipError_t launch_prompt_typed(const PromptParams &p, hipStream_t s) {
+    const PromptArgs &a = p.a;
+    const long long slots = (long long)a.n_rows * p.G / PromptShape<D, NW>::QB + a.B;
+    launch_kernel("prompt_attention", prompt_kernel<T, D, NW>, dim3(unsigned(slots * a.n_kv_heads)), dim3(64 * NW), s, p);
+    return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_prompt_waves(const PromptParams &p, const PromptPlan &plan, hipStream_t s) {
+    if constexpr (D < 256)
+        if (plan.waves == 8) return launch_prompt_typed<T, D, 8>(p, s);
+    if (plan.waves == 1) return launch_prompt_typed<T, D, 1>(p, s);
+    if (plan.waves == 2) return launch_prompt_typed<T, D, 2>(p, s);
+    return launch_prompt_typed<T, D, 4>(p, s);
+}
+
+template <typename T>
+hipError_t launch_prompt_dim(const PromptParams &p, const PromptPlan &plan, hipStream_t s) {
+    switch (p.a.head_dim) {
+        case 64: return launch_prompt_waves<T, 64>(p, plan, s);
+        case 128: return launch_prompt_waves<T, 128>(p, plan, s);
+        default: return launch_prompt_waves<T, 256>(p, plan, s);
+    }
+}
+
+}  // namespace
+
+PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim) {
+    PromptPlan p{};
+    // wide workgroups where they still fill the chip
+    const long long queries = (long long)n_rows * n_heads;
+    p.waves = head_dim < 256 && queries >= 256LL * 256 ? 8 : queries >= 128LL * 256 ? 4 : queries >= 64LL * 256 ? 2 : 1;
+    return p;
+}
+
+PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_rows, int n_heads, int head_dim, size_t *bytes) {
+    if (bytes) *bytes = 256;
+    return PromptWork{};
+}
+
+hipError_t launch_prompt(const PromptArgs &a, const PromptPlan &plan, const PromptWork &w, hipStream_t s) {
+    PromptParams p{};
+    p.a = a;
+    p.G = a.n_heads / a.n_kv_heads;
+    p.c = a.scale * kLog2e;
+    return a.dtype == DSPARK_BF16 ? launch_prompt_dim<TypeBf16>(p, plan, s) : launch_prompt_dim<TypeF16>(p, plan, s);
+}
+
+}  // namespace dspark

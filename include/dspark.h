@@ -71,10 +71,14 @@ typedef enum dspark_status {
     DSPARK_ERR_SCRATCH = -6       /* sizes need more than the allocation-free entry point's fixed scratch */
 } dspark_status;
 
-/* Element type of the Markov factors W1 and W2. */
+/* Element types.  The Markov factors W1 and W2 are DSPARK_BF16 or DSPARK_F32;
+ * attention rows and caches DSPARK_BF16 or DSPARK_F16, caches also
+ * DSPARK_E4M3. */
 typedef enum dspark_dtype {
     DSPARK_BF16 = 0, /* bfloat16 bit patterns (uint16_t) */
-    DSPARK_F32 = 1   /* IEEE float32 */
+    DSPARK_F32 = 1,  /* IEEE float32 */
+    DSPARK_F16 = 2,  /* IEEE float16 bit patterns (uint16_t) */
+    DSPARK_E4M3 = 3  /* OCP FP8 E4M3 bit patterns (uint8_t), scaled by powers of two */
 } dspark_dtype;
 
 /* Size limits checked by every entry point. */
@@ -85,6 +89,10 @@ typedef enum dspark_dtype {
 #define DSPARK_MAX_STS_SAMPLES (1 << 28) /* samples of one calibration fit */
 #define DSPARK_MAX_STS_CELLS 4096        /* grid values x bins of one fit */
 #define DSPARK_MAX_STS_GRID 1024         /* grid values of one fit */
+#define DSPARK_MAX_ROWS (1 << 24)        /* packed rows of one attention or cache call */
+#define DSPARK_MAX_HEADS 1024            /* query heads */
+#define DSPARK_MAX_CACHE_TOKENS (1 << 30) /* max_pages * page_size */
+#define DSPARK_MAX_ROW_STRIDE (1 << 24)  /* elements from one packed row to the next */
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int dspark_version(void);
@@ -382,6 +390,131 @@ int dspark_acceptance_rnn(const float *target, int n_target_rows, const int32_t 
                           const int32_t *anchor, const int32_t *x, const float *lse_q,
                           const float *temperature, int B, int gamma, int V, int r,
                           float *alpha_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Paged key-value cache ([CE] 02: the target forward of a round)      */
+/* ------------------------------------------------------------------ */
+
+/* Conventions of the cache and attention entry points.
+ *
+ * Packed rows.  A call works on n_rows rows of B requests; request b owns rows
+ * row_offsets[b] .. row_offsets[b + 1] - 1 (device [B + 1] int32, non-decreasing;
+ * NULL = one row a request, n_rows = B).  For a verify step these are the
+ * 1 + ell[b] target rows of dspark_verify, with the same offsets.  Rows of no
+ * request (before row_offsets[0], from row_offsets[B] on) are neither read into
+ * a result nor written.  Offsets are clamped into [0, n_rows] on the device.
+ * A row is [heads, head_dim]; q, k and v may be slices of wider rows: their
+ * *_stride is the distance of two rows in elements, a multiple of 8, at least
+ * heads * head_dim and at most DSPARK_MAX_ROW_STRIDE; rows are 16-byte aligned.
+ *
+ * Cache.  k_cache and v_cache are [n_pages, n_kv_heads, page_size, head_dim] of
+ * cache_dtype; page_size is a power of two from 16 to 1024.  Token t of request
+ * b lies in page page_table[b, t / page_size] (device [B, max_pages] int32) at
+ * slot t % page_size.  Several requests may share pages; a page id outside
+ * [0, n_pages) stands for no page, and so do tokens past the table: writes to
+ * them are dropped, reads give zeros, attention leaves them out.
+ * max_pages * page_size is at most DSPARK_MAX_CACHE_TOKENS; caches may be larger
+ * than 4 GiB.
+ *
+ * 8-bit caches (DSPARK_E4M3) hold, for each (token, head), head_dim e4m3 values
+ * and one scale byte e + 127 in k_scale / v_scale [n_pages, n_kv_heads,
+ * page_size] uint8: the element stands for value * 2^e.  dspark_kv_write takes
+ * the smallest e >= -126 with max|x| <= 448 * 2^e over the row's finite values
+ * and rounds x * 2^-e to the nearest e4m3 value, ties to even; infinities and
+ * NaN become NaN.  For other caches the scales are NULL.
+ *
+ * cache_len (device [B] int32) is the number of a request's tokens already in
+ * the cache: its row i of this call stands at position cache_len[b] + i.  After
+ * a verify step cache_len grows by n_accept + 1 (the anchor and the accepted
+ * drafts); the rows past them are simply written again.  A negative cache_len
+ * takes the request out of the call (a padded batch): nothing of it is written,
+ * attention gives it zeros.
+ *
+ * head_dim is 64, 128 or 256, otherwise DSPARK_ERR_UNSUPPORTED.  Row types are
+ * DSPARK_BF16 or DSPARK_F16; a cache has the rows' type or DSPARK_E4M3
+ * (otherwise DSPARK_ERR_UNSUPPORTED).  n_rows = 0 is valid and does nothing.
+ * The device current at the call must be the one that holds the buffers and
+ * owns `stream`. */
+
+/* Writes rows k, v [n_rows, n_kv_heads, head_dim] into the cache at positions
+ * cache_len[b] + i.  No two rows of one call may name the same slot (the result
+ * would be either's values).
+ *   k, v        device rows of `dtype`, row strides k_stride and v_stride
+ *   k_cache, v_cache, k_scale, v_scale   device, written at the rows' slots only */
+int dspark_kv_write(const void *k, const void *v, int64_t k_stride, int64_t v_stride, int dtype,
+                    const int32_t *row_offsets, int n_rows, const int32_t *cache_len, const int32_t *page_table, int B,
+                    int max_pages, int n_kv_heads, int head_dim, void *k_cache, void *v_cache, uint8_t *k_scale,
+                    uint8_t *v_scale, int cache_dtype, int n_pages, int page_size, void *stream);
+
+/* Reads rows back: row i of request b is the token at position first[b] + i
+ * (first NULL = 0; a negative first[b] gives zeros), as values of `dtype`.
+ * 8-bit values come back as value * 2^e rounded to `dtype` (exact in its normal
+ * range; what passes the type's largest value becomes that value).
+ *   k_out, v_out   device [n_rows, n_kv_heads, head_dim] of `dtype`, dense */
+int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
+                   int cache_dtype, int n_pages, int page_size, const int32_t *row_offsets, int n_rows,
+                   const int32_t *first, const int32_t *page_table, int B, int max_pages, int n_kv_heads, int head_dim,
+                   void *k_out, void *v_out, int dtype, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Attention ([CE] 02: one causal forward over the block's positions)  */
+/* ------------------------------------------------------------------ */
+
+/* Bytes of device workspace dspark_paged_attention needs; 0 for invalid sizes. */
+size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim);
+
+/* Attention of each request's rows over its cached tokens: row i of request b
+ * (position cache_len[b] + i), head h, with key-value head h / (n_heads /
+ * n_kv_heads):
+ *   s_t = scale * q . k_t,  out = sum_t softmax(s)_t v_t,  lse = log sum_t exp(s_t)
+ * over the tokens t <= cache_len[b] + i (causal != 0: decoding, verification)
+ * or t < cache_len[b] + rows of b (causal = 0: the rows see each other, as in a
+ * parallel draft stage).  The rows' own keys and values must be in the cache
+ * (dspark_kv_write of the same rows, before this call on the stream).  A row
+ * that sees no token gives zeros and lse = -inf.  Infinities and NaN in tokens
+ * a row does not see, or in unused slots, do not reach it.  Scores, softmax
+ * sums and products are kept in float32; probabilities enter the V product in
+ * the rows' type (bfloat16 for 8-bit caches).
+ *   q           device [n_rows, n_heads, head_dim] of `dtype`, row stride q_stride
+ *   n_heads     a multiple of n_kv_heads, at most DSPARK_MAX_HEADS
+ *   max_rows    >= 1: how many rows a request usually has at most (1 for
+ *               decoding, gamma + 1 for verification).  It only picks the
+ *               kernel: requests may have more or fewer.
+ *   scale       > 0, finite (usually head_dim^-1/2)
+ *   out         device [n_rows, n_heads, head_dim] of `dtype`, dense, 16-byte aligned
+ *   lse_out     device [n_rows, n_heads] float32 or NULL
+ *   workspace   device, >= dspark_paged_attention_workspace_size bytes
+ * The work is split over a request's length and joined in a fixed order:
+ * outputs are a pure function of the inputs.  Lengths, offsets and pages are
+ * read on the device, so a captured call follows them as they change. */
+int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
+                           int max_rows, const int32_t *cache_len, const int32_t *page_table, int B, int max_pages,
+                           int n_heads, int n_kv_heads, int head_dim, const void *k_cache, const void *v_cache,
+                           const uint8_t *k_scale, const uint8_t *v_scale, int cache_dtype, int n_pages, int page_size,
+                           float scale, int causal, void *out, float *lse_out, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Bytes of device workspace dspark_prompt_attention needs; 0 for invalid sizes. */
+size_t dspark_prompt_attention_workspace_size(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads,
+                                              int head_dim);
+
+/* Attention over whole prompts, packed: sequence b has query rows
+ * row_offsets[b] .. row_offsets[b + 1] - 1 of q and key rows kv_offsets[b] ..
+ * kv_offsets[b + 1] - 1 of k and v (kv_offsets NULL: the same rows, n_kv_rows =
+ * n_rows).  With R query rows and L keys, query row i stands at position
+ * L - R + i: causal != 0 lets it see keys t <= L - R + i (behind a prefix read
+ * back by dspark_kv_read L > R; rows with L - R + i < 0 see nothing), causal = 0
+ * every key of its sequence.  Outputs, empty rows, masked infinities and
+ * precision as for dspark_paged_attention.
+ *   q           device [n_rows, n_heads, head_dim] of `dtype`, row stride q_stride
+ *   k, v        device [n_kv_rows, n_kv_heads, head_dim], row strides k_stride, v_stride
+ *   out, lse_out   as for dspark_paged_attention; rows of no sequence are left alone
+ *   workspace   device, >= dspark_prompt_attention_workspace_size bytes */
+int dspark_prompt_attention(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, int dtype, const int32_t *row_offsets, int n_rows,
+                            const int32_t *kv_offsets, int n_kv_rows, int B, int n_heads, int n_kv_heads, int head_dim,
+                            float scale, int causal, void *out, float *lse_out, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* Host scheduler ([MG] 4.3; [CE] 04)                                  */

@@ -1,0 +1,171 @@
+"""dspark_prompt_attention against the definition in 64 bits: packed sequences of
+every length around the tile borders, prefixes, grouped heads, rows that see
+nothing, NaN and infinities in masked places, all types."""
+import math
+
+import pytest
+import torch
+
+from attendkit import U, attend, check, offsets
+
+pytestmark = pytest.mark.gpu
+
+BF, FH = torch.bfloat16, torch.float16
+
+
+def _ds():
+    import draft_sampling_verification_02_amd as ds
+    ds.load_library()
+    return ds
+
+
+def _run(rows, keys, Hkv, G, D, dtype=BF, causal=True, seed=0, lead=0, tail=0, klead=0, fused=False, scale=None, poke=None):
+    """keys None: the same rows.  poke(k, v) may change the keys and values in place."""
+    ds = _ds()
+    print(f"prompt: rows={rows[:6]} keys={None if keys is None else keys[:6]} Hkv={Hkv} G={G} D={D} {dtype} "
+          f"causal={causal}", flush=True)
+    g = torch.Generator().manual_seed(seed)
+    N = lead + sum(rows) + tail
+    if keys is None:
+        M, klead = N, lead
+    else:
+        M = klead + sum(keys) + tail
+    Hq = Hkv * G
+    if fused:
+        x = torch.randn((N, Hq + 2 * Hkv, D), generator=g).to(dtype)
+        q, k, v = x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+        xd = x.cuda()
+        qd, kd, vd = xd[:, :Hq], xd[:, Hq:Hq + Hkv], xd[:, Hq + Hkv:]
+    else:
+        q = torch.randn((N, Hq, D), generator=g).to(dtype)
+        k, v = ((torch.randn((M, Hkv, D), generator=g) * 1.3).to(dtype) for _ in range(2))
+        if poke:
+            poke(k, v)
+        qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
+    s = D ** -0.5 if scale is None else scale
+    out = {"out": torch.full((N, Hq, D), 7.0, dtype=dtype, device="cuda"), "lse": torch.full((N, Hq), 7.0, device="cuda")}
+    r = ds.dspark_prompt_attention(qd, kd, vd, offsets(rows, lead).cuda(),
+                                   kv_offsets=None if keys is None else offsets(keys, klead).cuda(), scale=scale,
+                                   causal=causal, out=out)
+    torch.cuda.synchronize()
+    at, kat = lead, klead
+    for b, n in enumerate(rows):
+        L = n if keys is None else keys[b]
+        lim = [min(L, max(0, L - n + i + 1)) if causal else L for i in range(n)]
+        o, z, tol, lt = attend(q[at:at + n].double(), k[kat:kat + L].double(), v[kat:kat + L].double(), lim, s, U[dtype],
+                               U[dtype])
+        check(f"out of {b}", r["out"][at:at + n], o, tol)
+        check(f"lse of {b}", r["lse"][at:at + n], z, lt)
+        at, kat = at + n, kat + L
+    for n in ("out", "lse"):
+        for other in (r[n][:lead], r[n][at:]):
+            assert bool((other == 7.0).all()), f"{n}: rows of no sequence were written"
+    return r
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_lengths_around_every_border(dtype, D, causal):
+    _run([1, 2, 7, 0, 31, 32, 33, 63, 64, 65, 0, 127, 129], None, 2, 4, D, dtype, causal, lead=3, tail=5)
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 8, 33])
+def test_group_sizes(G):
+    _run([70, 1, 130], None, 2, G, 64)
+
+
+@pytest.mark.parametrize("Hkv", [1, 3, 8])
+def test_wide_batches_take_wide_workgroups(Hkv):
+    # enough queries for every workgroup width
+    for n in (60, 300, 700):
+        _run([n, n // 3, 5, n], None, Hkv, 4, 64, seed=n)
+    _run([500, 9, 333], None, Hkv, 8, 128)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_behind_a_prefix(D, causal):
+    _run([1, 5, 64, 17, 3], [200, 5, 65, 400, 0], 2, 4, D, causal=causal, klead=2, tail=1)
+
+
+def test_few_rows_behind_a_long_prefix():
+    _run([3], [5000], 1, 4, 128)
+    _run([18, 1, 40], [2100, 3000, 41], 2, 8, 64)
+
+
+def test_more_rows_than_keys_leave_rows_empty():
+    _run([40, 70, 3], [10, 0, 3], 2, 2, 64)
+
+
+def test_slices_of_a_fused_projection():
+    _run([100, 1, 60], None, 2, 4, 128, fused=True)
+
+
+def test_scales():
+    _run([50], None, 1, 2, 64, scale=0.5)
+    _run([50], None, 1, 2, 64, scale=1e-6)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_bad_values_stay_behind_the_mask(bad, D):
+    # sequence 1's rows are bad, and the last rows of sequence 0: rows before
+    # them, and sequences 0 and 2 beside them, must not see them
+    ds = _ds()
+    n = [70, 30, 50]
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn((sum(n), h, D), generator=g).to(BF) for h in (4, 2, 2))
+    first = 61  # first bad row of sequence 0
+    for x in (k, v):
+        x[first:100] = bad
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets(n).cuda(), lse=True)
+    torch.cuda.synchronize()
+    o, z, tol, lt = attend(q[:first].double(), k.double(), v.double(), [i + 1 for i in range(first)], D ** -0.5, U[BF], U[BF])
+    check("out before", r["out"][:first], o, tol)
+    check("lse before", r["lse"][:first], z, lt)
+    o, z, tol, lt = attend(q[100:].double(), k[100:].double(), v[100:].double(), [i + 1 for i in range(50)], D ** -0.5, U[BF], U[BF])
+    check("out after", r["out"][100:], o, tol)
+    check("lse after", r["lse"][100:], z, lt)
+    if bad != bad:
+        assert bool(torch.isnan(r["out"][first:100]).all())
+
+
+def test_values_of_one_bad_value_reach_exactly_the_rows_that_see_it():
+    # an infinite value: the rows that see it are infinite in that channel only
+    ds = _ds()
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn((40, h, 64), generator=g).to(BF) for h in (2, 1, 1))
+    v[23, 0, 5] = math.inf
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets([40]).cuda())
+    torch.cuda.synchronize()
+    v[23, 0, 5] = 0.0
+    o, _, tol, _ = attend(q.double(), k.double(), v.double(), [i + 1 for i in range(40)], 0.125, U[BF], U[BF])
+    o[23:, :, 5] = math.inf
+    check("out", r["out"], o, tol)
+
+
+def test_same_bits_on_every_call_stream_and_graph_replay():
+    ds = _ds()
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn((300, h, 128), generator=g).to(BF).cuda() for h in (8, 2, 2))
+    off = offsets([120, 100, 80]).cuda()
+    a = ds.dspark_prompt_attention(q, k, v, off, lse=True)
+    b = ds.dspark_prompt_attention(q, k, v, off, lse=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c = ds.dspark_prompt_attention(q, k, v, off, lse=True, stream=side)
+    torch.cuda.synchronize()
+    for r in (b, c):
+        assert torch.equal(a["out"], r["out"]) and torch.equal(a["lse"], r["lse"])
+    out = ds.dspark_prompt_attention(q, k, v, off, lse=True)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        ds.dspark_prompt_attention(q, k, v, off, out=out)
+    for split in ([40, 200, 60], [300, 0, 0], [1, 1, 298]):
+        off.copy_(offsets(split).cuda())
+        eager = ds.dspark_prompt_attention(q, k, v, off, lse=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager["out"], out["out"]) and torch.equal(eager["lse"], out["lse"]), split
