@@ -11,6 +11,7 @@ immediately: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -524,6 +525,10 @@ def dspark_sts_fit(conf, n_accept, grid, *, ell=None, n_bins: int = 15, ece_grid
 
 
 # ---------------------------------------------------------------- cache and attention
+#
+# A decoding step calls these with kernels of a few microseconds, so the
+# checks take the short way where everything is in order (one expression a
+# tensor) and find the words only where something is not.
 
 _row_types = None
 
@@ -535,6 +540,19 @@ def _types():
         _row_types = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16, torch.float32: DSPARK_F32,
                       torch.float8_e4m3fn: DSPARK_E4M3}
     return _row_types
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t, name, dtype, shape, device):
+    try:
+        if t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape, device)
 
 
 def _rows(t, name, dtype, heads, device):
@@ -557,51 +575,55 @@ def _rows(t, name, dtype, heads, device):
 
 
 def _row_dtype(t, name):
-    dt = _types().get(t.dtype)
+    dt = _types().get(getattr(t, "dtype", None))
     if dt is None:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16 or float16")
+        raise TypeError(f"{name}: expected a bfloat16 or float16 tensor")
     return dt
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, device):
-    """Checks a paged cache; returns (dtype, n_pages, n_kv_heads, page_size, D)."""
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a paged cache; returns (device, dtype, n_pages, n_kv_heads, page_size, D)."""
     torch = _torch()
-    dt = _types().get(k_cache.dtype)
+    dt = _types().get(getattr(k_cache, "dtype", None))
     if dt is None:
-        raise TypeError(f"k_cache: dtype {k_cache.dtype}, expected bfloat16, float16 or float8_e4m3fn")
-    if k_cache.dim() != 4:
+        raise TypeError("k_cache: expected a bfloat16, float16 or float8_e4m3fn tensor")
+    shape, device = k_cache.shape, k_cache.device
+    if len(shape) != 4:
         raise ValueError("k_cache: [n_pages, n_kv_heads, page_size, D]")
-    _need(k_cache, "k_cache", k_cache.dtype, None, device)
-    _need(v_cache, "v_cache", k_cache.dtype, k_cache.shape, device)
+    _dense(k_cache, "k_cache", k_cache.dtype, shape, device)
+    _dense(v_cache, "v_cache", k_cache.dtype, shape, device)
     if dt == DSPARK_E4M3:
-        _need(k_scale, "k_scale", torch.uint8, k_cache.shape[:3], device)
-        _need(v_scale, "v_scale", torch.uint8, k_cache.shape[:3], device)
+        _dense(k_scale, "k_scale", torch.uint8, shape[:3], device)
+        _dense(v_scale, "v_scale", torch.uint8, shape[:3], device)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("k_scale/v_scale: only with a float8_e4m3fn cache")
-    return (dt,) + tuple(k_cache.shape)
+    return device, dt, *shape
 
 
 def _requests(row_offsets, n_rows, page_table, device):
     """Checks the request arrays; returns (B, max_pages)."""
-    torch = _torch()
+    int32 = _torch().int32
     if page_table.dim() != 2:
         raise ValueError("page_table: [B, max_pages]")
-    B = page_table.shape[0]
-    _need(page_table, "page_table", torch.int32, None, device)
+    B, max_pages = page_table.shape
+    _dense(page_table, "page_table", int32, (B, max_pages), device)
     if row_offsets is not None:
-        _need(row_offsets, "row_offsets", torch.int32, (B + 1,), device)
+        _dense(row_offsets, "row_offsets", int32, (B + 1,), device)
     elif n_rows != B:
         raise ValueError(f"row_offsets: needed for {n_rows} rows of {B} requests")
-    return B, page_table.shape[1]
+    return B, max_pages
 
 
-def _call_on(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current, on `stream` or its current stream."""
-    torch = _torch()
-    if device.index is None or device.index == torch.cuda.current_device():
-        return fn(*args, _stream_ptr(stream))
-    with torch.cuda.device(device):
-        return fn(*args, _stream_ptr(stream))
+def _call_on(device, stream, where, fn, *args):
+    """fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
+    cuda = _torch().cuda
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors on {device}, expected a HIP device")
+    if device.index != cuda.current_device():
+        with cuda.device(device):
+            return _call_on(device, stream, where, fn, *args)
+    raw = _torch()._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    _check(fn(*args, raw), where)
 
 
 def dspark_kv_write(k, v, k_cache, v_cache, cache_len, page_table, *, row_offsets=None, k_scale=None, v_scale=None,
@@ -612,19 +634,17 @@ def dspark_kv_write(k, v, k_cache, v_cache, cache_len, page_table, *, row_offset
     row i of request b, rows row_offsets[b] .. row_offsets[b + 1] - 1 (None: one
     row a request), goes to position cache_len[b] + i of page_table [B, max_pages]."""
     lib = load_library()
-    dev = k_cache.device
-    cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     dt = _row_dtype(k, "k")
     ks, vs = _rows(k, "k", k.dtype, Hkv, dev), _rows(v, "v", k.dtype, Hkv, dev)
     n = k.shape[0]
     if v.shape != k.shape or k.shape[2] != D:
         raise ValueError(f"k/v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [rows, {Hkv}, {D}]")
     B, max_pages = _requests(row_offsets, n, page_table, dev)
-    _need(cache_len, "cache_len", _torch().int32, (B,), dev)
-    st = _call_on(dev, stream, lib.dspark_kv_write, _ptr(k), _ptr(v), ks, vs, dt, _ptr(row_offsets), n,
-                  _ptr(cache_len), _ptr(page_table), B, max_pages, Hkv, D, _ptr(k_cache), _ptr(v_cache),
-                  _ptr(k_scale), _ptr(v_scale), cdt, n_pages, ps)
-    _check(st, "dspark_kv_write")
+    _dense(cache_len, "cache_len", page_table.dtype, (B,), dev)
+    _call_on(dev, stream, "dspark_kv_write", lib.dspark_kv_write, _at(k), _at(v), ks, vs, dt, _at(row_offsets), n,
+             _at(cache_len), _at(page_table), B, max_pages, Hkv, D, _at(k_cache), _at(v_cache), _at(k_scale),
+             _at(v_scale), cdt, n_pages, ps)
 
 
 def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=None, first=None, k_scale=None,
@@ -632,11 +652,10 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     """Reads rows back: row i of request b is the token at position first[b] + i
     (None: 0).  Returns {"k", "v"} [n_rows, Hkv, D] of `dtype` (None: the cache's
     type, bfloat16 for a float8_e4m3fn cache); rows of no request keep what
-    ``out`` holds (a new result holds zeros there)."""
+    ``out`` holds (zeros in a new result)."""
     torch = _torch()
     lib = load_library()
-    dev = k_cache.device
-    cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     if dtype is None:
         dtype = torch.bfloat16 if cdt == DSPARK_E4M3 else k_cache.dtype
     dt = _types().get(dtype)
@@ -644,31 +663,43 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
         raise TypeError(f"dtype: {dtype}, expected bfloat16 or float16")
     B, max_pages = _requests(row_offsets, n_rows, page_table, dev)
     if first is not None:
-        _need(first, "first", torch.int32, (B,), dev)
+        _dense(first, "first", torch.int32, (B,), dev)
     if out is None:
-        out = {n: torch.zeros((n_rows, Hkv, D), dtype=dtype, device=dev) for n in ("k", "v")}
+        new = torch.empty if row_offsets is None else torch.zeros
+        out = {n: new((n_rows, Hkv, D), dtype=dtype, device=dev) for n in ("k", "v")}
     for n in ("k", "v"):
-        _need(out[n], n, dtype, (n_rows, Hkv, D), dev)
-    st = _call_on(dev, stream, lib.dspark_kv_read, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), cdt,
-                  n_pages, ps, _ptr(row_offsets), n_rows, _ptr(first), _ptr(page_table), B, max_pages, Hkv, D,
-                  _ptr(out["k"]), _ptr(out["v"]), dt)
-    _check(st, "dspark_kv_read")
+        _dense(out[n], n, dtype, (n_rows, Hkv, D), dev)
+    _call_on(dev, stream, "dspark_kv_read", lib.dspark_kv_read, _at(k_cache), _at(v_cache), _at(k_scale),
+             _at(v_scale), cdt, n_pages, ps, _at(row_offsets), n_rows, _at(first), _at(page_table), B, max_pages, Hkv,
+             D, _at(out["k"]), _at(out["v"]), dt)
     return out
 
 
-def _attention_outputs(q, lse, out):
+def _attention_outputs(q, lse, out, every_row):
     torch = _torch()
+    dev, shape = q.device, q.shape
     if out is None:
         # rows of no request stay zero
-        out = {"out": torch.zeros(q.shape, dtype=q.dtype, device=q.device)}
+        new = torch.empty if every_row else torch.zeros
+        out = {"out": new(shape, dtype=q.dtype, device=dev)}
         if lse:
-            out["lse"] = torch.zeros(q.shape[:2], dtype=torch.float32, device=q.device)
-    _need(out["out"], "out", q.dtype, q.shape, q.device)
+            out["lse"] = new(shape[:2], dtype=torch.float32, device=dev)
+    _dense(out["out"], "out", q.dtype, shape, dev)
     if "lse" in out:
-        _need(out["lse"], "lse", torch.float32, q.shape[:2], q.device)
+        _dense(out["lse"], "lse", torch.float32, shape[:2], dev)
     return out
 
 
+def _attention_workspace(nbytes, device, workspace, out):
+    if workspace is not None:
+        out["workspace"] = workspace
+    ws = out.get("workspace")
+    if nbytes and (ws is None or ws.numel() < nbytes):  # 0 bytes: the call reports why
+        ws = out["workspace"] = _workspace(nbytes, device, None)
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+
+
+@functools.lru_cache(maxsize=1024)
 def dspark_paged_attention_workspace_size(max_rows: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return load_library().dspark_paged_attention_workspace_size(max_rows, n_heads, n_kv_heads, head_dim)
 
@@ -683,31 +714,27 @@ def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_of
     rounded up); scale: None = D^-1/2.  Returns {"out"[, "lse"], "workspace"};
     pass ``out`` (a previous result) to reuse its buffers."""
     lib = load_library()
-    dev = k_cache.device
-    cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     dt = _row_dtype(q, "q")
     qs = _rows(q, "q", q.dtype, None, dev)
-    n, Hq = q.shape[:2]
-    if q.shape[2] != D:
+    n, Hq, d = q.shape
+    if d != D:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, heads, {D}]")
     B, max_pages = _requests(row_offsets, n, page_table, dev)
-    _need(cache_len, "cache_len", _torch().int32, (B,), dev)
-    out = _attention_outputs(q, lse, out)
+    _dense(cache_len, "cache_len", page_table.dtype, (B,), dev)
+    out = _attention_outputs(q, lse, out, row_offsets is None)
     if max_rows is None:
-        max_rows = max(1, -(-n // B))
-    nbytes = lib.dspark_paged_attention_workspace_size(max_rows, Hq, Hkv, D)
-    if nbytes:  # 0: the call reports why
-        out["workspace"] = _workspace(nbytes, dev, workspace if workspace is not None else out.get("workspace"))
-    ws = out.get("workspace")
-    st = _call_on(dev, stream, lib.dspark_paged_attention, _ptr(q), qs, dt, _ptr(row_offsets), n, int(max_rows),
-                  _ptr(cache_len), _ptr(page_table), B, max_pages, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache),
-                  _ptr(k_scale), _ptr(v_scale), cdt, n_pages, ps, D ** -0.5 if scale is None else float(scale),
-                  int(bool(causal)), _ptr(out["out"]), _ptr(out.get("lse")), _ptr(ws),
-                  0 if ws is None else ws.numel())
-    _check(st, "dspark_paged_attention")
+        max_rows = max(1, -(-n // max(B, 1)))
+    ws, ws_bytes = _attention_workspace(dspark_paged_attention_workspace_size(max_rows, Hq, Hkv, D), dev, workspace,
+                                        out)
+    _call_on(dev, stream, "dspark_paged_attention", lib.dspark_paged_attention, _at(q), qs, dt, _at(row_offsets), n,
+             max_rows, _at(cache_len), _at(page_table), B, max_pages, Hq, Hkv, D, _at(k_cache), _at(v_cache),
+             _at(k_scale), _at(v_scale), cdt, n_pages, ps, D ** -0.5 if scale is None else scale, 1 if causal else 0,
+             _at(out["out"]), _at(out.get("lse")), ws, ws_bytes)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def dspark_prompt_attention_workspace_size(B: int, n_rows: int, n_kv_rows: int, n_heads: int, n_kv_heads: int,
                                            head_dim: int) -> int:
     return load_library().dspark_prompt_attention_workspace_size(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim)
@@ -720,33 +747,30 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
     (bfloat16 or float16; slices of a fused projection are fine), sequence b the
     rows row_offsets[b] .. row_offsets[b + 1] - 1 of q and kv_offsets[b] ..
     kv_offsets[b + 1] - 1 of k and v (None: the same rows).  Its query rows are
-    the last positions of its keys.  Returns {"out"[, "lse"], "workspace"}."""
+    the last positions of its keys.  scale: None = D^-1/2.  Returns {"out"[,
+    "lse"], "workspace"}; pass ``out`` (a previous result) to reuse its buffers."""
     torch = _torch()
     lib = load_library()
-    dev = q.device
     dt = _row_dtype(q, "q")
+    dev = q.device
     qs = _rows(q, "q", q.dtype, None, dev)
     n, Hq, D = q.shape
     ks, vs = _rows(k, "k", q.dtype, None, dev), _rows(v, "v", q.dtype, None, dev)
-    n_kv, Hkv = k.shape[:2]
-    if v.shape != k.shape or k.shape[2] != D:
+    n_kv, Hkv, d = k.shape
+    if v.shape != k.shape or d != D:
         raise ValueError(f"k/v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [rows, heads, {D}]")
     B = row_offsets.numel() - 1
-    _need(row_offsets, "row_offsets", torch.int32, (B + 1,), dev)
+    _dense(row_offsets, "row_offsets", torch.int32, (B + 1,), dev)
     if kv_offsets is not None:
-        _need(kv_offsets, "kv_offsets", torch.int32, (B + 1,), dev)
+        _dense(kv_offsets, "kv_offsets", torch.int32, (B + 1,), dev)
     elif n_kv != n:
         raise ValueError(f"kv_offsets: needed for {n} query rows and {n_kv} key rows")
-    out = _attention_outputs(q, lse, out)
-    nbytes = lib.dspark_prompt_attention_workspace_size(B, n, n_kv, Hq, Hkv, D)
-    if nbytes:  # 0: the call reports why
-        out["workspace"] = _workspace(nbytes, dev, workspace if workspace is not None else out.get("workspace"))
-    ws = out.get("workspace")
-    st = _call_on(dev, stream, lib.dspark_prompt_attention, _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, dt,
-                  _ptr(row_offsets), n, _ptr(kv_offsets), n_kv, B, Hq, Hkv, D,
-                  D ** -0.5 if scale is None else float(scale), int(bool(causal)), _ptr(out["out"]),
-                  _ptr(out.get("lse")), _ptr(ws), 0 if ws is None else ws.numel())
-    _check(st, "dspark_prompt_attention")
+    out = _attention_outputs(q, lse, out, False)
+    ws, ws_bytes = _attention_workspace(dspark_prompt_attention_workspace_size(B, n, n_kv, Hq, Hkv, D), dev,
+                                        workspace, out)
+    _call_on(dev, stream, "dspark_prompt_attention", lib.dspark_prompt_attention, _at(q), _at(k), _at(v), qs, ks, vs,
+             dt, _at(row_offsets), n, _at(kv_offsets), n_kv, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
+             1 if causal else 0, _at(out["out"]), _at(out.get("lse")), ws, ws_bytes)
     return out
 
 
