@@ -48,9 +48,11 @@ __device__ __forceinline__ f32x16_t mma32(f16x8_t a, f16x8_t b, f32x16_t c) {
 }
 
 // ---------------------------------------------------------------- LDS access
+// (`off`, a constant at the call, goes into the instruction)
+typedef __attribute__((address_space(3))) uint8_t *LdsBytes;
 template <typename T>
-__device__ __forceinline__ T lds_read(uint32_t at) {
-    return *reinterpret_cast<__attribute__((address_space(3))) const T *>(at);
+__device__ __forceinline__ T lds_read(uint32_t at, int off = 0) {
+    return *reinterpret_cast<__attribute__((address_space(3))) const T *>(reinterpret_cast<LdsBytes>(at) + off);
 }
 template <typename T>
 __device__ __forceinline__ void lds_write(uint32_t at, T v) {
@@ -63,12 +65,14 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) {
 // lane gets one of its 16 columns.  tr16: 4 rows of 16 16-bit values, lane
 // 4 i + c addressing row i, columns 4 c .. 4 c + 3 (8 bytes).  tr8: 8 rows of
 // 16 bytes, lane 2 j + c addressing row j, bytes 8 c .. 8 c + 7.
-__device__ __forceinline__ s16x4_t lds_read_tr16(uint32_t at) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<__attribute__((address_space(3))) s16x4_t *>(at));
+__device__ __forceinline__ s16x4_t lds_read_tr16(uint32_t at, int off = 0) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<__attribute__((address_space(3))) s16x4_t *>(reinterpret_cast<LdsBytes>(at) + off));
 }
-__device__ __forceinline__ u32x2_t lds_read_tr8(uint32_t at) {
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                                           reinterpret_cast<__attribute__((address_space(3))) i32x2_t *>(at)));
+__device__ __forceinline__ u32x2_t lds_read_tr8(uint32_t at, int off = 0) {
+    return __builtin_bit_cast(
+        u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                     reinterpret_cast<__attribute__((address_space(3))) i32x2_t *>(reinterpret_cast<LdsBytes>(at) + off)));
 }
 template <typename V8>
 __device__ __forceinline__ V8 join4(s16x4_t a, s16x4_t b) {

@@ -27,7 +27,8 @@ namespace dspark {
 
 namespace {
 
-constexpr int kKeys = 64;  // tokens of a tile
+constexpr int kKeys = 64;      // tokens of a tile
+constexpr float kSlack = 8.f;  // growth of the running maximum that is left alone, base-2 units
 
 struct PromptParams {
     PromptArgs a;
@@ -54,10 +55,10 @@ struct PromptShape {
     using S = KeyTile<D>;
     static constexpr int NT = 64 * NW;
     static constexpr int QB = 32 * NW;
-    static constexpr int NS = D >= 256 ? 2 : 3;              // tiles in the ring
+    static constexpr int NS = D >= 256 || NW < 8 ? 2 : 3;              // tiles in the ring
     static constexpr int LPT = kKeys * S::CPR / NT;          // loads a thread issues for K (and for V)
     static constexpr int LDS = NS * 2 * S::BYTES;
-    static constexpr int EU = D >= 256 ? 1 : (NW >= 8 ? 2 : 1);
+    static constexpr int EU = D >= 256 || NW < 4 ? 1 : 2;
     static_assert(LPT * NT == kKeys * S::CPR && LDS <= 160 * 1024, "tile loads");
 };
 
@@ -156,6 +157,10 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
         const E *src = static_cast<const E *>(a.q) + (long long)(q0 + qrow) * a.q_stride + (kvh * p.G + qhead) * D + 8 * h;
 #pragma unroll
         for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const V8 *>(src + 16 * k);
+        // plain register values from here on: the loop must not wait for these
+        // loads again, which would wait for every tile in flight
+#pragma unroll
+        for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(qf[k]));
     }
 
     // ---- read addresses ----------------------------------------------------
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     for (int c = 0; c < CB; ++c)
         vread[c] = vrow * S::RB + (((4 * c + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1);
     auto v_frag = [&](uint32_t buf, int r0, int c) __device__ {
-        return join4<V8>(lds_read_tr16(buf + r0 * S::RB + vread[c]), lds_read_tr16(buf + (r0 + 8) * S::RB + vread[c]));
+        return join4<V8>(lds_read_tr16(buf + vread[c], r0 * S::RB), lds_read_tr16(buf + vread[c], (r0 + 8) * S::RB));
     };
 
     float m = kNegInf, l = 0.f;
@@ -177,16 +182,18 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 #pragma unroll
     for (int c = 0; c < CB; ++c) o[c] = f32x16_t{};
 
-    for (int j = 0; j < ntile; ++j) {
-        if (NS > 2 && j + 1 < ntile)
+    // one tile: MASK where some query of the workgroup must not see some of its keys
+    auto tile = [&](int j, auto mask_tag) __device__ {
+        constexpr bool MASK = decltype(mask_tag)::value;
+        if (j + NS - 2 < ntile - 1)
             vm_wait<(NS - 2) * 2 * SH::LPT>();
         else
             vm_wait<0>();
         wg_barrier();  // tile j is in, and every wave is done with the buffer refilled next
         if (j + NS - 1 < ntile) issue(j + NS - 1);
         const int t = j * kKeys;
-        if (t >= wmax) continue;
-        const uint32_t buf = lds0 + (j % NS) * TILE;
+        if (MASK && t >= wmax) return;
+        const uint32_t buf = lds0 + (j % NS) * TILE, vbuf = buf + S::BYTES;
 
         // scores: s[tb][r] is token 32 tb + 8 (r / 4) + 4 h + r % 4, query n
         f32x16_t s[2];
@@ -194,9 +201,18 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
         for (int tb = 0; tb < 2; ++tb) {
             s[tb] = f32x16_t{};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) s[tb] = mma32(lds_read<V8>(buf + 32 * tb * S::RB + kread[k]), qf[k], s[tb]);
+            for (int k = 0; k < KS; ++k) s[tb] = mma32(lds_read<V8>(buf + kread[k], 32 * tb * S::RB), qf[k], s[tb]);
         }
-        const bool masked = t + kKeys > wmin;
+        if constexpr (!MASK) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * KS - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        }
+        const bool masked = MASK && t + kKeys > wmin;
         if (masked) {
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb)
@@ -208,15 +224,18 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 #pragma unroll
         for (int r = 1; r < 16; ++r) mx = fmaxf(fmaxf(s[0][r], s[1][r]), mx);
         mx = max_x32(mx) * p.c;
-        const float mn = fmaxf(m, mx);
-        if (__any(mn > m)) {
+        // the sums keep their scale until the maximum has grown by kSlack
+        // (base-2 units): probabilities stay below 2^kSlack, far from any
+        // type's range, and the products are rarely rescaled
+        if (__any(mx > m + kSlack)) {
+            const float mn = fmaxf(m, mx);
             const float al = fast_exp2(m - (mn == kNegInf ? 0.f : mn));
             l *= al;
 #pragma unroll
             for (int c = 0; c < CB; ++c) o[c] *= al;
             m = mn;
         }
-        const float ms = mn == kNegInf ? 0.f : mn;
+        const float ms = m == kNegInf ? 0.f : m;
         V8 pf[4];
         float sum = 0.f;
 #pragma unroll
@@ -229,8 +248,6 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
         }
         l += sum;
 
-        const uint32_t vbuf = buf + S::BYTES;
-        bool slow = false;
         if (masked) {
             // a V row that some queries must not see is harmless where it is
             // finite, as their probabilities are zero; 0 * v tells
@@ -243,35 +260,49 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
             float any = 0.f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) any += z[r];
-            slow = __any(any != 0.f);
-        }
-        if (!slow) {
+            if (__any(any != 0.f)) {
+                // infinities or NaN in such a row: a token at a time, kept only by the queries that see it
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
-#pragma unroll
-                for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vbuf, 16 * f, c), pf[f], o[c]);
-        } else {
-            // infinities or NaN in such a row: a token at a time, kept only by the queries that see it
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
+                for (int f = 0; f < 4; ++f)
 #pragma unroll 1
-                for (int k = 0; k < 16; ++k) {
-                    // token 16 f + k is element e of lane half (k / 4) % 2
-                    const int e = (k & 3) + 4 * (k >> 3), tok = t + 16 * f + k;
-                    const uint32_t keep = h == ((k >> 2) & 1) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
-                    asm volatile("" : : : "memory");
+                    for (int k = 0; k < 16; ++k) {
+                        // token 16 f + k is element e of lane half (k / 4) % 2
+                        const int e = (k & 3) + 4 * (k >> 3), tok = t + 16 * f + k;
+                        const uint32_t keep = h == ((k >> 2) & 1) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
+                        asm volatile("" : : : "memory");
 #pragma unroll
-                    for (int c = 0; c < CB; ++c) {
-                        u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, 16 * f, c));
+                        for (int c = 0; c < CB; ++c) {
+                            u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, 16 * f, c));
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
-                        const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
+                            for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
+                            const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) o[c][r] = tok < lim ? with[r] : o[c][r];
+                            for (int r = 0; r < 16; ++r) o[c][r] = tok < lim ? with[r] : o[c][r];
+                        }
                     }
-                }
+                return;
+            }
         }
-    }
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vbuf, 16 * f, c), pf[f], o[c]);
+        if constexpr (!MASK) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 28, 0);
+#pragma unroll
+        for (int i = 0; i < 4 * CB; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 28 / CB, 0);
+        }
+        }
+    };
+    // tiles that every query of the workgroup sees whole, then the rest
+    const int gmin = uniform(limit_of(block * SH::QB / p.G));
+    const int nfull = min(gmin / kKeys, ntile);
+    for (int j = 0; j < nfull; ++j) tile(j, std::false_type{});
+    for (int j = nfull; j < ntile; ++j) tile(j, std::true_type{});
 
     if (qi >= nq) return;
     l = sum_x32(l);
@@ -322,7 +353,7 @@ PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_h
     PromptPlan p{};
     // wide workgroups where they still fill the chip
     const long long queries = (long long)n_rows * n_heads;
-    p.waves = head_dim < 256 && queries >= 256LL * 256 ? 8 : queries >= 128LL * 256 ? 4 : queries >= 64LL * 256 ? 2 : 1;
+    p.waves = head_dim < 256 && queries >= 256LL * 25600000 ? 8 : queries >= 128LL * 256 ? 4 : queries >= 64LL * 256 ? 2 : 1;
     return p;
 }
 
