@@ -55,9 +55,8 @@ struct PromptShape {
     using S = KeyTile<D>;
     static constexpr int NT = 64 * NW;
     static constexpr int QB = 32 * NW;
-    static constexpr int NS = D >= 256 || NW < 8 ? 2 : 3;              // tiles in the ring
     static constexpr int LPT = kKeys * S::CPR / NT;          // loads a thread issues for K (and for V)
-    static constexpr int LDS = NS * 2 * S::BYTES;
+    static constexpr int LDS = 4 * S::BYTES;                  // two K tiles, two V tiles
     static constexpr int EU = D >= 256 || NW < 4 ? 1 : 2;
     static_assert(LPT * NT == kKeys * S::CPR && LDS <= 160 * 1024, "tile loads");
 };
@@ -68,7 +67,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     using S = KeyTile<D>;
     using V8 = typename T::V8;
     using E = typename T::E;
-    constexpr int NS = SH::NS, KS = D / 16, CB = D / 32, TILE = 2 * S::BYTES;
+    constexpr int KS = D / 16, CB = D / 32;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
     __shared__ int red[NW];
 
@@ -122,35 +121,35 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     const int ntile = (gmax + kKeys - 1) / kKeys;
 
     // ---- loads of a tile ---------------------------------------------------
-    uint32_t krow[SH::LPT], kch[SH::LPT], vch[SH::LPT];
+    const uint32_t kst = uint32_t(a.k_stride * 2), vst = uint32_t(a.v_stride * 2);
+    uint32_t koff[SH::LPT], voff[SH::LPT];
 #pragma unroll
     for (int j = 0; j < SH::LPT; ++j) {
-        const int s = (j * NW + wave) * 64 + lane;
-        krow[j] = s / S::CPR;
-        kch[j] = ((s % S::CPR) ^ S::k_swizzle(krow[j])) * 16;
-        vch[j] = ((s % S::CPR) ^ S::v_swizzle(krow[j])) * 16;
+        const int sl = (j * NW + wave) * 64 + lane, row = sl / S::CPR;
+        koff[j] = row * kst + ((sl % S::CPR) ^ S::k_swizzle(row)) * 16;
+        voff[j] = row * vst + ((sl % S::CPR) ^ S::v_swizzle(row)) * 16;
     }
-    const uint32_t kst = uint32_t(a.k_stride * 2), vst = uint32_t(a.v_stride * 2);
-    auto issue = [&](int j0) __device__ {
-        const int t = j0 * kKeys;
-        const uint32_t dst = lds0 + (j0 % NS) * TILE;
-        const uint8_t *kb = uniform(static_cast<const uint8_t *>(a.k) + 2 * ((long long)(k0 + t) * a.k_stride + kvh * D));
-        const uint8_t *vb = uniform(static_cast<const uint8_t *>(a.v) + 2 * ((long long)(k0 + t) * a.v_stride + kvh * D));
-        const uint32_t top = uint32_t(min(L - 1 - t, kKeys - 1));  // rows past the sequence repeat its last one: masked
+    auto issue = [&](const void *src, long long stride, uint32_t st, const uint32_t *off, uint32_t dst, int t) __device__ {
+        const uint8_t *base = uniform(static_cast<const uint8_t *>(src) + 2 * ((k0 + t) * stride + kvh * D));
+        if (t + kKeys <= L) {
 #pragma unroll
-        for (int j = 0; j < SH::LPT; ++j) {
-            const uint32_t r = min(krow[j], top);
-            dma16(uniform(dst + (j * NW + wave) * 1024), r * kst + kch[j], kb);
-        }
+            for (int j = 0; j < SH::LPT; ++j) dma16(uniform(dst + (j * NW + wave) * 1024), off[j], base);
+        } else {
+            // rows past the sequence repeat its last one: no query sees them
 #pragma unroll
-        for (int j = 0; j < SH::LPT; ++j) {
-            const uint32_t r = min(krow[j], top);
-            dma16(uniform(dst + S::BYTES + (j * NW + wave) * 1024), r * vst + vch[j], vb);
+            for (int j = 0; j < SH::LPT; ++j) {
+                const int row = ((j * NW + wave) * 64 + lane) / S::CPR;
+                dma16(uniform(dst + (j * NW + wave) * 1024), off[j] - max(row - (L - 1 - t), 0) * st, base);
+            }
         }
     };
-#pragma unroll
-    for (int j = 0; j < NS - 1; ++j)
-        if (j < ntile) issue(j);
+    auto issue_k = [&](int j) __device__ { issue(a.k, a.k_stride, kst, koff, lds0 + (j & 1) * S::BYTES, j * kKeys); };
+    auto issue_v = [&](int j) __device__ { issue(a.v, a.v_stride, vst, voff, lds0 + (2 + (j & 1)) * S::BYTES, j * kKeys); };
+    if (ntile > 0) {
+        issue_k(0);
+        if (ntile > 1) issue_k(1);
+        issue_v(0);
+    }
 
     V8 qf[KS];
     {
@@ -182,51 +181,38 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 #pragma unroll
     for (int c = 0; c < CB; ++c) o[c] = f32x16_t{};
 
-    // one tile: MASK where some query of the workgroup must not see some of its keys
-    auto tile = [&](int j, auto mask_tag) __device__ {
-        constexpr bool MASK = decltype(mask_tag)::value;
-        if (j + NS - 2 < ntile - 1)
-            vm_wait<(NS - 2) * 2 * SH::LPT>();
-        else
-            vm_wait<0>();
-        wg_barrier();  // tile j is in, and every wave is done with the buffer refilled next
-        if (j + NS - 1 < ntile) issue(j + NS - 1);
+    // ---- the walk, one tile ahead: while the scores of tile j become
+    // probabilities and meet V, the products of tile j + 1 with the queries run
+    // beside them in the same instruction stream
+    f32x16_t s[2];  // s[tb][r] is token 32 tb + 8 (r / 4) + 4 h + r % 4 of the tile, query n
+    auto scores = [&](int j, f32x16_t *x) __device__ {
+        const uint32_t buf = lds0 + (j & 1) * S::BYTES;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) x[tb] = f32x16_t{};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) x[tb] = mma32(lds_read<V8>(buf + kread[k], 32 * tb * S::RB), qf[k], x[tb]);
+    };
+    auto hide = [&](int j, f32x16_t *x) __device__ {
         const int t = j * kKeys;
-        if (MASK && t >= wmax) return;
-        const uint32_t buf = lds0 + (j % NS) * TILE, vbuf = buf + S::BYTES;
-
-        // scores: s[tb][r] is token 32 tb + 8 (r / 4) + 4 h + r % 4, query n
-        f32x16_t s[2];
+        if (t + kKeys <= wmin) return;
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            s[tb] = f32x16_t{};
+        for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-            for (int k = 0; k < KS; ++k) s[tb] = mma32(lds_read<V8>(buf + kread[k], 32 * tb * S::RB), qf[k], s[tb]);
-        }
-        if constexpr (!MASK) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+            for (int r = 0; r < 16; ++r)
+                if (t + 32 * tb + 8 * (r >> 2) + 4 * h + (r & 3) >= lim) x[tb][r] = kNegInf;
+    };
+    auto largest = [&](const f32x16_t *x) __device__ {
+        float mx = fmaxf(x[0][0], x[1][0]);
 #pragma unroll
-        for (int i = 0; i < 2 * KS - 4; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
-        }
-        const bool masked = MASK && t + kKeys > wmin;
-        if (masked) {
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (t + 32 * tb + 8 * (r >> 2) + 4 * h + (r & 3) >= lim) s[tb][r] = kNegInf;
-        }
-        float mx = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-        for (int r = 1; r < 16; ++r) mx = fmaxf(fmaxf(s[0][r], s[1][r]), mx);
-        mx = max_x32(mx) * p.c;
-        // the sums keep their scale until the maximum has grown by kSlack
-        // (base-2 units): probabilities stay below 2^kSlack, far from any
-        // type's range, and the products are rarely rescaled
+        for (int r = 1; r < 16; ++r) mx = fmaxf(fmaxf(x[0][r], x[1][r]), mx);
+        return max_x32(mx) * p.c;
+    };
+    // the sums keep their scale until the maximum has grown by kSlack (base-2
+    // units): probabilities stay below 2^kSlack, far from any type's range, and
+    // the products are rarely rescaled
+    auto raise = [&](float mx) __device__ {
         if (__any(mx > m + kSlack)) {
             const float mn = fmaxf(m, mx);
             const float al = fast_exp2(m - (mn == kNegInf ? 0.f : mn));
@@ -235,20 +221,136 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
             for (int c = 0; c < CB; ++c) o[c] *= al;
             m = mn;
         }
-        const float ms = m == kNegInf ? 0.f : m;
-        V8 pf[4];
-        float sum = 0.f;
+    };
+    auto probabilities = [&](const f32x16_t *x, float ms, int f, V8 &pf) __device__ {
+        float e[8];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            float e[8];
+        for (int i = 0; i < 8; ++i) e[i] = fast_exp2(__builtin_fmaf(x[f >> 1][8 * (f & 1) + i], p.c, -ms));
+        l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        pf = V8{E(e[0]), E(e[1]), E(e[2]), E(e[3]), E(e[4]), E(e[5]), E(e[6]), E(e[7])};
+    };
+    // K of tile j + 1 and V of tile j are in, and every wave is done with the
+    // buffers that K of tile j + 2 and V of tile j + 1 go to
+    auto turn = [&](int j) __device__ {
+        vm_wait<0>();
+        wg_barrier();
+        if (j + 2 < ntile) issue_k(j + 2);
+        if (j + 1 < ntile) issue_v(j + 1);
+    };
+    // infinities or NaN among V rows that some queries must not see: a token at
+    // a time, kept only by the queries that see it
+    auto product_by_token = [&](int t, uint32_t vbuf, const V8 *pf) __device__ {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = fast_exp2(__builtin_fmaf(s[f >> 1][8 * (f & 1) + i], p.c, -ms));
-            sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            pf[f] = V8{E(e[0]), E(e[1]), E(e[2]), E(e[3]), E(e[4]), E(e[5]), E(e[6]), E(e[7])};
-        }
-        l += sum;
+        for (int f = 0; f < 4; ++f)
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+                // token 16 f + k is element e of lane half (k / 4) % 2
+                const int e = (k & 3) + 4 * (k >> 3), tok = t + 16 * f + k;
+                const uint32_t keep = h == ((k >> 2) & 1) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
+                asm volatile("" : : : "memory");
+#pragma unroll
+                for (int c = 0; c < CB; ++c) {
+                    u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, 16 * f, c));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
+                    const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[c][r] = tok < lim ? with[r] : o[c][r];
+                }
+            }
+    };
+    auto product = [&](uint32_t vbuf, const V8 *pf, int f) __device__ {
+#pragma unroll
+        for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vbuf, 16 * f, c), pf[f], o[c]);
+    };
 
-        if (masked) {
+    if (ntile > 0) {
+        vm_wait<0>();
+        wg_barrier();
+        scores(0, s);
+        hide(0, s);
+        raise(largest(s));
+        wg_barrier();  // K of tile 0 is read: its buffer is refilled in turn(0)
+    }
+    // Tile j with scores y, the next tile's scores into x; both tiles are seen
+    // whole by every query.  The two loops are the two halves of the work on
+    // the matrix units; each step carries a share of the softmax and the LDS
+    // reads of the steps to come, and the compiler keeps to the steps.
+    auto step = [&](int jj, f32x16_t *y, f32x16_t *x) __device__ {
+        turn(jj);
+        const uint32_t kbuf = lds0 + ((jj + 1) & 1) * S::BYTES, vbuf = lds0 + (2 + (jj & 1)) * S::BYTES;
+        const float ms = m == kNegInf ? 0.f : m;
+        constexpr int KA = KS < 3 ? KS : 3, VA = 4;  // operands held: reads run two (K) and three (V) steps ahead
+        V8 ka[KA][2], va[VA], pf[4];
+        auto read_k = [&](int k) __device__ {
+            ka[k % KA][0] = lds_read<V8>(kbuf + kread[k]);
+            ka[k % KA][1] = lds_read<V8>(kbuf + kread[k], 32 * S::RB);
+        };
+        auto read_v = [&](int i) __device__ { va[i % VA] = v_frag(vbuf, 16 * (i / CB), i % CB); };
+#pragma unroll
+        for (int k = 0; k < KA - 1; ++k) read_k(k);
+        x[0] = x[1] = f32x16_t{};
+        constexpr int EPS = 32 / KS;  // probabilities a step
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            if (k + KA - 1 < KS) read_k(k + KA - 1);
+            if (k + VA - 1 >= KS) read_v(k + VA - 1 - KS);
+            x[0] = mma32(ka[k % KA][0], qf[k], x[0]);
+            x[1] = mma32(ka[k % KA][1], qf[k], x[1]);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPS; ++i) {
+                const int e = k * EPS + i;
+                const float pr = fast_exp2(__builtin_fmaf(y[e >> 4][e & 15], p.c, -ms));
+                sum += pr;
+                pf[e >> 3][e & 7] = E(pr);
+            }
+            l += sum;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        constexpr int NP = 4 * CB;  // products with V
+        float mx = kNegInf;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            if (i + VA - 1 < NP) read_v(i + VA - 1);
+            o[i % CB] = mma32(va[i % VA], pf[i / CB], o[i % CB]);
+#pragma unroll
+            for (int r = i * 16 / NP; r < (i + 1) * 16 / NP; ++r) mx = fmaxf(fmaxf(x[0][r], x[1][r]), mx);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        raise(max_x32(mx) * p.c);
+    };
+    // tiles whose successor, too, every query of the workgroup sees whole, then the rest
+    const int gmin = uniform(limit_of(block * SH::QB / p.G));
+    const int nfull = min(gmin / kKeys, ntile);
+    int j = 0;
+    {
+        f32x16_t x[2];
+        for (; j + 2 < nfull; j += 2) {
+            step(j, s, x);
+            step(j + 1, x, s);
+        }
+        if (j + 1 < nfull) {
+            step(j, s, x);
+            s[0] = x[0];
+            s[1] = x[1];
+            ++j;
+        }
+    }
+    for (; j < ntile; ++j) {
+        turn(j);
+        const int t = j * kKeys;
+        if (t >= wmax) continue;
+        const uint32_t vbuf = lds0 + (2 + (j & 1)) * S::BYTES;
+        const bool next = j + 1 < ntile && t + kKeys < wmax;
+        const float ms = m == kNegInf ? 0.f : m;
+        f32x16_t x[2];
+        V8 pf[4];
+        if (next) scores(j + 1, x);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
+        bool bad = false;
+        if (t + kKeys > wmin) {
             // a V row that some queries must not see is harmless where it is
             // finite, as their probabilities are zero; 0 * v tells
             f32x16_t z = f32x16_t{};
@@ -260,49 +362,21 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
             float any = 0.f;
 #pragma unroll
             for (int r = 0; r < 16; ++r) any += z[r];
-            if (__any(any != 0.f)) {
-                // infinities or NaN in such a row: a token at a time, kept only by the queries that see it
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-#pragma unroll 1
-                    for (int k = 0; k < 16; ++k) {
-                        // token 16 f + k is element e of lane half (k / 4) % 2
-                        const int e = (k & 3) + 4 * (k >> 3), tok = t + 16 * f + k;
-                        const uint32_t keep = h == ((k >> 2) & 1) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
-                        asm volatile("" : : : "memory");
-#pragma unroll
-                        for (int c = 0; c < CB; ++c) {
-                            u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, 16 * f, c));
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
-                            const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) o[c][r] = tok < lim ? with[r] : o[c][r];
-                        }
-                    }
-                return;
-            }
+            bad = __any(any != 0.f);
         }
+        if (bad) {
+            product_by_token(t, vbuf, pf);
+        } else {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vbuf, 16 * f, c), pf[f], o[c]);
-        if constexpr (!MASK) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 28, 0);
-#pragma unroll
-        for (int i = 0; i < 4 * CB; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, 28 / CB, 0);
+            for (int f = 0; f < 4; ++f) product(vbuf, pf, f);
         }
+        if (next) {
+            hide(j + 1, x);
+            raise(largest(x));
+            s[0] = x[0];
+            s[1] = x[1];
         }
-    };
-    // tiles that every query of the workgroup sees whole, then the rest
-    const int gmin = uniform(limit_of(block * SH::QB / p.G));
-    const int nfull = min(gmin / kKeys, ntile);
-    for (int j = 0; j < nfull; ++j) tile(j, std::false_type{});
-    for (int j = nfull; j < ntile; ++j) tile(j, std::true_type{});
+    }
 
     if (qi >= nq) return;
     l = sum_x32(l);
@@ -353,7 +427,7 @@ PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_h
     PromptPlan p{};
     // wide workgroups where they still fill the chip
     const long long queries = (long long)n_rows * n_heads;
-    p.waves = head_dim < 256 && queries >= 256LL * 25600000 ? 8 : queries >= 128LL * 256 ? 4 : queries >= 64LL * 256 ? 2 : 1;
+    p.waves = head_dim < 256 && queries >= 256LL * 256 ? 8 : queries >= 128LL * 256 ? 4 : queries >= 64LL * 256 ? 2 : 1;
     return p;
 }
 
