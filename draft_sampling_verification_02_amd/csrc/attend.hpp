@@ -25,14 +25,23 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4v_t __attribute__((ext_vector_type(4)));
 
 // Element types of rows and caches: storage is 16 bits, E names the value type.
+// kInf is the bit pattern of infinity: magnitudes from it on are not finite.
 struct TypeBf16 {
     using E = __bf16;
     using V8 = bf16x8_t;
+    static constexpr uint32_t kInf = 0x7f80;
 };
 struct TypeF16 {
     using E = _Float16;
     using V8 = f16x8_t;
+    static constexpr uint32_t kInf = 0x7c00;
 };
+
+// the larger of each of two 16-bit halves, unsigned
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
 
 __device__ __forceinline__ f32x4_t mma16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

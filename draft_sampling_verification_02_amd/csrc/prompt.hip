@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     using E = typename T::E;
     constexpr int KS = D / 16, CB = D / 32;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
-    __shared__ int red[NW];
+    __shared__ int found[5], found_bad;
 
     const PromptArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -80,31 +80,36 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 
     // ---- the sequence and query block of this slot -----------------------
     // sequence b owns the slots from floor(off_b G / QB) + b on: enough for its
-    // blocks, whatever the lengths, and found without a scan
-    auto first_slot = [&](int b) __device__ {
-        const int off = min(max(a.q_offsets[b], 0), a.n_rows);
-        return int((long long)off * p.G / SH::QB) + b;
-    };
-    int count = 0;
-    for (int b = tid; b < a.B; b += SH::NT) count += first_slot(b) <= slot;
-#pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) count += __shfl_xor(count, s);
-    if (lane == 0) red[wave] = count;
-    __syncthreads();
-    count = 0;
-    for (int w = 0; w < NW; ++w) count += red[w];
-    const int b = uniform(count) - 1;
-    if (b < 0) return;
-    const int q0 = uniform(min(max(a.q_offsets[b], 0), a.n_rows));
-    const int rows = uniform(min(max(a.q_offsets[b + 1], 0), a.n_rows)) - q0;
-    const int block = slot - uniform(first_slot(b));
-    const int nq = rows * p.G;
-    if (rows <= 0 || (long long)block * SH::QB >= nq) return;
-    int k0 = q0, L = rows;
-    if (a.kv_offsets) {
-        k0 = uniform(min(max(a.kv_offsets[b], 0), a.n_kv_rows));
-        L = uniform(max(min(max(a.kv_offsets[b + 1], 0), a.n_kv_rows) - k0, 0));
+    // blocks, whatever the lengths, and found without a scan.  Every thread
+    // tests its sequences with all it needs in one round of loads.
+    auto clamped = [&](const int32_t *off, int i, int n_max) __device__ { return min(max(off[i], 0), n_max); };
+    auto slot_of = [&](int off, int i) __device__ { return int((long long)off * p.G / SH::QB) + i; };
+    if (tid == 0) {
+        found[0] = -1;
+        found_bad = 0;
     }
+    __syncthreads();
+    for (int i = tid; i < a.B; i += SH::NT) {
+        const int r0 = clamped(a.q_offsets, i, a.n_rows), r1 = clamped(a.q_offsets, i + 1, a.n_rows);
+        int c0 = r0, c1 = r1;
+        if (a.kv_offsets) {
+            c0 = clamped(a.kv_offsets, i, a.n_kv_rows);
+            c1 = clamped(a.kv_offsets, i + 1, a.n_kv_rows);
+        }
+        const int s0 = slot_of(r0, i);
+        if (s0 <= slot && slot < slot_of(r1, i + 1)) {  // one sequence at most, as offsets do not decrease
+            found[0] = slot - s0;
+            found[1] = r0;
+            found[2] = r1 - r0;
+            found[3] = c0;
+            found[4] = max(c1 - c0, 0);
+        }
+    }
+    __syncthreads();
+    const int block = uniform(found[0]), q0 = uniform(found[1]), rows = uniform(found[2]);
+    const int k0 = uniform(found[3]), L = uniform(found[4]);
+    const int nq = rows * p.G;
+    if (block < 0 || rows <= 0 || (long long)block * SH::QB >= nq) return;
     const int past = L - rows;
     auto limit_of = [&](int row) __device__ { return a.causal ? max(min(L, past + row + 1), 0) : L; };
 
@@ -270,7 +275,6 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
         scores(0, s);
         hide(0, s);
         raise(largest(s));
-        wg_barrier();  // K of tile 0 is read: its buffer is refilled in turn(0)
     }
     // Tile j with scores y, the next tile's scores into x; both tiles are seen
     // whole by every query.  The two loops are the two halves of the work on
@@ -340,41 +344,39 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     for (; j < ntile; ++j) {
         turn(j);
         const int t = j * kKeys;
-        if (t >= wmax) continue;
         const uint32_t vbuf = lds0 + (2 + (j & 1)) * S::BYTES;
-        const bool next = j + 1 < ntile && t + kKeys < wmax;
+        // A V row that some queries must not see is harmless where it is finite,
+        // as their probabilities are zero.  The workgroup looks its tile over,
+        // a share a thread, for the rest.
+        bool bad = false;
+        if (t + kKeys > gmin) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < SH::LPT; ++i) {
+                const u32x4v_t w = lds_read<u32x4v_t>(vbuf + ((i * NW + wave) * 64 + lane) * 16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) top = max_u16x2(top, w[q] & 0x7fff7fffu);
+            }
+            const uint32_t inf = T::kInf;
+            if (__any((top & 0xffffu) >= inf || (top >> 16) >= inf) && lane == 0) found_bad = j + 1;
+            wg_barrier();
+            bad = found_bad == j + 1;
+        }
+        if (t >= wmax) continue;
         const float ms = m == kNegInf ? 0.f : m;
-        f32x16_t x[2];
         V8 pf[4];
-        if (next) scores(j + 1, x);
 #pragma unroll
         for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
-        bool bad = false;
-        if (t + kKeys > wmin) {
-            // a V row that some queries must not see is harmless where it is
-            // finite, as their probabilities are zero; 0 * v tells
-            f32x16_t z = f32x16_t{};
-            const V8 zero = {};
-#pragma unroll
-            for (int f = 0; f < 4; ++f)
-#pragma unroll
-                for (int c = 0; c < CB; ++c) z = mma32(v_frag(vbuf, 16 * f, c), zero, z);
-            float any = 0.f;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) any += z[r];
-            bad = __any(any != 0.f);
-        }
         if (bad) {
             product_by_token(t, vbuf, pf);
         } else {
 #pragma unroll
             for (int f = 0; f < 4; ++f) product(vbuf, pf, f);
         }
-        if (next) {
-            hide(j + 1, x);
-            raise(largest(x));
-            s[0] = x[0];
-            s[1] = x[1];
+        if (j + 1 < ntile && t + kKeys < wmax) {
+            scores(j + 1, s);
+            hide(j + 1, s);
+            raise(largest(s));
         }
     }
 
