@@ -10,7 +10,7 @@
 //
 // What bounds it: 4 D flops for every (query, key) pair against 16-bit K and V
 // tiles that a whole workgroup shares -- the matrix units, with the
-// exponentials of the softmax beside them.  A workgroup of up to eight waves
+// exponentials of the softmax beside them.  A workgroup of up to four waves
 // takes 32 queries a wave: a query is a (row, head of the group) pair, heads
 // fastest, so that the heads of a group share the K and V tiles and a
 // workgroup covers few rows (the causal diagonal wastes little).  Tiles of 64
@@ -127,24 +127,34 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 
     // ---- loads of a tile ---------------------------------------------------
     const uint32_t kst = uint32_t(a.k_stride * 2), vst = uint32_t(a.v_stride * 2);
-    uint32_t koff[SH::LPT], voff[SH::LPT];
+    // load j of a thread covers row j * RPL further down; where that is a whole
+    // period of the swizzles one offset serves them all
+    constexpr int RPL = SH::NT / S::CPR;
+    constexpr int OFFS = RPL % 16 == 0 ? 1 : SH::LPT;
+    uint32_t koff[OFFS], voff[OFFS];
 #pragma unroll
-    for (int j = 0; j < SH::LPT; ++j) {
+    for (int j = 0; j < OFFS; ++j) {
         const int sl = (j * NW + wave) * 64 + lane, row = sl / S::CPR;
         koff[j] = row * kst + ((sl % S::CPR) ^ S::k_swizzle(row)) * 16;
         voff[j] = row * vst + ((sl % S::CPR) ^ S::v_swizzle(row)) * 16;
     }
     auto issue = [&](const void *src, long long stride, uint32_t st, const uint32_t *off, uint32_t dst, int t) __device__ {
         const uint8_t *base = uniform(static_cast<const uint8_t *>(src) + 2 * ((k0 + t) * stride + kvh * D));
-        if (t + kKeys <= L) {
+        const int over = t + kKeys - L;
+        if (over <= 0) {
 #pragma unroll
-            for (int j = 0; j < SH::LPT; ++j) dma16(uniform(dst + (j * NW + wave) * 1024), off[j], base);
+            for (int j = 0; j < SH::LPT; ++j)
+                dma16(uniform(dst + (j * NW + wave) * 1024), off[OFFS == 1 ? 0 : j],
+                      OFFS == 1 ? uniform(base + size_t(j * RPL) * st) : base);
         } else {
             // rows past the sequence repeat its last one: no query sees them
+            // (offsets are unsigned, so a row's own offset is taken whole
+            // before the rows it goes back are subtracted)
 #pragma unroll
             for (int j = 0; j < SH::LPT; ++j) {
                 const int row = ((j * NW + wave) * 64 + lane) / S::CPR;
-                dma16(uniform(dst + (j * NW + wave) * 1024), off[j] - max(row - (L - 1 - t), 0) * st, base);
+                const uint32_t whole = OFFS == 1 ? off[0] + uint32_t(j * RPL) * st : off[OFFS == 1 ? 0 : j];
+                dma16(uniform(dst + (j * NW + wave) * 1024), whole - uint32_t(max(row + over - (kKeys - 1), 0)) * st, base);
             }
         }
     };
@@ -407,8 +417,6 @@ hipError_t launch_prompt_typed(const PromptParams &p, hipStream_t s) {
 
 template <typename T, int D>
 hipError_t launch_prompt_waves(const PromptParams &p, const PromptPlan &plan, hipStream_t s) {
-    if constexpr (D < 256)
-        if (plan.waves == 8) return launch_prompt_typed<T, D, 8>(p, s);
     if (plan.waves == 1) return launch_prompt_typed<T, D, 1>(p, s);
     if (plan.waves == 2) return launch_prompt_typed<T, D, 2>(p, s);
     return launch_prompt_typed<T, D, 4>(p, s);
@@ -427,9 +435,9 @@ hipError_t launch_prompt_dim(const PromptParams &p, const PromptPlan &plan, hipS
 
 PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim) {
     PromptPlan p{};
-    // wide workgroups where they still fill the chip
+    // wide workgroups where they still fill the chip (two a compute unit)
     const long long queries = (long long)n_rows * n_heads;
-    p.waves = head_dim < 256 && queries >= 256LL * 256 ? 8 : queries >= 128LL * 256 ? 4 : queries >= 64LL * 256 ? 2 : 1;
+    p.waves = queries >= 128LL * 512 ? 4 : queries >= 64LL * 512 ? 2 : 1;
     return p;
 }
 
