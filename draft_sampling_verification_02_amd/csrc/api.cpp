@@ -778,8 +778,7 @@ size_t dspark_prompt_attention_workspace_size(int B, int n_rows, int n_kv_rows, 
         !head_dim_supported(head_dim))
         return 0;
     size_t bytes = 0;
-    prompt_carve(nullptr, prompt_plan(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim), n_rows, n_heads, head_dim,
-                 &bytes);
+    prompt_carve(nullptr, prompt_plan(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim), n_kv_heads, head_dim, &bytes);
     return bytes;
 }
 
@@ -805,9 +804,9 @@ int dspark_prompt_attention(const void *q, const void *k, const void *v, int64_t
         return DSPARK_ERR_ARG;
     const PromptPlan plan = prompt_plan(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim);
     size_t need = 0;
-    prompt_carve(nullptr, plan, n_rows, n_heads, head_dim, &need);
+    prompt_carve(nullptr, plan, n_kv_heads, head_dim, &need);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
-    const PromptWork w = prompt_carve(workspace, plan, n_rows, n_heads, head_dim, nullptr);
+    const PromptWork w = prompt_carve(workspace, plan, n_kv_heads, head_dim, nullptr);
     PromptArgs a{};
     a.q = q;
     a.k = k;

@@ -180,4 +180,25 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? kNegInf : (m + fast_log2(l)) * kLn2;
 }
 
+// Four channels of one output row (row * heads + head = at), normalised: out =
+// o / l, zeros where nothing is visible; lse from the maximum and sum.
+template <typename T>
+__device__ __forceinline__ void store_row(void *out, float *lse, long long at, int c4, int D, f32x4_t o, float m, float l) {
+    using E = typename T::E;
+    typedef E e4_t __attribute__((ext_vector_type(4)));
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const e4_t x = l == 0.f ? e4_t{} : e4_t{E(o[0] * inv), E(o[1] * inv), E(o[2] * inv), E(o[3] * inv)};
+    *reinterpret_cast<e4_t *>(static_cast<E *>(out) + at * D + 4 * c4) = x;
+    if (lse && c4 == 0) lse[at] = lse_of(m, l);
+}
+
+// Adds a partial result (maximum m2, sum l2, products o2) to (m, l, o).
+__device__ __forceinline__ void merge_partial(float &m, float &l, f32x4_t &o, float m2, float l2, f32x4_t o2) {
+    const float mn = fmaxf(m, m2), ms = mn == kNegInf ? 0.f : mn;
+    const float f1 = fast_exp2(m - ms), f2 = fast_exp2(m2 - ms);
+    l = l * f1 + l2 * f2;
+    o = o * f1 + o2 * f2;
+    m = mn;
+}
+
 }  // namespace dspark

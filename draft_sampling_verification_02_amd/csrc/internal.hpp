@@ -309,13 +309,16 @@ struct PromptArgs {
     float *lse;
 };
 struct PromptPlan {
-    int waves;  // of a workgroup; each holds 32 queries
+    int slots;   // query blocks a key-value head has at most
+    int nsplit;  // ranges a block's keys are cut into at most
 };
 PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim);
 struct PromptWork {
-    float *ml, *o;  // unused while nothing is split
+    int4 *meta;  // [slots * n_kv_heads] parts, first row, queries and block of a unit
+    float *ml;   // [units * nsplit, 2, queries] partial maxima and sums
+    float *o;    // [units * nsplit, queries, D] partial products
 };
-PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_rows, int n_heads, int head_dim, size_t *bytes);
+PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_kv_heads, int head_dim, size_t *bytes);
 hipError_t launch_prompt(const PromptArgs &a, const PromptPlan &p, const PromptWork &w, hipStream_t s);
 
 // ---- diagnostics -----------------------------------------------------

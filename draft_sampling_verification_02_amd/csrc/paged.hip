@@ -138,20 +138,6 @@ struct PagedShape {
     static_assert(LDS <= 160 * 1024, "LDS of a workgroup");
 };
 
-// Four channels of one output row, normalised: out = o / l (0 where nothing is
-// visible), lse from the maximum and sum.
-template <typename T>
-__device__ __forceinline__ void store_row(const PagedParams &p, int row, int head, int c4, int D, f32x4_t o, float m,
-                                          float l) {
-    using E = typename T::E;
-    typedef E e4_t __attribute__((ext_vector_type(4)));
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long at = (long long)row * p.a.n_heads + head;
-    const e4_t x = l == 0.f ? e4_t{} : e4_t{E(o[0] * inv), E(o[1] * inv), E(o[2] * inv), E(o[3] * inv)};
-    *reinterpret_cast<e4_t *>(static_cast<E *>(p.a.out) + at * D + 4 * c4) = x;
-    if (p.a.lse && c4 == 0) p.a.lse[at] = lse_of(m, l);
-}
-
 template <typename T, bool E4, int D, int NQ>
 __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) void paged_kernel(PagedParams p) {
     using SH = PagedShape<T, E4, D, NQ>;
@@ -544,7 +530,7 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
                 acc += lds_read<f32x4_t>(lds0 + ((w * QB + q) * SH::OROW + 4 * c4) * 4) * f;
             }
             if (starts && ends) {
-                if (qi < nq_all) store_row<T>(p, rq.row0 + qi / p.G, h * p.G + qi % p.G, c4, D, acc, mm, ll);
+                if (qi < nq_all) store_row<T>(a.out, a.lse, (long long)(rq.row0 + qi / p.G) * a.n_heads + h * p.G + qi % p.G, c4, D, acc, mm, ll);
             } else {
                 *reinterpret_cast<f32x4_t *>(p.w.o + (slot * QB + q) * D + 4 * c4) = acc;
                 if (c4 == 0) {
@@ -585,16 +571,9 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p) {
     auto slot_of = [&](int j) __device__ { return 2LL * (blockIdx.x + j) + (j == 0 ? 1 : 0); };
     float m = kNegInf, l = 0.f;
     f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    auto merge = [&](float m2, float l2, f32x4_t o2) __device__ {
-        const float mn = fmaxf(m, m2), ms = mn == kNegInf ? 0.f : mn;
-        const float f1 = fast_exp2(m - ms), f2 = fast_exp2(m2 - ms);
-        l = l * f1 + l2 * f2;
-        o = o * f1 + o2 * f2;
-        m = mn;
-    };
     for (int j = grp; j < parts; j += LANES) {
         const long long s = slot_of(j);
-        merge(p.w.ml[s * 2 * QB + q], p.w.ml[s * 2 * QB + QB + q],
+        merge_partial(m, l, o, p.w.ml[s * 2 * QB + q], p.w.ml[s * 2 * QB + QB + q],
               *reinterpret_cast<const f32x4_t *>(p.w.o + (s * QB + q) * D + 4 * c4));
     }
     if (c4 == 0) {
@@ -606,8 +585,8 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p) {
     __syncthreads();
     if (grp != 0) return;
     for (int k = 1; k < LANES && k < parts; ++k)
-        merge(red[k][D], red[k][D + 1], f32x4_t{red[k][4 * c4], red[k][4 * c4 + 1], red[k][4 * c4 + 2], red[k][4 * c4 + 3]});
-    store_row<T>(p, rq.row0 + qi / p.G, seg.z * p.G + qi % p.G, c4, D, o, m, l);
+        merge_partial(m, l, o, red[k][D], red[k][D + 1], f32x4_t{red[k][4 * c4], red[k][4 * c4 + 1], red[k][4 * c4 + 2], red[k][4 * c4 + 3]});
+    store_row<T>(p.a.out, p.a.lse, (long long)(rq.row0 + qi / p.G) * p.a.n_heads + seg.z * p.G + qi % p.G, c4, D, o, m, l);
 }
 
 int log2_of(int x) {

@@ -19,6 +19,8 @@
 // Workgroups of one key-value head are neighbours modulo the XCDs where the
 // head count allows it, and the last rows of a sequence, which see the most
 // keys, go first.
+#include <algorithm>
+
 #include "attend.hpp"
 #include "dspark.h"
 #include "internal.hpp"
@@ -28,11 +30,16 @@ namespace dspark {
 namespace {
 
 constexpr int kKeys = 64;      // tokens of a tile
+constexpr int kPromptWaves = 4;                      // of a workgroup
+constexpr int kPromptQueries = 32 * kPromptWaves;    // queries of a workgroup
+constexpr int kPromptTarget = 640;                   // workgroups a split call aims at
+constexpr int kMinTiles = 2;                         // tiles of a split at least
 constexpr float kSlack = 8.f;  // growth of the running maximum that is left alone, base-2 units
 
 struct PromptParams {
     PromptArgs a;
-    int G;
+    PromptWork w;
+    int G, nsplit, slots;
     float c;  // scale * log2(e)
 };
 
@@ -50,20 +57,21 @@ struct KeyTile {
     __device__ static __forceinline__ int v_swizzle(int r) { return (((r & 3) / PER) * 4) & (SW - 1); }
 };
 
-template <int D, int NW>
+template <int D>
 struct PromptShape {
     using S = KeyTile<D>;
-    static constexpr int NT = 64 * NW;
-    static constexpr int QB = 32 * NW;
+    static constexpr int NW = kPromptWaves, NT = 64 * NW;
+    static constexpr int QB = kPromptQueries;
     static constexpr int LPT = kKeys * S::CPR / NT;          // loads a thread issues for K (and for V)
     static constexpr int LDS = 4 * S::BYTES;                  // two K tiles, two V tiles
-    static constexpr int EU = D >= 256 || NW < 4 ? 1 : 2;
+    static constexpr int EU = D >= 256 ? 1 : 2;  // waves a SIMD
     static_assert(LPT * NT == kKeys * S::CPR && LDS <= 160 * 1024, "tile loads");
 };
 
-template <typename T, int D, int NW>
-__global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kernel(PromptParams p) {
-    using SH = PromptShape<D, NW>;
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_kernel(PromptParams p) {
+    using SH = PromptShape<D>;
+    constexpr int NW = SH::NW;
     using S = KeyTile<D>;
     using V8 = typename T::V8;
     using E = typename T::E;
@@ -75,8 +83,9 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int n = lane & 31, h = lane >> 5;
     const uint32_t lds0 = lds_addr(lds);
-    const int kvh = blockIdx.x % a.n_kv_heads;
-    const int slot = int(gridDim.x / a.n_kv_heads) - 1 - int(blockIdx.x / a.n_kv_heads);
+    const int split = blockIdx.x % p.nsplit, unit = blockIdx.x / p.nsplit;
+    const int kvh = unit % a.n_kv_heads;
+    const int slot = p.slots - 1 - unit / a.n_kv_heads;
 
     // ---- the sequence and query block of this slot -----------------------
     // sequence b owns the slots from floor(off_b G / QB) + b on: enough for its
@@ -107,9 +116,12 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     }
     __syncthreads();
     const int block = uniform(found[0]), q0 = uniform(found[1]), rows = uniform(found[2]);
-    const int k0 = uniform(found[3]), L = uniform(found[4]);
+    int k0 = uniform(found[3]), L = uniform(found[4]);
     const int nq = rows * p.G;
-    if (block < 0 || rows <= 0 || (long long)block * SH::QB >= nq) return;
+    if (block < 0 || rows <= 0 || (long long)block * SH::QB >= nq) {
+        if (p.nsplit > 1 && split == 0 && tid == 0) p.w.meta[unit] = make_int4(0, 0, 0, 0);
+        return;
+    }
     const int past = L - rows;
     auto limit_of = [&](int row) __device__ { return a.causal ? max(min(L, past + row + 1), 0) : L; };
 
@@ -117,20 +129,29 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     const int wq0 = block * SH::QB + wave * 32;
     const int qi = wq0 + n;
     const int qrow = min(qi, nq - 1) / p.G, qhead = min(qi, nq - 1) - qrow * p.G;
-    const int lim = qi < nq ? limit_of(qrow) : 0;
     const int wlast = min(wq0 + 31, nq - 1);
-    const int wmin = uniform(wq0 < nq ? limit_of(wq0 / p.G) : 0);
-    const int wmax = uniform(wq0 < nq ? limit_of(wlast / p.G) : 0);
     const int glast = min(block * SH::QB + SH::QB - 1, nq - 1);
-    const int gmax = uniform(limit_of(glast / p.G));
-    const int ntile = (gmax + kKeys - 1) / kKeys;
+    const int tiles = (uniform(limit_of(glast / p.G)) + kKeys - 1) / kKeys;  // that any query of the workgroup sees
+    // this split's tiles; from here on keys count from its first
+    const int per = max((tiles + p.nsplit - 1) / p.nsplit, p.nsplit > 1 ? kMinTiles : 0);
+    const int parts = p.nsplit > 1 && per < tiles ? (tiles + per - 1) / per : 1;
+    if (p.nsplit > 1 && split == 0 && tid == 0) p.w.meta[unit] = make_int4(parts, q0, nq, block);
+    if (split >= parts) return;
+    const int t0 = parts > 1 ? split * per * kKeys : 0;
+    const int ntile = parts > 1 ? min(per, tiles - split * per) : tiles;
+    k0 += t0;
+    const int lim = (qi < nq ? limit_of(qrow) : 0) - t0;
+    const int wmin = uniform(wq0 < nq ? limit_of(wq0 / p.G) : 0) - t0;
+    const int wmax = uniform(wq0 < nq ? limit_of(wlast / p.G) : 0) - t0;
+    const int gmin = uniform(limit_of(block * SH::QB / p.G)) - t0;
+    L -= t0;
 
     // ---- loads of a tile ---------------------------------------------------
     const uint32_t kst = uint32_t(a.k_stride * 2), vst = uint32_t(a.v_stride * 2);
-    // load j of a thread covers row j * RPL further down; where that is a whole
-    // period of the swizzles one offset serves them all
+    // load j of a thread covers row j * RPL further down; the swizzles repeat
+    // every 16 rows, so OFFS offsets serve all loads
     constexpr int RPL = SH::NT / S::CPR;
-    constexpr int OFFS = RPL % 16 == 0 ? 1 : SH::LPT;
+    constexpr int OFFS = RPL >= 16 ? 1 : 16 / RPL;
     uint32_t koff[OFFS], voff[OFFS];
 #pragma unroll
     for (int j = 0; j < OFFS; ++j) {
@@ -144,8 +165,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
         if (over <= 0) {
 #pragma unroll
             for (int j = 0; j < SH::LPT; ++j)
-                dma16(uniform(dst + (j * NW + wave) * 1024), off[OFFS == 1 ? 0 : j],
-                      OFFS == 1 ? uniform(base + size_t(j * RPL) * st) : base);
+                dma16(uniform(dst + (j * NW + wave) * 1024), off[j % OFFS], uniform(base + size_t(j / OFFS * OFFS * RPL) * st));
         } else {
             // rows past the sequence repeat its last one: no query sees them
             // (offsets are unsigned, so a row's own offset is taken whole
@@ -153,7 +173,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 #pragma unroll
             for (int j = 0; j < SH::LPT; ++j) {
                 const int row = ((j * NW + wave) * 64 + lane) / S::CPR;
-                const uint32_t whole = OFFS == 1 ? off[0] + uint32_t(j * RPL) * st : off[OFFS == 1 ? 0 : j];
+                const uint32_t whole = off[j % OFFS] + uint32_t(j / OFFS * OFFS * RPL) * st;
                 dma16(uniform(dst + (j * NW + wave) * 1024), whole - uint32_t(max(row + over - (kKeys - 1), 0)) * st, base);
             }
         }
@@ -178,17 +198,37 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     }
 
     // ---- read addresses ----------------------------------------------------
-    uint32_t kread[KS];
-#pragma unroll
-    for (int k = 0; k < KS; ++k) kread[k] = n * S::RB + (((2 * k + h) ^ S::k_swizzle(n)) * 16);
-    // V^T fragment (32 channels cb, 16 tokens from row r0): rows r0 + 4 h + i and r0 + 8 + 4 h + i
+    // K fragment (32 tokens from row r0, step k): chunk 2 k + h of row r0 + n;
+    // V^T fragment (32 channels c, 16 tokens from row r0): rows r0 + 4 h + i and
+    // r0 + 8 + 4 h + i.  The swizzles are XORs of chunk bits, so a step's chunk
+    // is the first step's address with constant bits flipped.
+    const uint32_t kread = n * S::RB + ((h ^ S::k_swizzle(n)) * 16);
     const int vrow = 4 * h + ((lane >> 2) & 3);
-    uint32_t vread[CB];
+    const uint32_t vread = vrow * S::RB + (((((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1);
+    // Held in registers for every step, except at D = 256, where there is no
+    // room for them and they are made anew every tile.
+    constexpr bool HELD = D < 256;
+    uint32_t kheld[HELD ? KS : 1], vheld[HELD ? CB : 1];
+    if constexpr (HELD) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-        vread[c] = vrow * S::RB + (((4 * c + ((lane >> 4) & 1) * 2 + ((lane >> 1) & 1)) ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1);
-    auto v_frag = [&](uint32_t buf, int r0, int c) __device__ {
-        return join4<V8>(lds_read_tr16(buf + vread[c], r0 * S::RB), lds_read_tr16(buf + vread[c], (r0 + 8) * S::RB));
+        for (int k = 0; k < KS; ++k) kheld[k] = kread ^ (32 * k);
+#pragma unroll
+        for (int c = 0; c < CB; ++c) vheld[c] = vread ^ (64 * c);
+    }
+    auto base_in = [&](uint32_t buf, uint32_t first) __device__ {
+        if constexpr (HELD) return buf;
+        uint32_t x = buf + first;
+        asm volatile("" : "+v"(x));
+        return x;
+    };
+    auto k_base = [&](uint32_t buf) __device__ { return base_in(buf, kread); };
+    auto v_base = [&](uint32_t buf) __device__ { return base_in(buf, vread); };
+    auto k_frag = [&](uint32_t base, int r0, int k) __device__ {
+        return lds_read<V8>(HELD ? base + kheld[HELD ? k : 0] : base ^ (32 * k), r0 * S::RB);
+    };
+    auto v_frag = [&](uint32_t base, int r0, int c) __device__ {
+        const uint32_t at = HELD ? base + vheld[HELD ? c : 0] : base ^ (64 * c);
+        return join4<V8>(lds_read_tr16(at, r0 * S::RB), lds_read_tr16(at, (r0 + 8) * S::RB));
     };
 
     float m = kNegInf, l = 0.f;
@@ -201,13 +241,13 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     // beside them in the same instruction stream
     f32x16_t s[2];  // s[tb][r] is token 32 tb + 8 (r / 4) + 4 h + r % 4 of the tile, query n
     auto scores = [&](int j, f32x16_t *x) __device__ {
-        const uint32_t buf = lds0 + (j & 1) * S::BYTES;
+        const uint32_t kb = k_base(lds0 + (j & 1) * S::BYTES);
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) x[tb] = f32x16_t{};
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int tb = 0; tb < 2; ++tb) x[tb] = mma32(lds_read<V8>(buf + kread[k], 32 * tb * S::RB), qf[k], x[tb]);
+            for (int tb = 0; tb < 2; ++tb) x[tb] = mma32(k_frag(kb, 32 * tb, k), qf[k], x[tb]);
     };
     auto hide = [&](int j, f32x16_t *x) __device__ {
         const int t = j * kKeys;
@@ -254,7 +294,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     };
     // infinities or NaN among V rows that some queries must not see: a token at
     // a time, kept only by the queries that see it
-    auto product_by_token = [&](int t, uint32_t vbuf, const V8 *pf) __device__ {
+    auto product_by_token = [&](int t, uint32_t vb, const V8 *pf) __device__ {
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll 1
@@ -265,7 +305,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
                 asm volatile("" : : : "memory");
 #pragma unroll
                 for (int c = 0; c < CB; ++c) {
-                    u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, 16 * f, c));
+                    u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vb, 16 * f, c));
 #pragma unroll
                     for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
                     const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
@@ -274,9 +314,9 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
                 }
             }
     };
-    auto product = [&](uint32_t vbuf, const V8 *pf, int f) __device__ {
+    auto product = [&](uint32_t vb, const V8 *pf, int f) __device__ {
 #pragma unroll
-        for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vbuf, 16 * f, c), pf[f], o[c]);
+        for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vb, 16 * f, c), pf[f], o[c]);
     };
 
     if (ntile > 0) {
@@ -292,15 +332,15 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
     // reads of the steps to come, and the compiler keeps to the steps.
     auto step = [&](int jj, f32x16_t *y, f32x16_t *x) __device__ {
         turn(jj);
-        const uint32_t kbuf = lds0 + ((jj + 1) & 1) * S::BYTES, vbuf = lds0 + (2 + (jj & 1)) * S::BYTES;
+        const uint32_t kb = k_base(lds0 + ((jj + 1) & 1) * S::BYTES), vb = v_base(lds0 + (2 + (jj & 1)) * S::BYTES);
         const float ms = m == kNegInf ? 0.f : m;
         constexpr int KA = KS < 3 ? KS : 3, VA = 4;  // operands held: reads run two (K) and three (V) steps ahead
         V8 ka[KA][2], va[VA], pf[4];
         auto read_k = [&](int k) __device__ {
-            ka[k % KA][0] = lds_read<V8>(kbuf + kread[k]);
-            ka[k % KA][1] = lds_read<V8>(kbuf + kread[k], 32 * S::RB);
+            ka[k % KA][0] = k_frag(kb, 0, k);
+            ka[k % KA][1] = k_frag(kb, 32, k);
         };
-        auto read_v = [&](int i) __device__ { va[i % VA] = v_frag(vbuf, 16 * (i / CB), i % CB); };
+        auto read_v = [&](int i) __device__ { va[i % VA] = v_frag(vb, 16 * (i / CB), i % CB); };
 #pragma unroll
         for (int k = 0; k < KA - 1; ++k) read_k(k);
         x[0] = x[1] = f32x16_t{};
@@ -335,8 +375,7 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
         raise(max_x32(mx) * p.c);
     };
     // tiles whose successor, too, every query of the workgroup sees whole, then the rest
-    const int gmin = uniform(limit_of(block * SH::QB / p.G));
-    const int nfull = min(gmin / kKeys, ntile);
+    const int nfull = min(max(gmin, 0) / kKeys, ntile);
     int j = 0;
     {
         f32x16_t x[2];
@@ -378,10 +417,11 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 #pragma unroll
         for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
         if (bad) {
-            product_by_token(t, vbuf, pf);
+            product_by_token(t, v_base(vbuf), pf);
         } else {
+            const uint32_t vb = v_base(vbuf);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) product(vbuf, pf, f);
+            for (int f = 0; f < 4; ++f) product(vb, pf, f);
         }
         if (j + 1 < ntile && t + kKeys < wmax) {
             scores(j + 1, s);
@@ -392,66 +432,107 @@ __global__ __launch_bounds__(64 * NW, (PromptShape<D, NW>::EU)) void prompt_kern
 
     if (qi >= nq) return;
     l = sum_x32(l);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (parts > 1) {
+        const long long part = (long long)unit * p.nsplit + split;
+        const int q = wave * 32 + n;
+        float *dst = p.w.o + (part * SH::QB + q) * D + 4 * h;
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                *reinterpret_cast<f32x4_t *>(dst + 32 * c + 2 * r) = f32x4_t{o[c][r], o[c][r + 1], o[c][r + 2], o[c][r + 3]};
+        if (h == 0) {
+            p.w.ml[part * 2 * SH::QB + q] = m;
+            p.w.ml[part * 2 * SH::QB + SH::QB + q] = l;
+        }
+        return;
+    }
     const long long at = (long long)(q0 + qrow) * a.n_heads + kvh * p.G + qhead;
-    typedef E e4_t __attribute__((ext_vector_type(4)));
-    E *dst = static_cast<E *>(a.out) + at * D + 4 * h;
 #pragma unroll
     for (int c = 0; c < CB; ++c)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            const e4_t x = l == 0.f ? e4_t{}
-                                    : e4_t{E(o[c][r] * inv), E(o[c][r + 1] * inv), E(o[c][r + 2] * inv), E(o[c][r + 3] * inv)};
-            *reinterpret_cast<e4_t *>(dst + 32 * c + 2 * r) = x;
-        }
-    if (a.lse && h == 0) a.lse[at] = lse_of(m, l);
+        for (int r = 0; r < 16; r += 4)
+            store_row<T>(a.out, a.lse, at, 8 * c + r / 2 + h, D, f32x4_t{o[c][r], o[c][r + 1], o[c][r + 2], o[c][r + 3]}, m, l);
 }
 
-template <typename T, int D, int NW>
-hipError_t launch_prompt_typed(const PromptParams &p, hipStream_t s) {
-    const PromptArgs &a = p.a;
-    const long long slots = (long long)a.n_rows * p.G / PromptShape<D, NW>::QB + a.B;
-    launch_kernel("prompt_attention", prompt_kernel<T, D, NW>, dim3(unsigned(slots * a.n_kv_heads)), dim3(64 * NW), s, p);
-    return hipGetLastError();
+// The units whose keys were split: workgroup (unit, y) merges the partials of
+// 32 of its queries in their order, D / 4 threads a query.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p) {
+    constexpr int QB = kPromptQueries, TPQ = D / 4;
+    const int4 unit = p.w.meta[blockIdx.x];
+    const int parts = unit.x;
+    if (parts <= 1) return;
+    const int c4 = threadIdx.x % TPQ;
+    for (int q = blockIdx.y * 32 + threadIdx.x / TPQ; q < int(blockIdx.y) * 32 + 32; q += 256 / TPQ) {
+        const int qi = unit.w * QB + q;
+        if (qi >= unit.z) return;
+        float m = kNegInf, l = 0.f;
+        f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < parts; ++i) {
+            const long long part = (long long)blockIdx.x * p.nsplit + i;
+            merge_partial(m, l, o, p.w.ml[part * 2 * QB + q], p.w.ml[part * 2 * QB + QB + q],
+                          *reinterpret_cast<const f32x4_t *>(p.w.o + (part * QB + q) * D + 4 * c4));
+        }
+        const int row = qi / p.G, kvh = blockIdx.x % p.a.n_kv_heads;
+        store_row<T>(p.a.out, p.a.lse, (long long)(unit.y + row) * p.a.n_heads + kvh * p.G + (qi - row * p.G), c4, D, o, m, l);
+    }
 }
 
 template <typename T, int D>
-hipError_t launch_prompt_waves(const PromptParams &p, const PromptPlan &plan, hipStream_t s) {
-    if (plan.waves == 1) return launch_prompt_typed<T, D, 1>(p, s);
-    if (plan.waves == 2) return launch_prompt_typed<T, D, 2>(p, s);
-    return launch_prompt_typed<T, D, 4>(p, s);
+hipError_t launch_prompt_typed(const PromptParams &p, hipStream_t s) {
+    const unsigned units = unsigned(p.slots) * p.a.n_kv_heads;
+    launch_kernel("prompt_attention", prompt_kernel<T, D>, dim3(units * p.nsplit), dim3(64 * kPromptWaves), s, p);
+    if (p.nsplit > 1)
+        launch_kernel("prompt_join", prompt_join_kernel<T, D>, dim3(units, kPromptQueries / 32), dim3(256), s, p);
+    return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_prompt_dim(const PromptParams &p, const PromptPlan &plan, hipStream_t s) {
+hipError_t launch_prompt_dim(const PromptParams &p, hipStream_t s) {
     switch (p.a.head_dim) {
-        case 64: return launch_prompt_waves<T, 64>(p, plan, s);
-        case 128: return launch_prompt_waves<T, 128>(p, plan, s);
-        default: return launch_prompt_waves<T, 256>(p, plan, s);
+        case 64: return launch_prompt_typed<T, 64>(p, s);
+        case 128: return launch_prompt_typed<T, 128>(p, s);
+        default: return launch_prompt_typed<T, 256>(p, s);
     }
 }
 
 }  // namespace
 
+// Query blocks that do not fill the chip (two workgroups a compute unit) have
+// their keys split, as far as the keys go.
 PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim) {
     PromptPlan p{};
-    // wide workgroups where they still fill the chip (two a compute unit)
-    const long long queries = (long long)n_rows * n_heads;
-    p.waves = queries >= 128LL * 512 ? 4 : queries >= 64LL * 512 ? 2 : 1;
+    p.slots = int((long long)n_rows * (n_heads / n_kv_heads) / kPromptQueries + B);
+    const long long units = (long long)p.slots * n_kv_heads;
+    const long long want = units >= kPromptTarget / 2 ? 1 : (kPromptTarget + units - 1) / units;
+    const long long most = 2LL * n_kv_rows / B / (kMinTiles * kKeys);  // twice the average sequence
+    p.nsplit = int(std::max(1LL, std::min(std::min(want, most), 64LL)));
     return p;
 }
 
-PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_rows, int n_heads, int head_dim, size_t *bytes) {
-    if (bytes) *bytes = 256;
-    return PromptWork{};
+PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_kv_heads, int head_dim, size_t *bytes) {
+    Carve c(ws);
+    PromptWork w{};
+    if (p.nsplit > 1) {
+        const size_t units = size_t(p.slots) * n_kv_heads;
+        w.meta = c.take<int4>(units);
+        w.ml = c.take<float>(units * p.nsplit * 2 * kPromptQueries);
+        w.o = c.take<float>(units * p.nsplit * kPromptQueries * head_dim);
+    }
+    if (bytes) *bytes = std::max(size_t(256), (c.off + 255) & ~size_t(255));
+    return w;
 }
 
 hipError_t launch_prompt(const PromptArgs &a, const PromptPlan &plan, const PromptWork &w, hipStream_t s) {
     PromptParams p{};
     p.a = a;
+    p.w = w;
     p.G = a.n_heads / a.n_kv_heads;
+    p.nsplit = plan.nsplit;
+    p.slots = plan.slots;
     p.c = a.scale * kLog2e;
-    return a.dtype == DSPARK_BF16 ? launch_prompt_dim<TypeBf16>(p, plan, s) : launch_prompt_dim<TypeF16>(p, plan, s);
+    return a.dtype == DSPARK_BF16 ? launch_prompt_dim<TypeBf16>(p, s) : launch_prompt_dim<TypeF16>(p, s);
 }
 
 }  // namespace dspark
