@@ -153,7 +153,68 @@ __device__ __forceinline__ float sum_x16(float x) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The value again, opaque to the compiler: what is derived from it is made
+// anew here instead of being held in registers across a loop.
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// ---------------------------------------------------------------- values
+template <typename T>
+__device__ __forceinline__ float2 widen(uint32_t w) {
+    if constexpr (std::is_same<T, TypeBf16>::value) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+        const f16x2_t h = __builtin_bit_cast(f16x2_t, w);
+        return make_float2(float(h[0]), float(h[1]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void widen4(u32x2_t w, float *v) {
+    const float2 a = widen<T>(w[0]), b = widen<T>(w[1]);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+}
+// element e of fragment f of N (both may vary: selects, no memory)
+template <typename T, int N>
+__device__ __forceinline__ float element(const typename T::V8 *frag, int f, int e) {
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const u32x4v_t w = __builtin_bit_cast(u32x4v_t, frag[i]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x = f == i && (e >> 1) == q ? w[q] : x;
+    }
+    const float2 v = widen<T>(x);
+    return (e & 1) ? v.y : v.x;
+}
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin_huge_valf(); }
+// a pair of 16-bit values, and four e4m3 values, with zeros in the place of what is not finite
+template <typename T>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
+    if ((w & 0x7fffu) >= T::kInf) w &= 0xffff0000u;
+    if (((w >> 16) & 0x7fffu) >= T::kInf) w &= 0xffffu;
+    return w;
+}
+__device__ __forceinline__ uint32_t finite_e4m3(uint32_t w) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        if (((w >> i) & 0x7fu) == 0x7fu) w &= ~(0xffu << i);
+    return w;
+}
+
 // ---------------------------------------------------------------- e4m3
+__device__ __forceinline__ void e4m3_to4(uint32_t w, float *v) {
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
+    v[0] = a[0];
+    v[1] = a[1];
+    v[2] = b[0];
+    v[3] = b[1];
+}
 // Eight e4m3 values (two words) as 16-bit floats; every e4m3 value is exact in
 // both types.
 __device__ __forceinline__ void e4m3_to8(u32x2_t w, bf16x8_t &o) {

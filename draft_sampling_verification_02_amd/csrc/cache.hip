@@ -105,19 +105,6 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return e < -126 ? -126 : e;
 }
 
-// the 16-bit pattern pairs of a word as floats
-template <typename T>
-__device__ __forceinline__ float2 widen(uint32_t w);
-template <>
-__device__ __forceinline__ float2 widen<TypeBf16>(uint32_t w) {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-template <>
-__device__ __forceinline__ float2 widen<TypeF16>(uint32_t w) {
-    const f16x2_t h = __builtin_bit_cast(f16x2_t, w);
-    return make_float2(float(h[0]), float(h[1]));
-}
-
 struct Item {
     int row, head, chunk;  // row relative to the workgroup's first
     bool v;
@@ -267,16 +254,14 @@ __global__ __launch_bounds__(kCacheThreads) void kv_read_kernel(CacheParams p) {
         if (int(threadIdx.x) + j * kCacheThreads >= run.count || !inside[im[j].row]) continue;
         uint4 o = x[j];
         if constexpr (E4) {
-            typedef float f32x2_t __attribute__((ext_vector_type(2)));
-            const f32x2_t t0 = __builtin_amdgcn_cvt_pk_f32_fp8(int(x[j].x), false);
-            const f32x2_t t1 = __builtin_amdgcn_cvt_pk_f32_fp8(int(x[j].x), true);
-            const f32x2_t t2 = __builtin_amdgcn_cvt_pk_f32_fp8(int(x[j].y), false);
-            const f32x2_t t3 = __builtin_amdgcn_cvt_pk_f32_fp8(int(x[j].y), true);
+            float f[8];
+            e4m3_to4(x[j].x, f);
+            e4m3_to4(x[j].y, f + 4);
             const bool none = slots[im[j].row] < 0;  // zeros, whatever the scale
-            o.x = none ? 0u : narrow2<T>(t0[0] * sc[j], t0[1] * sc[j]);
-            o.y = none ? 0u : narrow2<T>(t1[0] * sc[j], t1[1] * sc[j]);
-            o.z = none ? 0u : narrow2<T>(t2[0] * sc[j], t2[1] * sc[j]);
-            o.w = none ? 0u : narrow2<T>(t3[0] * sc[j], t3[1] * sc[j]);
+            o.x = none ? 0u : narrow2<T>(f[0] * sc[j], f[1] * sc[j]);
+            o.y = none ? 0u : narrow2<T>(f[2] * sc[j], f[3] * sc[j]);
+            o.z = none ? 0u : narrow2<T>(f[4] * sc[j], f[5] * sc[j]);
+            o.w = none ? 0u : narrow2<T>(f[6] * sc[j], f[7] * sc[j]);
         }
         uint8_t *dst = static_cast<uint8_t *>(im[j].v ? a.v_out : a.k_out);
         *reinterpret_cast<uint4 *>(

@@ -212,32 +212,27 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
     int seg = uniform(int(rest / rq.T));      // (head, group) segment of the request
     int u0 = uniform(int(rest - (long long)seg * rq.T));
 
-    // fixed parts of the load and read addresses
-    uint32_t kvoff[S::NI], vvoff[S::NI];
-#pragma unroll
-    for (int j = 0; j < S::NI; ++j) {
-        const int slot = j * 64 + lane, row = slot / S::CPR, c = slot % S::CPR;
-        const int rin = row - j * S::RPI;  // row of the instruction
-        kvoff[j] = rin * S::RB + ((c ^ S::k_swizzle(row)) * 16);
-        vvoff[j] = rin * S::RB + ((c ^ S::v_swizzle(row)) * 16);
+    // Fixed parts of the load and read addresses.  The swizzles are XORs of
+    // chunk bits with row bits, so load j's offset is the first load's with
+    // constant bits flipped, and so is a step's read address; they are made
+    // anew where they are used, as registers are short.
+    uint32_t kload, vload;
+    {
+        const int rin = lane / S::CPR, c = lane % S::CPR;  // row of the load, chunk
+        kload = rin * S::RB + ((c ^ S::k_swizzle(rin)) * 16);
+        vload = rin * S::RB + ((c ^ S::v_swizzle(rin)) * 16);
     }
-
-    // where the wave's lanes read a tile
-    uint32_t kread[KSTEP], vread[2];
-#pragma unroll
-    for (int k = 0; k < KSTEP; ++k) kread[k] = n * S::RB + (((4 * k + g) ^ S::k_swizzle(n)) * 16);
+    const uint32_t kread = n * S::RB + ((g ^ S::k_swizzle(n)) * 16);
     // transposing reads: 16-bit, row 4 g + i of a half; 8-bit, rows 4 g + i of both halves
     const int vrow = E4 ? ((lane >> 1) & 3) + 4 * g + ((lane & 8) ? 16 : 0) : 4 * g + ((lane >> 2) & 3);
-    vread[0] = vrow * S::RB;
-    vread[1] = (vrow + 16) * S::RB;
-    auto v_frag = [&](uint32_t buf, int cb) __device__ {
+    const uint32_t vread = vrow * S::RB + (((E4 ? 0 : (lane >> 1) & 1) ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1);
+    auto v_frag = [&](uint32_t base, int cb) __device__ {
         if constexpr (E4) {
             P8 f;
-            e4m3_to8(lds_read_tr8(buf + vread[0] + ((cb ^ S::v_swizzle(vrow)) * 16) + 8 * (lane & 1)), f);
+            e4m3_to8(lds_read_tr8(base ^ (16 * cb)), f);
             return f;
         } else {
-            const uint32_t c = uint32_t(((2 * cb + ((lane >> 1) & 1)) ^ S::v_swizzle(vrow)) * 16 + 8 * (lane & 1));
-            return join4<P8>(lds_read_tr16(buf + vread[0] + c), lds_read_tr16(buf + vread[1] + c));
+            return join4<P8>(lds_read_tr16(base ^ (32 * cb)), lds_read_tr16(base ^ (32 * cb), 16 * S::RB));
         }
     };
 
@@ -262,19 +257,19 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
         auto row_of = [&](int page, int t) __device__ {
             return (((long long)(bad_page(page) ? 0 : page) * a.n_kv_heads + h) << p.pshift) + (t & pmask);
         };
-        auto issue = [&](const void *cache, const uint32_t *off, uint32_t dst, int t, int pa, int pb) __device__ {
+        auto issue = [&](const void *cache, auto swizzle, uint32_t off, uint32_t dst, int t, int pa, int pb) __device__ {
             const uint8_t *ba = static_cast<const uint8_t *>(cache) + row_of(pa, t) * S::RB;
             const uint8_t *bb = static_cast<const uint8_t *>(cache) + row_of(pb, t + 16) * S::RB;
 #pragma unroll
             for (int j = 0; j < S::NI; ++j) {
                 const int row = j * S::RPI;  // first row of the load; a load stays in one half, so in one page
-                dma16(dst + j * 1024, off[j], uniform((row < 16 ? ba : bb) + (row & 15) * S::RB));
+                dma16(dst + j * 1024, off ^ (swizzle(row) * 16), uniform((row < 16 ? ba : bb) + (row & 15) * S::RB));
             }
         };
         auto issue_k = [&](int i, int pa, int pb) __device__ {
             const int t = tile_at(i);
             const uint32_t dst = uniform(ring + (i % NS) * SH::STAGE);
-            issue(a.k_cache, kvoff, dst, t, pa, pb);
+            issue(a.k_cache, S::k_swizzle, fresh(kload), dst, t, pa, pb);
             if constexpr (E4) {
                 // bytes 0-31: K scales of the tokens, 32-63: V scales (lane i brings 4 bytes; lanes past 15 repeat)
                 const uint8_t *sc = (lane & 8) ? a.v_scale : a.k_scale;
@@ -282,7 +277,7 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
             }
         };
         auto issue_v = [&](int i, int pa, int pb) __device__ {
-            issue(a.v_cache, vvoff, uniform(ring + (i % NS) * SH::STAGE + S::BYTES), tile_at(i), pa, pb);
+            issue(a.v_cache, S::v_swizzle, fresh(vload), uniform(ring + (i % NS) * SH::STAGE + S::BYTES), tile_at(i), pa, pb);
         };
 
         // ---- queries into LDS (the workgroup's waves share them), first tiles
@@ -356,6 +351,7 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
                 vm_wait<SH::FLY>();
             else
                 vm_wait<0>();
+            const uint32_t kbase = fresh(buf + kread);
             f32x4_t s[NQ][2];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -363,7 +359,7 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
                 for (int q = 0; q < NQ; ++q) s[q][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < KSTEP; ++k) {
-                    const u32x4v_t x = lds_read<u32x4v_t>(buf + 16 * hf * S::RB + kread[k]);
+                    const u32x4v_t x = lds_read<u32x4v_t>(kbase ^ (64 * k), 16 * hf * S::RB);
                     if constexpr (E4) {
                         V8 lo, hi;
                         e4m3_to8(u32x2_t{x[0], x[1]}, lo);
@@ -447,50 +443,67 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
             else
                 vm_wait<0>();
             const uint32_t vbuf = buf + S::BYTES;
-            bool slow = false;
+            const uint32_t vbase = fresh(vbuf + vread);
             if (masked) {
                 // rows that no query sees (past the request's end, pages outside the cache) may hold anything
+#pragma unroll 1
                 for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
                     const int row = slot / S::CPR;
                     if (t + row >= rq.L || ((bad_now >> (row >> 4)) & 1)) lds_write(vbuf + slot * 16, u32x4v_t{0, 0, 0, 0});
                 }
                 lds_drain();
-                // a row that some queries see and others must not: harmless where it is finite, as the others'
-                // probabilities are zero; 0 * v tells
+                // A row that some queries see and others must not is harmless where it is finite, as the others'
+                // probabilities are zero; 0 * v tells.  What is not finite is taken out of the tile: the queries
+                // that see it get their share of it here.
                 if (t + kTokens > lim_min && lim_min < rq.L) {
                     const P8 zero = {};
                     f32x4_t z = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbuf, c), zero, z);
-                    slow = __any(!(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f));
-                }
-            }
-            if (!slow) {
-#pragma unroll
-                for (int c = 0; c < CB; ++c) {
-                    const P8 vf = v_frag(vbuf, c);
-#pragma unroll
-                    for (int q = 0; q < NQ; ++q) o[q][c] = mma16(vf, pf[q], o[q][c]);
-                }
-            } else {
-                // infinities or NaN in such a row: a token at a time, kept only by the queries that see it
+                    for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbase, c), zero, z);
+                    if (__any(!(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f))) {
 #pragma unroll 1
-                for (int k = 0; k < kTokens; ++k) {
-                    const int e = (k & 3) + 4 * (k >> 4), tok = t + k;  // token k is element e of lane group (k / 4) % 4
-                    const uint32_t keep = g == ((k >> 2) & 3) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
-                    asm volatile("" : : : "memory");  // the fragments are read again: no registers held for them
+                        for (int k = 0; k < kTokens; ++k) {
+                            // token k is element e of lane group (k / 4) % 4; the lane holds channels 16 c + 4 g ..
+                            const int e = (k & 3) + 4 * (k >> 4), from = ((k >> 2) & 3) * 16 + n;
+                            const uint32_t row = vbuf + k * S::RB + (E4 ? 4 * g : 8 * (g & 1));
+                            const int sw = S::v_swizzle(k);
 #pragma unroll
-                    for (int c = 0; c < CB; ++c) {
-                        u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vbuf, c));
+                            for (int q = 0; q < NQ; ++q) {
+                                const float pk = __shfl(element<PT, 1>(&pf[q], 0, e), from);
+                                const bool sees = t + k < lim[q];
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
+                                for (int c = 0; c < CB; ++c) {
+                                    asm volatile("" : : : "memory");  // read four values at a time: registers are short
+                                    float v[4];
+                                    if constexpr (E4)
+                                        e4m3_to4(lds_read<uint32_t>(row + ((c ^ sw) * 16)), v);
+                                    else
+                                        widen4<T>(lds_read<u32x2_t>(row + (((2 * c + (g >> 1)) ^ sw) * 16)), v);
+                                    if (__any(sees && !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3])))) {
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            const f32x4_t with = mma16(__builtin_bit_cast(P8, one), pf[q], o[q][c]);
-                            if (tok < lim[q]) o[q][c] = with;
+                                        for (int r = 0; r < 4; ++r)
+                                            o[q][c][r] += sees && !is_finite(v[r]) ? pk * v[r] : 0.f;
+                                    }
+                                }
+                            }
                         }
+                        lds_drain();
+#pragma unroll 1
+                        for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
+                            u32x4v_t w = lds_read<u32x4v_t>(vbuf + slot * 16);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) w[x] = E4 ? finite_e4m3(w[x]) : finite_pair<T>(w[x]);
+                            lds_write(vbuf + slot * 16, w);
+                        }
+                        lds_drain();
                     }
                 }
+            }
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+                const P8 vf = v_frag(vbase, c);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) o[q][c] = mma16(vf, pf[q], o[q][c]);
             }
             lds_drain();
             if (more) issue_v(i + NS, pa, pb);

@@ -292,27 +292,39 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         if (j + 2 < ntile) issue_k(j + 2);
         if (j + 1 < ntile) issue_v(j + 1);
     };
-    // infinities or NaN among V rows that some queries must not see: a token at
-    // a time, kept only by the queries that see it
-    auto product_by_token = [&](int t, uint32_t vb, const V8 *pf) __device__ {
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
+    // Infinities or NaN among V rows that some queries must not see: the queries
+    // that see them get their share here, then they leave the tile.  Every wave
+    // of the workgroup comes here.
+    auto take_out_bad = [&](int t, uint32_t vbuf, const V8 *pf) __device__ {
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-                // token 16 f + k is element e of lane half (k / 4) % 2
-                const int e = (k & 3) + 4 * (k >> 3), tok = t + 16 * f + k;
-                const uint32_t keep = h == ((k >> 2) & 1) ? ((e & 1) ? 0xffff0000u : 0xffffu) : 0u;
-                asm volatile("" : : : "memory");
+        for (int k = 0; k < kKeys; ++k) {
+            // token k is element e of fragment k / 16, lane half (k / 4) % 2;
+            // the lane holds channels 32 c + 8 i + 4 h .. + 3
+            const int e = (k & 3) + 4 * ((k >> 3) & 1), sw = S::v_swizzle(k);
+            const float pk = __shfl(element<T, 4>(pf, k >> 4, e), n + 32 * ((k >> 2) & 1));
+            const bool sees = t + k < lim;
 #pragma unroll
-                for (int c = 0; c < CB; ++c) {
-                    u32x4v_t one = __builtin_bit_cast(u32x4v_t, v_frag(vb, 16 * f, c));
+            for (int c = 0; c < CB; ++c)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) one[w] &= (e >> 1) == w ? keep : 0u;
-                    const f32x16_t with = mma32(__builtin_bit_cast(V8, one), pf[f], o[c]);
+                for (int i = 0; i < 4; ++i) {
+                    asm volatile("" : : : "memory");  // read four values at a time: registers are short
+                    float v[4];
+                    widen4<T>(lds_read<u32x2_t>(vbuf + k * S::RB + (((4 * c + i) ^ sw) * 16) + 8 * h), v);
+                    if (__any(sees && !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3])))) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) o[c][r] = tok < lim ? with[r] : o[c][r];
+                        for (int r = 0; r < 4; ++r) o[c][4 * i + r] += sees && !is_finite(v[r]) ? pk * v[r] : 0.f;
+                    }
                 }
-            }
+        }
+        wg_barrier();
+#pragma unroll 1
+        for (int i = tid; i < kKeys * S::CPR; i += SH::NT) {
+            u32x4v_t w = lds_read<u32x4v_t>(vbuf + i * 16);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = finite_pair<T>(w[q]);
+            lds_write(vbuf + i * 16, w);
+        }
+        wg_barrier();
     };
     auto product = [&](uint32_t vb, const V8 *pf, int f) __device__ {
 #pragma unroll
@@ -411,18 +423,16 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             wg_barrier();
             bad = found_bad == j + 1;
         }
-        if (t >= wmax) continue;
+        if (t >= wmax && !bad) continue;
         const float ms = m == kNegInf ? 0.f : m;
         V8 pf[4];
 #pragma unroll
         for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
-        if (bad) {
-            product_by_token(t, v_base(vbuf), pf);
-        } else {
-            const uint32_t vb = v_base(vbuf);
+        if (bad) take_out_bad(t, vbuf, pf);
+        if (t >= wmax) continue;
+        const uint32_t vb = v_base(vbuf);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) product(vb, pf, f);
-        }
+        for (int f = 0; f < 4; ++f) product(vb, pf, f);
         if (j + 1 < ntile && t + kKeys < wmax) {
             scores(j + 1, s);
             hide(j + 1, s);
