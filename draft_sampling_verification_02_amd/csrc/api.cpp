@@ -718,7 +718,11 @@ int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_sc
 size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim) {
     if (max_rows < 1 || head_geometry(0, n_heads, n_kv_heads) != DSPARK_OK || !head_dim_supported(head_dim)) return 0;
     size_t bytes = 0;
-    paged_carve(nullptr, paged_plan(max_rows, n_heads, n_kv_heads, head_dim, 0), head_dim, &bytes);
+    for (const bool e4 : {false, true}) {
+        size_t need = 0;
+        paged_carve(nullptr, paged_plan(max_rows, n_heads, n_kv_heads, head_dim, e4, 0), head_dim, &need);
+        bytes = need > bytes ? need : bytes;
+    }
     return bytes;
 }
 
@@ -739,7 +743,8 @@ int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int
     if (!row_stride_ok(q_stride, n_heads, head_dim)) return DSPARK_ERR_ARG;
     st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
     if (st != DSPARK_OK) return st;
-    const PagedPlan plan = paged_plan(max_rows, n_heads, n_kv_heads, head_dim, (long long)max_pages * page_size);
+    const PagedPlan plan = paged_plan(max_rows, n_heads, n_kv_heads, head_dim, cache_dtype == DSPARK_E4M3,
+                                      (long long)max_pages * page_size);
     size_t need = 0;
     paged_carve(nullptr, plan, head_dim, &need);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;

@@ -38,7 +38,6 @@ constexpr int kPagedThreads = 64 * kPagedWaves;
 constexpr int kTokens = 32;                          // tokens of a wave's tile
 constexpr int kUnit = kTokens * kPagedWaves;         // tokens of a work unit
 constexpr int kMinUnits = 2;                         // units a workgroup takes at least
-constexpr int kPagedGrid = 512;                      // two workgroups a compute unit
 constexpr int kWholeTokens = 512;                    // tables up to this long are not split
 
 typedef __attribute__((address_space(4))) const int32_t *ConstInts;  // read by scalar loads
@@ -117,24 +116,40 @@ struct ProbType<T, true> {
     using type = TypeBf16;
 };
 
+#ifndef PNS
+#define PNS 1
+#endif
+// LDS of a workgroup and how many share a compute unit.
+constexpr int paged_row(bool e4, int d) { return e4 ? d : 2 * d; }
+constexpr int paged_stages(bool e4, int d) { return paged_row(e4, d) >= 512 ? 1 : PNS; }
+constexpr int paged_body(bool e4, int d, int nq) {
+    const int ring = kPagedWaves * paged_stages(e4, d) * (2 * kTokens * paged_row(e4, d) + (e4 ? 256 : 0));
+    const int join = kPagedWaves * 16 * nq * (d + 6) * 4;
+    return ring > join ? ring : join;
+}
+constexpr int paged_per_cu(bool e4, int d, int nq) {
+    const int fit = 163840 / (paged_body(e4, d, nq) + 16 * nq * d * 2 + 64);
+    const int most = nq == 1 && d <= 128 ? 3 : (nq <= 2 && d <= 128) || (nq == 4 && d == 64) ? 2 : 1;  // by registers
+    return fit < most ? fit : most;
+}
+
 template <typename T, bool E4, int D, int NQ>
 struct PagedShape {
     using S = TileShape<E4, D>;
     static constexpr int QB = 16 * NQ;
-    static constexpr int NS = S::RB >= 512 ? 1 : 2;                 // tiles in the ring
+    static constexpr int NS = paged_stages(E4, D);                  // tiles in the ring
     static constexpr int SCALE = E4 ? 256 : 0;                      // a tile's scales
     static constexpr int STAGE = 2 * S::BYTES + SCALE;
     static constexpr int RING = NS * STAGE;                         // bytes of a wave
     static constexpr int OROW = D + 4;                              // padded floats of a joined row
-    static constexpr int JOIN = kPagedWaves * QB * (OROW + 2) * 4;  // the waves' results
     static constexpr int QBYTES = QB * D * 2;
-    static constexpr int BODY = RING * kPagedWaves > JOIN ? RING * kPagedWaves : JOIN;
+    static constexpr int BODY = paged_body(E4, D, NQ);              // the rings, or the waves' results to be joined
     static constexpr int LDS = BODY + QBYTES;
     static constexpr int KL = S::NI + (E4 ? 1 : 0);  // loads of a tile's K (and scales)
     static constexpr int VL = S::NI;
     static constexpr int FLY = (NS - 1) * (KL + VL) + VL;  // loads younger than a tile's K when it is taken
     static constexpr int FLYV = (NS - 1) * (KL + VL) + KL; // and than its V, K being refilled
-    static constexpr int PER_CU = LDS <= 80 * 1024 ? 2 : 1;
+    static constexpr int PER_CU = paged_per_cu(E4, D, NQ);
     static_assert(LDS <= 160 * 1024, "LDS of a workgroup");
 };
 
@@ -643,12 +658,12 @@ hipError_t launch_paged_dim(const PagedParams &pp, const PagedPlan &plan, hipStr
 // The query blocks cover a request's rows times its group where they fit
 // (16 to 64 queries; 32 at D = 256, whose accumulators are twice as long);
 // more rows take several groups, which read the cache again.
-PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, long long table_tokens) {
+PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long table_tokens) {
     PagedPlan p{};
     const long long queries = (long long)max_rows * (n_heads / n_kv_heads);
     const int most = head_dim >= 256 ? 2 : 4;
     p.qblocks = queries <= 16 ? 1 : (queries <= 32 || most == 2 ? 2 : 4);
-    p.grid = kPagedGrid;
+    p.grid = 256 * paged_per_cu(e4, head_dim, p.qblocks);
     p.whole = table_tokens <= kWholeTokens;
     return p;
 }
