@@ -269,11 +269,13 @@ hipError_t launch_cache(const CacheArgs &a, bool write, hipStream_t s);
 // The split of a paged attention call.
 struct PagedPlan {
     int qblocks;   // 16-query blocks a workgroup holds
+    int waves;     // of a workgroup
     int grid;      // workgroups
     int whole;     // 1: a workgroup takes whole (request, head, query group) segments, nothing to join
 };
 // table_tokens: max_pages * page_size, the longest a request can be
-PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long table_tokens);
+PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long requests,
+                     long long table_tokens);
 struct PagedWork {
     int4 *meta;       // [grid] the segment a workgroup left unfinished at its end
     float *ml;        // [2 grid, 2, queries] partial maxima and sums

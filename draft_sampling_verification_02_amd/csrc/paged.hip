@@ -33,12 +33,12 @@ namespace dspark {
 
 namespace {
 
-constexpr int kPagedWaves = 4;
-constexpr int kPagedThreads = 64 * kPagedWaves;
-constexpr int kTokens = 32;                          // tokens of a wave's tile
-constexpr int kUnit = kTokens * kPagedWaves;         // tokens of a work unit
-constexpr int kMinUnits = 2;                         // units a workgroup takes at least
-constexpr int kWholeTokens = 512;                    // tables up to this long are not split
+constexpr int kTokens = 32;       // tokens of a wave's tile
+constexpr int kUnit = 128;        // tokens of a work unit: a tile for each of four waves
+constexpr int kMinUnits = 2;      // units a workgroup takes at least
+constexpr int kWholeTokens = 512;   // tables up to this long are not split,
+constexpr int kWideTokens = 1024;   // nor up to this by eight waves a segment
+constexpr int kJoinQueries = 4;   // queries of a join workgroup
 
 typedef __attribute__((address_space(4))) const int32_t *ConstInts;  // read by scalar loads
 
@@ -46,7 +46,8 @@ struct PagedParams {
     PagedArgs a;
     PagedWork w;
     int G, pshift, whole;
-    float c;  // scale * log2(e)
+    int unit;  // tokens of a work unit
+    float c;   // scale * log2(e)
 };
 
 struct Request {
@@ -72,12 +73,11 @@ __device__ __forceinline__ Request request_of(const PagedParams &p, int b) {
     const long long cap = (long long)a.max_pages << p.pshift;
     r.L = r.past < 0 ? 0 : int(min((long long)r.past + r.rows, cap));
     r.groups = (r.rows * p.G + QB - 1) / QB;
-    r.T = p.whole ? 1 : max(1, (r.L + kUnit - 1) / kUnit);
+    r.T = p.whole ? 1 : max(1, (r.L + p.unit - 1) / p.unit);
     return r;
 }
-__device__ __forceinline__ long long cost_of(const PagedParams &p, const Request &r) {
-    return (long long)r.groups * p.a.n_kv_heads * r.T;
-}
+// its units, over all heads and groups (the unit is chosen so that all fit 31 bits)
+__device__ __forceinline__ int cost_of(const PagedParams &p, const Request &r) { return r.groups * p.a.n_kv_heads * r.T; }
 
 // Layout of a wave's LDS tiles: rows of RB bytes in CPR chunks of 16, chunk c
 // of row r at c ^ k_swizzle(r) (K) or c ^ v_swizzle(r) (V).  K is read 16 rows
@@ -116,57 +116,51 @@ struct ProbType<T, true> {
     using type = TypeBf16;
 };
 
-#ifndef PNS
-#define PNS 1
-#endif
-// LDS of a workgroup and how many share a compute unit.
-constexpr int paged_row(bool e4, int d) { return e4 ? d : 2 * d; }
-constexpr int paged_stages(bool e4, int d) { return paged_row(e4, d) >= 512 ? 1 : PNS; }
-constexpr int paged_body(bool e4, int d, int nq) {
-    const int ring = kPagedWaves * paged_stages(e4, d) * (2 * kTokens * paged_row(e4, d) + (e4 ? 256 : 0));
-    const int join = kPagedWaves * 16 * nq * (d + 6) * 4;
+// LDS of a workgroup of nw waves and how many share a compute unit.
+constexpr int paged_body(bool e4, int d, int nq, int nw) {
+    const int ring = nw * (2 * kTokens * (e4 ? d : 2 * d) + (e4 ? 256 : 0));
+    const int join = nw * 16 * nq * (d + 6) * 4;
     return ring > join ? ring : join;
 }
-constexpr int paged_per_cu(bool e4, int d, int nq) {
-    const int fit = 163840 / (paged_body(e4, d, nq) + 16 * nq * d * 2 + 64);
-    const int most = nq == 1 && d <= 128 ? 3 : (nq <= 2 && d <= 128) || (nq == 4 && d == 64) ? 2 : 1;  // by registers
+constexpr int paged_per_cu(bool e4, int d, int nq, int nw) {
+    const int fit = 163840 / (paged_body(e4, d, nq, nw) + 16 * nq * d * 2 + 128);
+    const int eu = nq == 1 && d <= 128 ? 3 : (nq <= 2 && d <= 128) || (nq == 4 && d == 64) ? 2 : 1;  // waves a SIMD, by registers
+    const int most = eu * 4 / nw;
     return fit < most ? fit : most;
 }
 
-template <typename T, bool E4, int D, int NQ>
+template <bool E4, int D, int NQ, int NW>
 struct PagedShape {
     using S = TileShape<E4, D>;
     static constexpr int QB = 16 * NQ;
-    static constexpr int NS = paged_stages(E4, D);                  // tiles in the ring
-    static constexpr int SCALE = E4 ? 256 : 0;                      // a tile's scales
-    static constexpr int STAGE = 2 * S::BYTES + SCALE;
-    static constexpr int RING = NS * STAGE;                         // bytes of a wave
-    static constexpr int OROW = D + 4;                              // padded floats of a joined row
+    static constexpr int SCALE = E4 ? 256 : 0;                // a tile's scales
+    static constexpr int RING = 2 * S::BYTES + SCALE;         // bytes of a wave: K tile, V tile, scales
+    static constexpr int OROW = D + 4;                        // padded floats of a joined row
     static constexpr int QBYTES = QB * D * 2;
-    static constexpr int BODY = paged_body(E4, D, NQ);              // the rings, or the waves' results to be joined
+    static constexpr int BODY = paged_body(E4, D, NQ, NW);    // the waves' tiles, or their results to be joined
     static constexpr int LDS = BODY + QBYTES;
-    static constexpr int KL = S::NI + (E4 ? 1 : 0);  // loads of a tile's K (and scales)
+    static constexpr int KL = S::NI + (E4 ? 1 : 0);           // loads of a tile's K (and scales)
     static constexpr int VL = S::NI;
-    static constexpr int FLY = (NS - 1) * (KL + VL) + VL;  // loads younger than a tile's K when it is taken
-    static constexpr int FLYV = (NS - 1) * (KL + VL) + KL; // and than its V, K being refilled
-    static constexpr int PER_CU = paged_per_cu(E4, D, NQ);
+    static constexpr int PER_CU = paged_per_cu(E4, D, NQ, NW);
+    static constexpr int EU = PER_CU * NW / 4;                // waves a SIMD
+    static_assert(PER_CU >= 1, "a workgroup fits a compute unit");
     static_assert(LDS <= 160 * 1024, "LDS of a workgroup");
 };
 
-template <typename T, bool E4, int D, int NQ>
-__global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) void paged_kernel(PagedParams p) {
-    using SH = PagedShape<T, E4, D, NQ>;
+template <typename T, bool E4, int D, int NQ, int NW>
+__global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void paged_kernel(PagedParams p) {
+    using SH = PagedShape<E4, D, NQ, NW>;
+    constexpr int NT = 64 * NW;
     using S = TileShape<E4, D>;
     using V8 = typename T::V8;
     using PT = typename ProbType<T, E4>::type;
     using P8 = typename PT::V8;
     using QS = TileShape<false, D>;  // query rows in LDS are laid out as 16-bit K rows
-    constexpr int QB = SH::QB, NS = SH::NS, KS = D / 32, CB = D / 16;
+    constexpr int QB = SH::QB, KS = D / 32, CB = D / 16;
     constexpr int KSTEP = S::RB / 64;  // 16-byte chunks of a K row a lane reads
     __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
-    __shared__ long long scan[kPagedWaves];
-    __shared__ long long found[2];
-    __shared__ int found_b;
+    __shared__ int scan[NW];
+    __shared__ int found[8];
 
     const PagedArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -175,57 +169,73 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
     const uint32_t ring = lds0 + wave * SH::RING;
     const uint32_t qlds = lds0 + SH::BODY;
 
-    // ---- this workgroup's range of units --------------------------------
-    long long total = 0;
-    long long mine = 0;  // with B <= kPagedThreads: the cost of request tid
-    for (int b = tid; b < a.B; b += kPagedThreads) {
-        mine = cost_of(p, request_of<QB>(p, b));
-        total += mine;
+    // ---- this workgroup's range of units, and the request it starts in -----
+    // (one round of loads where a thread has one request)
+    Request rq{};
+    int mine = 0, all = 0;
+    for (int i = tid; i < a.B; i += NT) {
+        rq = request_of<QB>(p, i);
+        mine = cost_of(p, rq);
+        all += mine;
     }
+    auto total_of = [&](int x) __device__ {  // over the workgroup; inclusive sums of x stay in `inc`
+        int inc = x;
 #pragma unroll
-    for (int s = 32; s >= 1; s >>= 1) total += __shfl_xor(total, s);
-    if (lane == 0) scan[wave] = total;
-    __syncthreads();
-    total = scan[0] + scan[1] + scan[2] + scan[3];
-    const long long min_units = p.whole ? 1 : kMinUnits;
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, min_units);
-    const long long begin = (long long)blockIdx.x * per;
-    const long long end = min(begin + per, total);
-    if (tid == 0 && !p.whole) p.w.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (begin >= end) return;
-    // the request `begin` falls in
-    {
-        long long before = 0;  // cost of the requests before this chunk
-        for (int b0 = 0; b0 < a.B; b0 += kPagedThreads) {
-            const int b = b0 + tid;
-            const long long cost = a.B <= kPagedThreads ? mine : (b < a.B ? cost_of(p, request_of<QB>(p, b)) : 0);
-            long long inc = cost;
-#pragma unroll
-            for (int s = 1; s < 64; s <<= 1) {
-                const long long up = __shfl_up(inc, s);
-                if (lane >= s) inc += up;
-            }
-            __syncthreads();
-            if (lane == 63) scan[wave] = inc;
-            __syncthreads();
-            for (int w = 0; w < wave; ++w) inc += scan[w];
-            const long long chunk = scan[0] + scan[1] + scan[2] + scan[3];
-            inc += before;
-            if (b < a.B && begin < inc && begin >= inc - cost) {
-                found_b = b;
-                found[0] = inc - cost;
-            }
-            before += chunk;
-            if (begin < before) break;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(inc, d);
+            if (lane >= d) inc += up;
         }
         __syncthreads();
+        if (lane == 63) scan[wave] = inc;
+        __syncthreads();
+        int sum = 0;
+        for (int w = 0; w < NW; ++w) {
+            if (w == wave) inc += sum;
+            sum += scan[w];
+        }
+        return make_int2(inc, sum);
+    };
+    int2 sums = total_of(all);
+    const int total = uniform(sums.y);
+    const int per = max(int((unsigned(total) + gridDim.x - 1) / gridDim.x), p.whole ? 1 : kMinUnits);
+    const int begin = int(min((long long)blockIdx.x * per, (long long)total)), end = int(min((long long)begin + per, (long long)total));
+    if (tid == 0 && !p.whole) p.w.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (begin < 0 || begin >= end) return;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    int before = 0;  // units of the requests before this chunk of NT
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
+        const int i = b0 + tid;
+        if (a.B > NT) {
+            mine = 0;
+            if (i < a.B) {
+                rq = request_of<QB>(p, i);
+                mine = cost_of(p, rq);
+            }
+            sums = total_of(mine);
+        }
+        const int past_it = before + sums.x;
+        if (i < a.B && begin < past_it && begin >= past_it - mine) {
+            found[0] = i;
+            found[1] = past_it - mine;
+            found[2] = rq.row0;
+            found[3] = rq.rows;
+            found[4] = rq.past;
+            found[5] = rq.L;
+            found[6] = rq.groups;
+            found[7] = rq.T;
+        }
+        before += sums.y;
+        if (begin < before) break;
     }
-    int b = uniform(found_b);
-    Request rq = request_of<QB>(p, b);
-    long long at = begin;
-    const long long rest = begin - found[0];  // units into the request
-    int seg = uniform(int(rest / rq.T));      // (head, group) segment of the request
-    int u0 = uniform(int(rest - (long long)seg * rq.T));
+    __syncthreads();
+    int b = uniform(found[0]);
+    if (b < 0) return;
+    rq = Request{uniform(found[2]), uniform(found[3]), uniform(found[4]), uniform(found[5]), uniform(found[6]), uniform(found[7])};
+    int at = begin;
+    const int rest = begin - uniform(found[1]);      // units into the request
+    int seg = uniform(int(unsigned(rest) / unsigned(rq.T)));  // (head, group) segment of the request
+    int u0 = rest - seg * rq.T;
 
     // Fixed parts of the load and read addresses.  The swizzles are XORs of
     // chunk bits with row bits, so load j's offset is the first load's with
@@ -254,17 +264,17 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
     while (at < end) {
         // ---- one segment: query group grp of head h of request b ---------
         const int h = uniform(seg / rq.groups), grp = uniform(seg - h * rq.groups);
-        const int u1 = uniform(int(min((long long)rq.T, u0 + (end - at))));
-        const int tok0 = p.whole ? 0 : u0 * kUnit;
-        const int tok1 = p.whole ? rq.L : min(u1 * kUnit, rq.L);
+        const int u1 = uniform(min(rq.T, u0 + (end - at)));
+        const int tok0 = p.whole ? 0 : u0 * p.unit;
+        const int tok1 = p.whole ? rq.L : int(min((long long)u1 * p.unit, (long long)rq.L));
         const int nq_all = rq.rows * p.G;  // queries of the request
-        // this wave's tiles: tok0 + (wave + 4 i) * kTokens
+        // this wave's tiles: tok0 + (wave + NW i) * kTokens
         const int ntile = (max(tok1 - tok0, 0) + kTokens - 1) / kTokens;
-        const int tiles = uniform(ntile > wave ? (ntile - wave + kPagedWaves - 1) / kPagedWaves : 0);
+        const int tiles = uniform(ntile > wave ? (ntile - wave + NW - 1) / NW : 0);
         const ConstInts table = (ConstInts)(a.page_table + (long long)b * a.max_pages);
         const int pmask = (1 << p.pshift) - 1;
 
-        auto tile_at = [&](int i) __device__ { return tok0 + (wave + i * kPagedWaves) * kTokens; };
+        auto tile_at = [&](int i) __device__ { return tok0 + (wave + i * NW) * kTokens; };
         // the page of token t (the last page of the table for tokens past it: they are masked)
         auto page_of = [&](int t) __device__ { return table[min(t >> p.pshift, a.max_pages - 1)]; };
         auto bad_page = [&](int page) __device__ { return page < 0 || page >= a.n_pages; };
@@ -278,26 +288,25 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
 #pragma unroll
             for (int j = 0; j < S::NI; ++j) {
                 const int row = j * S::RPI;  // first row of the load; a load stays in one half, so in one page
-                dma16(dst + j * 1024, off ^ (swizzle(row) * 16), uniform((row < 16 ? ba : bb) + (row & 15) * S::RB));
+                dma16(uniform(dst + j * 1024), off ^ (swizzle(row) * 16), uniform((row < 16 ? ba : bb) + (row & 15) * S::RB));
             }
         };
         auto issue_k = [&](int i, int pa, int pb) __device__ {
             const int t = tile_at(i);
-            const uint32_t dst = uniform(ring + (i % NS) * SH::STAGE);
-            issue(a.k_cache, S::k_swizzle, fresh(kload), dst, t, pa, pb);
+            issue(a.k_cache, S::k_swizzle, fresh(kload), ring, t, pa, pb);
             if constexpr (E4) {
                 // bytes 0-31: K scales of the tokens, 32-63: V scales (lane i brings 4 bytes; lanes past 15 repeat)
                 const uint8_t *sc = (lane & 8) ? a.v_scale : a.k_scale;
-                dma4(uniform(dst + 2 * S::BYTES), sc + ((lane & 4) ? row_of(pb, t + 16) : row_of(pa, t)) + 4 * (lane & 3));
+                dma4(uniform(ring + 2 * S::BYTES), sc + ((lane & 4) ? row_of(pb, t + 16) : row_of(pa, t)) + 4 * (lane & 3));
             }
         };
         auto issue_v = [&](int i, int pa, int pb) __device__ {
-            issue(a.v_cache, S::v_swizzle, fresh(vload), uniform(ring + (i % NS) * SH::STAGE + S::BYTES), tile_at(i), pa, pb);
+            issue(a.v_cache, S::v_swizzle, fresh(vload), ring + S::BYTES, tile_at(i), pa, pb);
         };
 
         // ---- queries into LDS (the workgroup's waves share them), first tiles
         constexpr int QCH = D / 8;  // 16-byte chunks of a query row
-        for (int j = wave; j < SH::QBYTES / 1024; j += kPagedWaves) {
+        for (int j = wave; j < SH::QBYTES / 1024; j += NW) {
             const int slot = j * 64 + lane, row = slot / QCH;
             const int qi = min(grp * QB + row, nq_all - 1);
             const int i = qi / p.G;
@@ -305,21 +314,19 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
                                   (((slot % QCH) ^ QS::k_swizzle(row & 15)) * 8);
             dma16(uniform(qlds + j * 1024), static_cast<const uint8_t *>(a.q) + 2 * src);
         }
-        int bad = 0;  // two bits a ring slot: the tile's halves lie on pages outside the cache
-        for (int i = 0; i < NS; ++i)
-            if (i < tiles) {
-                const int pa = page_of(tile_at(i)), pb = page_of(tile_at(i) + 16);
-                issue_k(i, pa, pb);
-                issue_v(i, pa, pb);
-                bad |= (int(bad_page(pa)) | int(bad_page(pb)) << 1) << (2 * i);
-            }
-        int na = 0, nb = 0;  // pages of the next tile to issue
-        if (NS < tiles) {
-            na = page_of(tile_at(NS));
-            nb = page_of(tile_at(NS) + 16);
+        int pa = 0, pb = 0, na = 0, nb = 0;  // pages of the tile at hand and of the next one
+        if (tiles > 0) {
+            pa = page_of(tile_at(0));
+            pb = page_of(tile_at(0) + 16);
+            issue_k(0, pa, pb);
+            issue_v(0, pa, pb);
         }
-        if (tiles >= NS)
-            vm_wait<NS *(SH::KL + SH::VL)>();
+        if (tiles > 1) {
+            na = page_of(tile_at(1));
+            nb = page_of(tile_at(1) + 16);
+        }
+        if (tiles > 0)
+            vm_wait<SH::KL + SH::VL>();
         else
             vm_wait<0>();
         wg_barrier();
@@ -352,21 +359,17 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
         }
 
         for (int i = 0; i < tiles; ++i) {
-            const uint32_t buf = ring + (i % NS) * SH::STAGE;
             const int t = tile_at(i);
-            const int bad_now = (bad >> (2 * (i % NS))) & 3;
-            const bool more = i + NS < tiles;
-            const int pa = na, pb = nb;
-            if (i + NS + 1 < tiles) {
-                na = page_of(tile_at(i + NS + 1));
-                nb = page_of(tile_at(i + NS + 1) + 16);
+            const int bad_now = int(bad_page(pa)) | int(bad_page(pb)) << 1;  // the tile's halves on pages outside the cache
+            const bool more = i + 1 < tiles;
+            int fa = 0, fb = 0;  // pages of the tile after next, on their way
+            if (i + 2 < tiles) {
+                fa = page_of(tile_at(i + 2));
+                fb = page_of(tile_at(i + 2) + 16);
             }
             // ---- scores: s[q][half][r] is token 16 half + 4 g + r, query n
-            if (i + NS - 1 < tiles)
-                vm_wait<SH::FLY>();
-            else
-                vm_wait<0>();
-            const uint32_t kbase = fresh(buf + kread);
+            vm_wait<SH::VL>();
+            const uint32_t kbase = fresh(ring + kread);
             f32x4_t s[NQ][2];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
@@ -394,8 +397,8 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
             if constexpr (E4) {
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t kw = lds_read<uint32_t>(buf + 2 * S::BYTES + 16 * hf + 4 * g);
-                    const uint32_t vw = lds_read<uint32_t>(buf + 2 * S::BYTES + 32 + 16 * hf + 4 * g);
+                    const uint32_t kw = lds_read<uint32_t>(ring + 2 * S::BYTES + 16 * hf + 4 * g);
+                    const uint32_t vw = lds_read<uint32_t>(ring + 2 * S::BYTES + 32 + 16 * hf + 4 * g);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float ks = scale_of((kw >> (8 * r)) & 255);
@@ -406,9 +409,7 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
                 }
             }
             lds_drain();
-            if (more) issue_k(i + NS, pa, pb);
-            bad &= ~(3 << (2 * (i % NS)));
-            if (more) bad |= (int(bad_page(pa)) | int(bad_page(pb)) << 1) << (2 * (i % NS));
+            if (more) issue_k(i + 1, na, nb);
 
             // ---- running maximum, probabilities
             const bool masked = t + kTokens > lim_min || bad_now != 0;
@@ -452,12 +453,10 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
 
             // ---- products with V
             if (more)
-                vm_wait<SH::FLYV>();
-            else if (i + NS - 1 < tiles)
-                vm_wait<(NS - 1) * (SH::KL + SH::VL)>();
+                vm_wait<SH::KL>();
             else
                 vm_wait<0>();
-            const uint32_t vbuf = buf + S::BYTES;
+            const uint32_t vbuf = ring + S::BYTES;
             const uint32_t vbase = fresh(vbuf + vread);
             if (masked) {
                 // rows that no query sees (past the request's end, pages outside the cache) may hold anything
@@ -521,12 +520,16 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
                 for (int q = 0; q < NQ; ++q) o[q][c] = mma16(vf, pf[q], o[q][c]);
             }
             lds_drain();
-            if (more) issue_v(i + NS, pa, pb);
+            if (more) issue_v(i + 1, na, nb);
+            pa = na;
+            pb = nb;
+            na = fa;
+            nb = fb;
         }
 
         // ---- the waves' results through LDS ------------------------------
         wg_barrier();
-        const uint32_t jml = lds0 + kPagedWaves * QB * SH::OROW * 4;  // [wave][QB][2]: maximum, sum
+        const uint32_t jml = lds0 + NW * QB * SH::OROW * 4;  // [wave][QB][2]: maximum, sum
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             l[q] = sum_x16(sum_x32(l[q]));
@@ -538,12 +541,12 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
         wg_barrier();
         const bool starts = u0 == 0, ends = u1 == rq.T;
         const long long slot = 2LL * blockIdx.x + (starts ? 1 : 0);
-        for (int e = tid; e < QB * (D / 4); e += kPagedThreads) {
+        for (int e = tid; e < QB * (D / 4); e += NT) {
             const int q = e / (D / 4), c4 = e % (D / 4);
             const int qi = grp * QB + q;
-            float mw[kPagedWaves], lw[kPagedWaves], mm = kNegInf, ll = 0.f;
+            float mw[NW], lw[NW], mm = kNegInf, ll = 0.f;
 #pragma unroll
-            for (int w = 0; w < kPagedWaves; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const u32x2_t x = lds_read<u32x2_t>(jml + (w * QB + q) * 8);
                 mw[w] = __uint_as_float(x[0]);
                 lw[w] = __uint_as_float(x[1]);
@@ -552,7 +555,7 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
             f32x4_t acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
             const float ms = mm == kNegInf ? 0.f : mm;
 #pragma unroll
-            for (int w = 0; w < kPagedWaves; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const float f = fast_exp2(mw[w] - ms);
                 ll += lw[w] * f;
                 acc += lds_read<f32x4_t>(lds0 + ((w * QB + q) * SH::OROW + 4 * c4) * 4) * f;
@@ -568,53 +571,62 @@ __global__ __launch_bounds__(kPagedThreads, (PagedShape<T, E4, D, NQ>::PER_CU)) 
             }
         }
         if (starts && !ends && tid == 0)
-            p.w.meta[blockIdx.x] = make_int4(int((rq.T - u1 + per - 1) / per), b, h, grp);
+            p.w.meta[blockIdx.x] = make_int4((rq.T - u1 + per - 1) / per, b, h, grp);
         wg_barrier();
 
         at += u1 - u0;
         u0 = 0;
         if (++seg >= rq.groups * a.n_kv_heads && at < end) {
             seg = 0;
-            do rq = request_of<QB>(p, ++b);
-            while (rq.groups == 0 && b + 1 < a.B);
+            do {
+                if (++b >= a.B) return;  // (not with offsets that do not decrease)
+                rq = request_of<QB>(p, b);
+            } while (rq.groups == 0);
         }
     }
 }
 
-// The segments that workgroups left unfinished: workgroup (i, q) merges query
-// q of the segment workgroup i started and its successors went on with, in
-// their order.  Its threads take the partials in turn, D / 4 threads each.
+// The segments that workgroups left unfinished: workgroup (i, y) merges
+// kJoinQueries queries of the segment that workgroup i started and its
+// successors went on with, in their order.  64 threads a query take the
+// partials in turn, D / 4 threads each.
 template <typename T, int D, int QB>
-__global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p) {
-    constexpr int TPP = D / 4, LANES = 256 / TPP;  // partials in flight
-    __shared__ float red[LANES][D + 2];
+__global__ __launch_bounds__(64 * kJoinQueries) void paged_join_kernel(PagedParams p) {
+    constexpr int TPP = D / 4, LANES = 64 / TPP;  // threads a partial, partials in flight
     const int4 seg = p.w.meta[blockIdx.x];
     if (seg.x == 0) return;
     const Request rq = request_of<QB>(p, seg.y);
-    const int q = blockIdx.y, qi = seg.w * QB + q;
+    const int lane = threadIdx.x & 63, q = blockIdx.y * kJoinQueries + (threadIdx.x >> 6);
+    const int qi = seg.w * QB + q;
     if (qi >= rq.rows * p.G) return;
-    const int grp = threadIdx.x / TPP, c4 = threadIdx.x % TPP;
+    const int grp = lane / TPP, c4 = lane % TPP;
     const int parts = seg.x + 1;
-    // partial j lies in slot 2 i + 1 (the start) or 2 (i + j)
-    auto slot_of = [&](int j) __device__ { return 2LL * (blockIdx.x + j) + (j == 0 ? 1 : 0); };
     float m = kNegInf, l = 0.f;
     f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int j = grp; j < parts; j += LANES) {
-        const long long s = slot_of(j);
-        merge_partial(m, l, o, p.w.ml[s * 2 * QB + q], p.w.ml[s * 2 * QB + QB + q],
-              *reinterpret_cast<const f32x4_t *>(p.w.o + (s * QB + q) * D + 4 * c4));
+    for (int j0 = grp; j0 < parts; j0 += 4 * LANES) {
+        float pm[4], pl[4];
+        f32x4_t po[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = min(j0 + i * LANES, parts - 1);
+            // partial j lies in slot 2 i + 1 (the start) or 2 (i + j)
+            const long long slot = 2LL * (blockIdx.x + j) + (j == 0 ? 1 : 0);
+            pm[i] = p.w.ml[slot * 2 * QB + q];
+            pl[i] = p.w.ml[slot * 2 * QB + QB + q];
+            po[i] = *reinterpret_cast<const f32x4_t *>(p.w.o + (slot * QB + q) * D + 4 * c4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j0 + i * LANES < parts) merge_partial(m, l, o, pm[i], pl[i], po[i]);
     }
-    if (c4 == 0) {
-        red[grp][D] = m;
-        red[grp][D + 1] = l;
+#pragma unroll
+    for (int s = TPP; s < 64; s <<= 1) {
+        const float m2 = __shfl_xor(m, s), l2 = __shfl_xor(l, s);
+        const f32x4_t o2 = f32x4_t{__shfl_xor(o[0], s), __shfl_xor(o[1], s), __shfl_xor(o[2], s), __shfl_xor(o[3], s)};
+        merge_partial(m, l, o, m2, l2, o2);
     }
-    *reinterpret_cast<float2 *>(&red[grp][4 * c4]) = make_float2(o[0], o[1]);
-    *reinterpret_cast<float2 *>(&red[grp][4 * c4 + 2]) = make_float2(o[2], o[3]);
-    __syncthreads();
-    if (grp != 0) return;
-    for (int k = 1; k < LANES && k < parts; ++k)
-        merge_partial(m, l, o, red[k][D], red[k][D + 1], f32x4_t{red[k][4 * c4], red[k][4 * c4 + 1], red[k][4 * c4 + 2], red[k][4 * c4 + 3]});
-    store_row<T>(p.a.out, p.a.lse, (long long)(rq.row0 + qi / p.G) * p.a.n_heads + seg.z * p.G + qi % p.G, c4, D, o, m, l);
+    if (grp == 0)
+        store_row<T>(p.a.out, p.a.lse, (long long)(rq.row0 + qi / p.G) * p.a.n_heads + seg.z * p.G + qi % p.G, c4, D, o, m, l);
 }
 
 int log2_of(int x) {
@@ -625,9 +637,17 @@ int log2_of(int x) {
 
 template <typename T, bool E4, int D, int NQ>
 hipError_t launch_paged_typed(const PagedParams &pp, const PagedPlan &plan, hipStream_t s) {
-    launch_kernel("paged_attention", paged_kernel<T, E4, D, NQ>, dim3(plan.grid), dim3(kPagedThreads), s, pp);
+    const dim3 grid(plan.grid);
+    bool done = false;
+    if constexpr (paged_per_cu(E4, D, NQ, 8) >= 1)
+        if (plan.waves == 8) {
+            launch_kernel("paged_attention", paged_kernel<T, E4, D, NQ, 8>, grid, dim3(512), s, pp);
+            done = true;
+        }
+    if (!done) launch_kernel("paged_attention", paged_kernel<T, E4, D, NQ, 4>, grid, dim3(256), s, pp);
     if (!plan.whole)
-        launch_kernel("paged_join", paged_join_kernel<T, D, 16 * NQ>, dim3(plan.grid - 1, 16 * NQ), dim3(256), s, pp);
+        launch_kernel("paged_join", paged_join_kernel<T, D, 16 * NQ>, dim3(plan.grid - 1, 16 * NQ / kJoinQueries),
+                      dim3(64 * kJoinQueries), s, pp);
     return hipGetLastError();
 }
 
@@ -658,13 +678,21 @@ hipError_t launch_paged_dim(const PagedParams &pp, const PagedPlan &plan, hipStr
 // The query blocks cover a request's rows times its group where they fit
 // (16 to 64 queries; 32 at D = 256, whose accumulators are twice as long);
 // more rows take several groups, which read the cache again.
-PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long table_tokens) {
+PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long requests,
+                     long long table_tokens) {
     PagedPlan p{};
     const long long queries = (long long)max_rows * (n_heads / n_kv_heads);
     const int most = head_dim >= 256 ? 2 : 4;
     p.qblocks = queries <= 16 ? 1 : (queries <= 32 || most == 2 ? 2 : 4);
-    p.grid = 256 * paged_per_cu(e4, head_dim, p.qblocks);
+    p.waves = 4;
+    p.grid = 256 * paged_per_cu(e4, head_dim, p.qblocks, 4);
     p.whole = table_tokens <= kWholeTokens;
+    // few short segments: eight waves each, and no second launch
+    if (table_tokens > kUnit && table_tokens <= kWideTokens && requests * n_kv_heads <= 256 &&
+        paged_per_cu(e4, head_dim, p.qblocks, 8) >= 1) {
+        p.whole = 1;
+        p.waves = 8;
+    }
     return p;
 }
 
@@ -685,6 +713,10 @@ hipError_t launch_paged(const PagedArgs &a, const PagedPlan &plan, const PagedWo
     p.G = a.n_heads / a.n_kv_heads;
     p.pshift = log2_of(a.page_size);
     p.whole = plan.whole;
+    p.unit = kUnit;
+    const long long segments = (long long)a.n_rows * a.n_heads / (16 * plan.qblocks) + (long long)a.B * a.n_kv_heads;
+    const long long tokens = (long long)a.max_pages * a.page_size;
+    while (segments * (tokens / p.unit + 1) > INT32_MAX) p.unit *= 2;
     p.c = a.scale * kLog2e;
     const bool e4 = a.cache_dtype == DSPARK_E4M3;
     if (a.dtype == DSPARK_BF16)
