@@ -6,12 +6,15 @@ kernels (or, for the scheduler, its host C++).  Device arrays are torch
 tensors on the current HIP device, passed by pointer together with torch's
 current stream; host arrays (scheduler) are numpy arrays.  The functions
 carry the C entry points' names.  A missing or unloadable library raises
-immediately: there is no fallback path.
+immediately: there is no fallback path.  The cache and attention functions
+marshal through a compiled module (csrc/marshal.cpp) where they can, the others
+through ctypes.
 """
 from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 
 import numpy as np
@@ -41,6 +44,7 @@ DSPARK_F16 = 2
 DSPARK_E4M3 = 3
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdspark.so")
+MARSHAL_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_marshal.so")
 
 _c_void_p = ctypes.c_void_p
 _c_int = ctypes.c_int
@@ -526,11 +530,29 @@ def dspark_sts_fit(conf, n_accept, grid, *, ell=None, n_bins: int = 15, ece_grid
 
 # ---------------------------------------------------------------- cache and attention
 #
-# A decoding step calls these with kernels of a few microseconds, so the
-# checks take the short way where everything is in order (one expression a
-# tensor) and find the words only where something is not.
+# A decoding step calls these with kernels of a few microseconds.  A call on
+# the current stream with its outputs given goes the short way through the
+# compiled marshalling module, which makes the same checks and answers None
+# where something is not in order (or not of the common kind); the checks below
+# then find the words.
 
+_short = None
 _row_types = None
+
+
+def _load_marshal():
+    global _short
+    torch = _torch()
+    lib = load_library()
+    if not os.path.exists(MARSHAL_PATH):
+        raise RuntimeError(f"marshalling module not built at {MARSHAL_PATH}; run __graft_entry__.build()")
+    module = importlib.import_module(__name__ + "._marshal")
+    names = ("dspark_kv_write", "dspark_kv_read", "dspark_paged_attention_workspace_size", "dspark_paged_attention",
+             "dspark_prompt_attention_workspace_size", "dspark_prompt_attention")
+    module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    _short = module
+    return module
 
 
 def _types():
@@ -633,6 +655,11 @@ def dspark_kv_write(k, v, k_cache, v_cache, cache_len, page_table, *, row_offset
     or float8_e4m3fn (then with k_scale, v_scale [n_pages, Hkv, page_size] uint8):
     row i of request b, rows row_offsets[b] .. row_offsets[b + 1] - 1 (None: one
     row a request), goes to position cache_len[b] + i of page_table [B, max_pages]."""
+    if stream is None:
+        st = (_short or _load_marshal()).kv_write(k, v, k_cache, v_cache, cache_len, page_table, row_offsets,
+                                                    k_scale, v_scale)
+        if st is not None:
+            return _check(st, "dspark_kv_write")
     lib = load_library()
     dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     dt = _row_dtype(k, "k")
@@ -654,6 +681,12 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     type, bfloat16 for a float8_e4m3fn cache); rows of no request keep what
     ``out`` holds (zeros in a new result)."""
     torch = _torch()
+    if out is not None and stream is None and dtype is out["k"].dtype and n_rows == out["k"].shape[0]:
+        st = (_short or _load_marshal()).kv_read(k_cache, v_cache, page_table, row_offsets, first, k_scale, v_scale,
+                                                   out["k"], out["v"])
+        if st is not None:
+            _check(st, "dspark_kv_read")
+            return out
     lib = load_library()
     dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     if dtype is None:
@@ -713,6 +746,13 @@ def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_of
     values).  max_rows: rows a request usually has at most (None: the average,
     rounded up); scale: None = D^-1/2.  Returns {"out"[, "lse"], "workspace"};
     pass ``out`` (a previous result) to reuse its buffers."""
+    if out is not None and stream is None:
+        st = (_short or _load_marshal()).paged_attention(
+            q, k_cache, v_cache, cache_len, page_table, row_offsets, k_scale, v_scale, scale, causal, max_rows,
+            out["out"], out.get("lse"), workspace if workspace is not None else out.get("workspace"))
+        if st is not None:
+            _check(st, "dspark_paged_attention")
+            return out
     lib = load_library()
     dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     dt = _row_dtype(q, "q")
@@ -749,6 +789,13 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
     kv_offsets[b + 1] - 1 of k and v (None: the same rows).  Its query rows are
     the last positions of its keys.  scale: None = D^-1/2.  Returns {"out"[,
     "lse"], "workspace"}; pass ``out`` (a previous result) to reuse its buffers."""
+    if out is not None and stream is None:
+        st = (_short or _load_marshal()).prompt_attention(
+            q, k, v, row_offsets, kv_offsets, scale, causal, out["out"], out.get("lse"),
+            workspace if workspace is not None else out.get("workspace"))
+        if st is not None:
+            _check(st, "dspark_prompt_attention")
+            return out
     torch = _torch()
     lib = load_library()
     dt = _row_dtype(q, "q")

@@ -1,12 +1,16 @@
-"""Build libdspark.so (HIP for gfx950) in-tree.
+"""Build libdspark.so (HIP for gfx950) and the Python binding's marshalling
+module in-tree.
 
 Every translation unit is compiled by hipcc for gfx950 only, warnings
 (shadowed names included) as errors and packed-FP32 instruction selection
-switched off, then linked into one shared library next to this file.  Run as a script or call ``build()``.
+switched off, then linked into one shared library next to this file.  The
+marshalling module (csrc/marshal.cpp, host code only) is compiled by the host
+compiler against the installed torch.  Run as a script or call ``build()``.
 """
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -14,7 +18,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdspark.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 
 SOURCES = ["api.cpp", "schedule.cpp", "draft.hip", "verify.hip", "accept.hip", "rnn.hip", "sts.hip", "cache.hip", "paged.hip", "prompt.hip",
            "debug.hip"]
@@ -41,10 +47,30 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_marshal(verbose: bool) -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra", "-Wshadow", "-Werror",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
+           os.path.join(CSRC, "marshal.cpp"), "-o", MARSHAL + ".tmp",
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for marshal.cpp:\n{r.stderr}")
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
+        marshal = ex.submit(_compile_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        marshal.result()
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
