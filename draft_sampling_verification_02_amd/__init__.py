@@ -559,8 +559,7 @@ def _types():
     global _row_types
     if _row_types is None:
         torch = _torch()
-        _row_types = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16, torch.float32: DSPARK_F32,
-                      torch.float8_e4m3fn: DSPARK_E4M3}
+        _row_types = {torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16, torch.float8_e4m3fn: DSPARK_E4M3}
     return _row_types
 
 
@@ -597,8 +596,8 @@ def _rows(t, name, dtype, heads, device):
 
 
 def _row_dtype(t, name):
-    dt = _types().get(getattr(t, "dtype", None))
-    if dt is None:
+    dt = _types().get(getattr(t, "dtype", None), DSPARK_E4M3)
+    if dt == DSPARK_E4M3:
         raise TypeError(f"{name}: expected a bfloat16 or float16 tensor")
     return dt
 
@@ -691,8 +690,8 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     if dtype is None:
         dtype = torch.bfloat16 if cdt == DSPARK_E4M3 else k_cache.dtype
-    dt = _types().get(dtype)
-    if dt is None:
+    dt = _types().get(dtype, DSPARK_E4M3)
+    if dt == DSPARK_E4M3:
         raise TypeError(f"dtype: {dtype}, expected bfloat16 or float16")
     B, max_pages = _requests(row_offsets, n_rows, page_table, dev)
     if first is not None:

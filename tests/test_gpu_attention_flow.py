@@ -1,0 +1,135 @@
+"""The cache and attention operators together, as a serving loop uses them
+around the library's rounds: prompts attend over themselves and enter the
+paged cache; every round drafts, the verify rows (anchor and drafts) are
+written and attend over the cache, their logits go to dspark_verify, and
+cache_len grows by what was accepted.
+
+The model is one layer with fixed weights (embedding rows, their query, key
+and value projections, an output matrix): enough that a wrong token, position
+or stale cache slot changes the result."""
+import numpy as np
+import pytest
+import torch
+
+from attendkit import U, attend, check, dequantise, quantise
+
+pytestmark = pytest.mark.gpu
+
+BF, E4 = torch.bfloat16, torch.float8_e4m3fn
+
+
+class Model:
+    V, R, Hq, Hkv, D = 1000, 16, 4, 2, 64
+
+    def __init__(self, seed):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda *s: torch.randn(s, generator=g)
+        self.qkv = (r(self.V, self.Hq + 2 * self.Hkv, self.D)).to(BF)  # rows of a fused projection, by token
+        self.out = (r(self.V, self.Hq * self.D) * 0.3).to(BF)
+        self.W1, self.W2 = (r(self.V, self.R) * 0.3).to(BF), (r(self.V, self.R) * 0.3).to(BF)
+
+    def logits(self, o):
+        return (o.float().reshape(o.shape[0], -1) @ self.out.to(o.device).float().t()).contiguous()
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_prompts_then_rounds(cache):
+    import draft_sampling_verification_02_amd as ds
+    ds.load_library()
+    m = Model(3)
+    Hq, Hkv, D, V = m.Hq, m.Hkv, m.D, m.V
+    g = torch.Generator().manual_seed(4)
+    B, gamma, page, rounds = 6, 4, 16, 5
+    lens = [1, 16, 37, 64, 5, 130]
+    prompts = [torch.randint(0, V, (n,), generator=g) for n in lens]
+    width = (max(lens) + rounds * (gamma + 1)) // page + 2
+    n_pages = B * width
+    table = torch.randperm(n_pages, generator=g).to(torch.int32).reshape(B, width)
+    dev = "cuda"
+    kc, vc = (torch.full((n_pages, Hkv, page, D), float("nan"), dtype=torch.float32, device=dev).to(cache) for _ in range(2))
+    sc = {} if cache == BF else {n: torch.zeros((n_pages, Hkv, page), dtype=torch.uint8, device=dev) for n in ("k_scale", "v_scale")}
+    qkv = m.qkv.to(dev)
+    split = lambda t: (t[:, :Hq], t[:, Hq:Hq + Hkv], t[:, Hq + Hkv:])
+    table_d = table.to(dev)
+    zeros = torch.zeros(B, dtype=torch.int32, device=dev)
+    up = U[BF]
+
+    def history(tokens):
+        """Keys and values of a token list as the cache holds them, float64."""
+        _, k, v = split(m.qkv[tokens])
+        return [x.double() if cache == BF else dequantise(*quantise(x)) for x in (k, v)]
+
+    # ---- prompts: attention over themselves, and into the cache
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+    q, k, v = split(qkv[torch.cat(prompts).to(dev)])
+    whole = ds.dspark_prompt_attention(q, k, v, off, lse=True)
+    ds.dspark_kv_write(k, v, kc, vc, zeros, table_d, row_offsets=off, **sc)
+    again = ds.dspark_paged_attention(q, kc, vc, zeros, table_d, row_offsets=off, lse=True, max_rows=max(lens), **sc)
+    torch.cuda.synchronize()
+    at = 0
+    for b, n in enumerate(lens):
+        qb, kb, vb = (x.double() for x in split(m.qkv[prompts[b]]))
+        o, z, tol, lt = attend(qb, kb, vb, list(range(1, n + 1)), D ** -0.5, up, up)
+        check("prompt out", whole["out"][at:at + n], o, tol)
+        check("prompt lse", whole["lse"][at:at + n], z, lt)
+        o, z, tol, lt = attend(qb, *history(prompts[b]), list(range(1, n + 1)), D ** -0.5, up, up)
+        check("the same rows over the cache", again["out"][at:at + n], o, tol)
+        check("their lse", again["lse"][at:at + n], z, lt)
+        at += n
+
+    # ---- rounds
+    tokens = [p.tolist() for p in prompts]  # every token whose key and value are in the cache
+    anchor = torch.randint(0, V, (B,), generator=g).to(torch.int32)
+    cache_len = torch.tensor(lens, dtype=torch.int32, device=dev)
+    temperature = torch.tensor([1.0, 0.0, 1.0, 1.0, 0.0, 1.0], device=dev)
+    W1, W2 = m.W1.to(dev), m.W2.to(dev)
+    accepted = 0
+    for rnd in range(rounds):
+        U_logits = torch.randn((B, gamma, V), generator=g).to(dev)
+        ell = torch.randint(0, gamma + 1, (B,), generator=g).to(torch.int32)
+        d = ds.dspark_draft_sample(U_logits, W1, W2, anchor.to(dev), temperature, 77, rnd)
+        x = d["x"].cpu()
+        rows = [[int(anchor[b])] + x[b, :int(ell[b])].tolist() for b in range(B)]
+        roff = torch.tensor(np.concatenate([[0], np.cumsum([len(r) for r in rows])]), dtype=torch.int32, device=dev)
+        flat = torch.tensor(sum(rows, []))
+        q, k, v = split(qkv[flat.to(dev)])
+        ds.dspark_kv_write(k, v, kc, vc, cache_len, table_d, row_offsets=roff, **sc)
+        r = ds.dspark_paged_attention(q, kc, vc, cache_len, table_d, row_offsets=roff, lse=True, max_rows=gamma + 1, **sc)
+        target = m.logits(r["out"])
+        if rnd % 2:
+            # a target that follows the drafts of every other request, so that some are accepted
+            for b in range(0, B, 2):
+                for i in range(int(ell[b])):
+                    target[int(roff[b]) + i, int(x[b, i])] += 40.0
+        ver = ds.dspark_verify(target, ell.to(dev), U_logits, W1, W2, anchor.to(dev), d["x"], d["lse"], d["qx"], temperature,
+                               77, rnd, row_offsets=roff)
+        torch.cuda.synchronize()
+        at = 0
+        for b in range(B):
+            n = len(rows[b])
+            qb = split(m.qkv[torch.tensor(rows[b])])[0].double()
+            seen = tokens[b] + rows[b]
+            o, z, tol, lt = attend(qb, *history(torch.tensor(seen)), [len(tokens[b]) + i + 1 for i in range(n)], D ** -0.5,
+                                   up, up)
+            check(f"round {rnd} request {b} out", r["out"][at:at + n], o, tol)
+            check(f"round {rnd} request {b} lse", r["lse"][at:at + n], z, lt)
+            at += n
+        n_acc = ver["n"].cpu()
+        out = ver["tokens"].cpu()
+        assert bool((n_acc >= 0).all()) and bool((n_acc <= ell).all())
+        for b in range(B):
+            na = int(n_acc[b])
+            tokens[b] += rows[b][:na + 1]  # the anchor and the accepted drafts stay; the rest is written over
+            anchor[b] = out[b, na]
+            accepted += na
+        cache_len += ver["n"] + 1
+    assert accepted > 0
+
+    # ---- what the cache holds at the end
+    total = [len(t) for t in tokens]
+    assert cache_len.tolist() == total
+    off = torch.tensor(np.concatenate([[0], np.cumsum(total)]), dtype=torch.int32, device=dev)
+    back = ds.dspark_kv_read(kc, vc, table_d, sum(total), row_offsets=off, **sc)
+    torch.cuda.synchronize()
+    k, v = history(torch.tensor(sum(tokens, [])))
+    assert torch.equal(back["k"].cpu().double(), k) and torch.equal(back["v"].cpu().double(), v)
