@@ -105,6 +105,18 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return e < -126 ? -126 : e;
 }
 
+// Maximum over the C neighbouring lanes (8, 16 or 32; items in order) that hold
+// one (row, head); x >= 0, so its bits order as it does.
+__device__ __forceinline__ float group_max(float x, int C) {
+    uint32_t u = __float_as_uint(x);
+    u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0xB1, 0xF, 0xF, true)));   // lanes l ^ 1
+    u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x4E, 0xF, 0xF, true)));   // l ^ 2
+    u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x141, 0xF, 0xF, true)));  // the eight lanes mirrored
+    if (C >= 16) u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x140, 0xF, 0xF, true)));  // the sixteen
+    const float m = __uint_as_float(u);
+    return C >= 32 ? max_x16(m) : m;
+}
+
 struct Item {
     int row, head, chunk;  // row relative to the workgroup's first
     bool v;
@@ -152,18 +164,19 @@ template <typename T, bool E4, int ITEMS>
 __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(CacheParams p) {
     __shared__ long long slots[kMaxRowsPerBlock];
     __shared__ int red[8];
+    __shared__ uint8_t bytes[E4 ? kCacheThreads * ITEMS / 8 : 1];  // scales by (row, head) of the run
     const CacheArgs &a = p.a;
     const Run run = run_of(p);
     const int row0 = run.row0;
     // the rows go out first: their addresses need no request
     Item im[ITEMS];
-    uint4 x[ITEMS];
+    u32x4v_t x[ITEMS];
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         im[j] = item_of(p, run.rel0 + min(int(threadIdx.x) + j * kCacheThreads, run.count - 1));
         const uint8_t *src = static_cast<const uint8_t *>(im[j].v ? a.v : a.k);
         const long long stride = im[j].v ? a.v_stride : a.k_stride;
-        x[j] = *reinterpret_cast<const uint4 *>(
+        x[j] = *reinterpret_cast<const u32x4v_t *>(
             src + 2 * ((row0 + im[j].row) * stride + ((long long)im[j].head * p.C + im[j].chunk) * 8));
     }
     place_rows(p, row0, run.row1, slots, nullptr, red);
@@ -174,22 +187,20 @@ __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(CacheParams p) 
         const long long rowat = slot + ((long long)im[j].head << p.pshift);  // row of the cache, D values each
         uint8_t *cache = static_cast<uint8_t *>(im[j].v ? a.v_cache : a.k_cache);
         if constexpr (!E4) {
-            if (live && slot >= 0) *reinterpret_cast<uint4 *>(cache + (rowat * p.C + im[j].chunk) * 16) = x[j];
+            if (live && slot >= 0) *reinterpret_cast<u32x4v_t *>(cache + (rowat * p.C + im[j].chunk) * 16) = x[j];
         } else {
-            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
             float f[8];
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 t = widen<T>(w[i]);
+                const float2 t = widen<T>(x[j][i]);
                 f[2 * i] = t.x;
                 f[2 * i + 1] = t.y;
                 // the scale is that of the finite values; the others become NaN
                 if (fabsf(t.x) < __builtin_huge_valf()) amax = fmaxf(amax, fabsf(t.x));
                 if (fabsf(t.y) < __builtin_huge_valf()) amax = fmaxf(amax, fabsf(t.y));
             }
-            // the C lanes of a (row, head) are neighbours (C = 8, 16 or 32, items in order)
-            for (int s = p.C >> 1; s >= 1; s >>= 1) amax = fmaxf(amax, __shfl_xor(amax, s));
+            amax = group_max(amax, p.C);
             const int e = scale_exponent(amax);
             const float inv = __uint_as_float(uint32_t(127 - e) << 23);  // e in -126 .. 120
             int lo = 0, hi = 0;
@@ -199,8 +210,22 @@ __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(CacheParams p) 
             hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
             if (live && slot >= 0) {
                 *reinterpret_cast<int2 *>(cache + (rowat * p.C + im[j].chunk) * 8) = make_int2(lo, hi);
-                if (im[j].chunk == 0) (im[j].v ? a.v_scale : a.k_scale)[rowat] = uint8_t(e + 127);
             }
+            if (live && im[j].chunk == 0) bytes[(threadIdx.x + j * kCacheThreads) >> p.cshift] = uint8_t(e + 127);
+        }
+    }
+    if constexpr (E4) {
+        // the scales of a head's neighbouring tokens are neighbouring bytes:
+        // neighbouring lanes write them
+        __syncthreads();
+        const int rows = run.row1 - row0 + 1;
+        for (int t = threadIdx.x; t < rows * 2 * a.n_kv_heads; t += kCacheThreads) {
+            const int hv = unsigned(t) / unsigned(rows), row = t - hv * rows;
+            const int rel = row * p.per_row + (hv << p.cshift) - run.rel0;  // the run's item that starts the (row, head)
+            if (rel < 0 || rel >= run.count || slots[row] < 0) continue;
+            const bool v = hv >= a.n_kv_heads;
+            const int head = v ? hv - a.n_kv_heads : hv;
+            (v ? a.v_scale : a.k_scale)[slots[row] + ((long long)head << p.pshift)] = bytes[rel >> p.cshift];
         }
     }
 }
@@ -220,7 +245,7 @@ __device__ __forceinline__ uint32_t narrow2(float x, float y) {
 }
 
 template <typename T, bool E4, int ITEMS>
-__global__ __launch_bounds__(kCacheThreads) void kv_read_kernel(CacheParams p) {
+__global__ __launch_bounds__(kCacheThreads, 8) void kv_read_kernel(CacheParams p) {
     __shared__ long long slots[kMaxRowsPerBlock];
     __shared__ int inside[kMaxRowsPerBlock];
     __shared__ int red[8];
@@ -229,7 +254,7 @@ __global__ __launch_bounds__(kCacheThreads) void kv_read_kernel(CacheParams p) {
     const int row0 = run.row0;
     place_rows(p, row0, run.row1, slots, inside, red);
     Item im[ITEMS];
-    uint4 x[ITEMS];
+    u32x4v_t x[ITEMS];
     float sc[ITEMS];
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
@@ -237,34 +262,34 @@ __global__ __launch_bounds__(kCacheThreads) void kv_read_kernel(CacheParams p) {
         const long long slot = slots[im[j].row];
         const long long rowat = max(slot, 0LL) + ((long long)im[j].head << p.pshift);
         const uint8_t *cache = static_cast<const uint8_t *>(im[j].v ? a.v_cache : a.k_cache);
-        x[j] = make_uint4(0, 0, 0, 0);
+        x[j] = u32x4v_t{0, 0, 0, 0};
         sc[j] = 0.f;
         if (slot < 0) continue;
         if constexpr (E4) {
-            const uint2 t = *reinterpret_cast<const uint2 *>(cache + (rowat * p.C + im[j].chunk) * 8);
-            x[j].x = t.x;
-            x[j].y = t.y;
+            const u32x2_t t = *reinterpret_cast<const u32x2_t *>(cache + (rowat * p.C + im[j].chunk) * 8);
+            x[j][0] = t[0];
+            x[j][1] = t[1];
             sc[j] = scale_of((im[j].v ? a.v_scale : a.k_scale)[rowat]);
         } else {
-            x[j] = *reinterpret_cast<const uint4 *>(cache + (rowat * p.C + im[j].chunk) * 16);
+            x[j] = *reinterpret_cast<const u32x4v_t *>(cache + (rowat * p.C + im[j].chunk) * 16);
         }
     }
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         if (int(threadIdx.x) + j * kCacheThreads >= run.count || !inside[im[j].row]) continue;
-        uint4 o = x[j];
+        u32x4v_t o = x[j];
         if constexpr (E4) {
             float f[8];
-            e4m3_to4(x[j].x, f);
-            e4m3_to4(x[j].y, f + 4);
+            e4m3_to4(x[j][0], f);
+            e4m3_to4(x[j][1], f + 4);
             const bool none = slots[im[j].row] < 0;  // zeros, whatever the scale
-            o.x = none ? 0u : narrow2<T>(f[0] * sc[j], f[1] * sc[j]);
-            o.y = none ? 0u : narrow2<T>(f[2] * sc[j], f[3] * sc[j]);
-            o.z = none ? 0u : narrow2<T>(f[4] * sc[j], f[5] * sc[j]);
-            o.w = none ? 0u : narrow2<T>(f[6] * sc[j], f[7] * sc[j]);
+            o[0] = none ? 0u : narrow2<T>(f[0] * sc[j], f[1] * sc[j]);
+            o[1] = none ? 0u : narrow2<T>(f[2] * sc[j], f[3] * sc[j]);
+            o[2] = none ? 0u : narrow2<T>(f[4] * sc[j], f[5] * sc[j]);
+            o[3] = none ? 0u : narrow2<T>(f[6] * sc[j], f[7] * sc[j]);
         }
         uint8_t *dst = static_cast<uint8_t *>(im[j].v ? a.v_out : a.k_out);
-        *reinterpret_cast<uint4 *>(
+        *reinterpret_cast<u32x4v_t *>(
             dst + 2 * (((long long)(row0 + im[j].row) * a.n_kv_heads + im[j].head) * p.C + im[j].chunk) * 8) = o;
     }
 }
