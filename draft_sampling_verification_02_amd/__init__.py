@@ -697,8 +697,7 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     if first is not None:
         _dense(first, "first", torch.int32, (B,), dev)
     if out is None:
-        new = torch.empty if row_offsets is None else torch.zeros
-        out = {n: new((n_rows, Hkv, D), dtype=dtype, device=dev) for n in ("k", "v")}
+        out = _new_outputs({n: ((n_rows, Hkv, D), dtype) for n in ("k", "v")}, dev, row_offsets is None, stream)
     for n in ("k", "v"):
         _dense(out[n], n, dtype, (n_rows, Hkv, D), dev)
     _call_on(dev, stream, "dspark_kv_read", lib.dspark_kv_read, _at(k_cache), _at(v_cache), _at(k_scale),
@@ -707,27 +706,36 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     return out
 
 
-def _attention_outputs(q, lse, out, every_row):
+def _new_outputs(shapes, device, every_row, stream):
+    """New buffers {name: (shape, dtype)}, made on the call's stream; rows that
+    no request owns are zero."""
+    torch = _torch()
+    new = torch.empty if every_row else torch.zeros
+    with torch.cuda.stream(stream):
+        return {n: new(shape, dtype=dtype, device=device) for n, (shape, dtype) in shapes.items()}
+
+
+def _attention_outputs(q, lse, out, every_row, stream):
     torch = _torch()
     dev, shape = q.device, q.shape
     if out is None:
-        # rows of no request stay zero
-        new = torch.empty if every_row else torch.zeros
-        out = {"out": new(shape, dtype=q.dtype, device=dev)}
+        shapes = {"out": (shape, q.dtype)}
         if lse:
-            out["lse"] = new(shape[:2], dtype=torch.float32, device=dev)
+            shapes["lse"] = (shape[:2], torch.float32)
+        out = _new_outputs(shapes, dev, every_row, stream)
     _dense(out["out"], "out", q.dtype, shape, dev)
     if "lse" in out:
         _dense(out["lse"], "lse", torch.float32, shape[:2], dev)
     return out
 
 
-def _attention_workspace(nbytes, device, workspace, out):
+def _attention_workspace(nbytes, device, workspace, out, stream):
     if workspace is not None:
         out["workspace"] = workspace
     ws = out.get("workspace")
     if nbytes and (ws is None or ws.numel() < nbytes):  # 0 bytes: the call reports why
-        ws = out["workspace"] = _workspace(nbytes, device, None)
+        with _torch().cuda.stream(stream):
+            ws = out["workspace"] = _workspace(nbytes, device, None)
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
@@ -761,11 +769,11 @@ def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_of
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, heads, {D}]")
     B, max_pages = _requests(row_offsets, n, page_table, dev)
     _dense(cache_len, "cache_len", page_table.dtype, (B,), dev)
-    out = _attention_outputs(q, lse, out, row_offsets is None)
+    out = _attention_outputs(q, lse, out, row_offsets is None, stream)
     if max_rows is None:
         max_rows = max(1, -(-n // max(B, 1)))
     ws, ws_bytes = _attention_workspace(dspark_paged_attention_workspace_size(max_rows, Hq, Hkv, D), dev, workspace,
-                                        out)
+                                        out, stream)
     _call_on(dev, stream, "dspark_paged_attention", lib.dspark_paged_attention, _at(q), qs, dt, _at(row_offsets), n,
              max_rows, _at(cache_len), _at(page_table), B, max_pages, Hq, Hkv, D, _at(k_cache), _at(v_cache),
              _at(k_scale), _at(v_scale), cdt, n_pages, ps, D ** -0.5 if scale is None else scale, 1 if causal else 0,
@@ -811,9 +819,9 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
         _dense(kv_offsets, "kv_offsets", torch.int32, (B + 1,), dev)
     elif n_kv != n:
         raise ValueError(f"kv_offsets: needed for {n} query rows and {n_kv} key rows")
-    out = _attention_outputs(q, lse, out, False)
+    out = _attention_outputs(q, lse, out, False, stream)
     ws, ws_bytes = _attention_workspace(dspark_prompt_attention_workspace_size(B, n, n_kv, Hq, Hkv, D), dev,
-                                        workspace, out)
+                                        workspace, out, stream)
     _call_on(dev, stream, "dspark_prompt_attention", lib.dspark_prompt_attention, _at(q), _at(k), _at(v), qs, ks, vs,
              dt, _at(row_offsets), n, _at(kv_offsets), n_kv, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
              1 if causal else 0, _at(out["out"]), _at(out.get("lse")), ws, ws_bytes)

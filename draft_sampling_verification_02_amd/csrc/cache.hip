@@ -106,15 +106,33 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 
 // Maximum over the C neighbouring lanes (8, 16 or 32; items in order) that hold
-// one (row, head); x >= 0, so its bits order as it does.
-__device__ __forceinline__ float group_max(float x, int C) {
-    uint32_t u = __float_as_uint(x);
+// one (row, head).
+__device__ __forceinline__ uint32_t group_max(uint32_t u, int C) {
     u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0xB1, 0xF, 0xF, true)));   // lanes l ^ 1
     u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x4E, 0xF, 0xF, true)));   // l ^ 2
     u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x141, 0xF, 0xF, true)));  // the eight lanes mirrored
     if (C >= 16) u = max(u, uint32_t(__builtin_amdgcn_mov_dpp(int(u), 0x140, 0xF, 0xF, true)));  // the sixteen
-    const float m = __uint_as_float(u);
-    return C >= 32 ? max_x16(m) : m;
+    if (C >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        u = max(uint32_t(r[0]), uint32_t(r[1]));
+    }
+    return u;
+}
+
+// Two pairs of 16-bit floats, divided by a power of two, as four e4m3 values
+// (none of them past 448).
+template <typename T>
+__device__ __forceinline__ int to_e4m3(uint32_t a, uint32_t b, float scale) {
+    typedef short s16x2_t __attribute__((ext_vector_type(2)));
+    s16x2_t r = {0, 0};
+    if constexpr (std::is_same<T, TypeBf16>::value) {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, a), scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, b), scale, true);
+    } else {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(f16x2_t, a), scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, __builtin_bit_cast(f16x2_t, b), scale, true);
+    }
+    return __builtin_bit_cast(int, r);
 }
 
 struct Item {
@@ -164,7 +182,6 @@ template <typename T, bool E4, int ITEMS>
 __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(CacheParams p) {
     __shared__ long long slots[kMaxRowsPerBlock];
     __shared__ int red[8];
-    __shared__ uint8_t bytes[E4 ? kCacheThreads * ITEMS / 8 : 1];  // scales by (row, head) of the run
     const CacheArgs &a = p.a;
     const Run run = run_of(p);
     const int row0 = run.row0;
@@ -176,8 +193,10 @@ __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(CacheParams p) 
         im[j] = item_of(p, run.rel0 + min(int(threadIdx.x) + j * kCacheThreads, run.count - 1));
         const uint8_t *src = static_cast<const uint8_t *>(im[j].v ? a.v : a.k);
         const long long stride = im[j].v ? a.v_stride : a.k_stride;
-        x[j] = *reinterpret_cast<const u32x4v_t *>(
-            src + 2 * ((row0 + im[j].row) * stride + ((long long)im[j].head * p.C + im[j].chunk) * 8));
+        // read once: non-temporal (measured with the row's conversion at 37,700 rows
+        // of 8 heads, D = 128, into 8 bits: 58 us against 65)
+        x[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v_t *>(
+            src + 2 * ((row0 + im[j].row) * stride + ((long long)im[j].head * p.C + im[j].chunk) * 8)));
     }
     place_rows(p, row0, run.row1, slots, nullptr, red);
 #pragma unroll
@@ -189,43 +208,39 @@ __global__ __launch_bounds__(kCacheThreads) void kv_write_kernel(CacheParams p) 
         if constexpr (!E4) {
             if (live && slot >= 0) *reinterpret_cast<u32x4v_t *>(cache + (rowat * p.C + im[j].chunk) * 16) = x[j];
         } else {
-            float f[8];
-            float amax = 0.f;
+            // magnitudes of 16-bit floats order as their bits do
+            uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 t = widen<T>(x[j][i]);
-                f[2 * i] = t.x;
-                f[2 * i + 1] = t.y;
-                // the scale is that of the finite values; the others become NaN
-                if (fabsf(t.x) < __builtin_huge_valf()) amax = fmaxf(amax, fabsf(t.x));
-                if (fabsf(t.y) < __builtin_huge_valf()) amax = fmaxf(amax, fabsf(t.y));
+            for (int i = 0; i < 4; ++i) top = max_u16x2(top, x[j][i] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+            const bool odd = __any(top >= T::kInf);
+            if (odd) {
+                // infinities or NaN: the scale is that of the finite values
+                top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = max_u16x2(top, finite_pair<T>(x[j][i]) & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
             }
-            amax = group_max(amax, p.C);
-            const int e = scale_exponent(amax);
-            const float inv = __uint_as_float(uint32_t(127 - e) << 23);  // e in -126 .. 120
-            int lo = 0, hi = 0;
-            lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, lo, false);
-            lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
-            hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4] * inv, f[5] * inv, hi, false);
-            hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
+            const int e = scale_exponent(widen<T>(group_max(top, p.C)).x);
+            int lo, hi;
+            if (!odd) {
+                const float scale = __uint_as_float(uint32_t(e + 127) << 23);  // e in -126 .. 120
+                lo = to_e4m3<T>(x[j][0], x[j][1], scale);
+                hi = to_e4m3<T>(x[j][2], x[j][3], scale);
+            } else {
+                const float inv = __uint_as_float(uint32_t(127 - e) << 23);
+                float f[8];
+                widen4<T>(u32x2_t{x[j][0], x[j][1]}, f);
+                widen4<T>(u32x2_t{x[j][2], x[j][3]}, f + 4);
+                lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0] * inv, f[1] * inv, 0, false);
+                lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2] * inv, f[3] * inv, lo, true);
+                hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4] * inv, f[5] * inv, 0, false);
+                hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6] * inv, f[7] * inv, hi, true);
+            }
             if (live && slot >= 0) {
                 *reinterpret_cast<int2 *>(cache + (rowat * p.C + im[j].chunk) * 8) = make_int2(lo, hi);
+                if (im[j].chunk == 0) (im[j].v ? a.v_scale : a.k_scale)[rowat] = uint8_t(e + 127);
             }
-            if (live && im[j].chunk == 0) bytes[(threadIdx.x + j * kCacheThreads) >> p.cshift] = uint8_t(e + 127);
-        }
-    }
-    if constexpr (E4) {
-        // the scales of a head's neighbouring tokens are neighbouring bytes:
-        // neighbouring lanes write them
-        __syncthreads();
-        const int rows = run.row1 - row0 + 1;
-        for (int t = threadIdx.x; t < rows * 2 * a.n_kv_heads; t += kCacheThreads) {
-            const int hv = unsigned(t) / unsigned(rows), row = t - hv * rows;
-            const int rel = row * p.per_row + (hv << p.cshift) - run.rel0;  // the run's item that starts the (row, head)
-            if (rel < 0 || rel >= run.count || slots[row] < 0) continue;
-            const bool v = hv >= a.n_kv_heads;
-            const int head = v ? hv - a.n_kv_heads : hv;
-            (v ? a.v_scale : a.k_scale)[slots[row] + ((long long)head << p.pshift)] = bytes[rel >> p.cshift];
         }
     }
 }

@@ -115,8 +115,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         }
     }
     __syncthreads();
-    const int block = uniform(found[0]), q0 = uniform(found[1]), rows = uniform(found[2]);
-    int k0 = uniform(found[3]), L = uniform(found[4]);
+    // (the minima change nothing unless offsets decrease: then no row outside the arrays is touched)
+    const int block = uniform(found[0]), q0 = uniform(found[1]), rows = min(uniform(found[2]), a.n_rows - q0);
+    int k0 = uniform(found[3]), L = min(uniform(found[4]), a.n_kv_rows - k0);
     const int nq = rows * p.G;
     if (block < 0 || rows <= 0 || (long long)block * SH::QB >= nq) {
         if (p.nsplit > 1 && split == 0 && tid == 0) p.w.meta[unit] = make_int4(0, 0, 0, 0);

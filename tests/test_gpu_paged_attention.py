@@ -253,3 +253,30 @@ def test_same_bits_on_every_call_streams_and_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(eager["out"], out["out"]) and torch.equal(eager["lse"], out["lse"]), step
+
+
+def test_two_calls_at_once_on_two_streams():
+    ds = _ds()
+    rows, lens = [3, 1, 2, 6], [700, 30, 2000, 5]
+    pg = Paged([l + r for l, r in zip(lens, rows)], 2, 128, 16, BF, BF, 4)
+    dev = pg.on("cuda")
+    q = torch.randn((sum(rows) + 4, 8, 128), generator=torch.Generator().manual_seed(2)).to(BF).cuda()
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    off = offsets(rows, lead=1).cuda()
+
+    def call(**kw):
+        return ds.dspark_paged_attention(q, dev["k_cache"], dev["v_cache"], cl, dev["page_table"], row_offsets=off,
+                                         lse=True, max_rows=6, **kw)
+
+    want = call()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(call(stream=s))
+        torch.cuda.synchronize()
+        for r in got:
+            assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
+            assert bool((r["out"][:1] == 0).all()) and bool((r["out"][13:] == 0).all())

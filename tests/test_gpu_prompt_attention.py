@@ -169,3 +169,24 @@ def test_same_bits_on_every_call_stream_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(eager["out"], out["out"]) and torch.equal(eager["lse"], out["lse"]), split
+
+
+def test_two_calls_at_once_and_new_outputs_on_the_calls_stream():
+    # two streams, each with its own results and workspace, while both run; the
+    # zeros of rows that no sequence owns come from the call's own stream
+    ds = _ds()
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn((600, h, 64), generator=g).to(BF).cuda() for h in (4, 1, 1))
+    off = offsets([100, 300], lead=50).cuda()
+    want = ds.dspark_prompt_attention(q, k, v, off, lse=True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(ds.dspark_prompt_attention(q, k, v, off, lse=True, stream=s))
+        torch.cuda.synchronize()
+        for r in got:
+            assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
+            assert bool((r["out"][:50] == 0).all()) and bool((r["out"][450:] == 0).all())
