@@ -339,15 +339,19 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         hide(0, s);
         raise(largest(s));
     }
-    // Tile j with scores y, the next tile's scores into x; both tiles are seen
-    // whole by every query.  The two loops are the two halves of the work on
+    // Tile j, which every query sees whole, with scores y; the next tile's scores
+    // into x (HIDE: some of its keys may be hidden).  The two loops are the two halves of the work on
     // the matrix units; each step carries a share of the softmax and the LDS
     // reads of the steps to come, and the compiler keeps to the steps.
-    auto step = [&](int jj, f32x16_t *y, f32x16_t *x) __device__ {
+    auto step = [&](int jj, f32x16_t *y, f32x16_t *x, auto hide_tag) __device__ {
+        constexpr bool HIDE = decltype(hide_tag)::value;
         turn(jj);
         const uint32_t kb = k_base(lds0 + ((jj + 1) & 1) * S::BYTES), vb = v_base(lds0 + (2 + (jj & 1)) * S::BYTES);
         const float ms = m == kNegInf ? 0.f : m;
-        constexpr int KA = KS < 3 ? KS : 3, VA = 4;  // operands held: reads run two (K) and three (V) steps ahead
+        // operands held: reads run one (K) and two (V) steps ahead, one more at
+        // D = 64, whose steps are shorter (measured: D = 128 1966 against 1947 us at
+        // 16384 tokens with one more, D = 64 203 against 224 us at 8192)
+        constexpr int KA = D == 64 ? 3 : 2, VA = KA + 1;
         V8 ka[KA][2], va[VA], pf[4];
         auto read_k = [&](int k) __device__ {
             ka[k % KA][0] = k_frag(kb, 0, k);
@@ -381,26 +385,32 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         for (int i = 0; i < NP; ++i) {
             if (i + VA - 1 < NP) read_v(i + VA - 1);
             o[i % CB] = mma32(va[i % VA], pf[i / CB], o[i % CB]);
+            if constexpr (!HIDE) {
 #pragma unroll
-            for (int r = i * 16 / NP; r < (i + 1) * 16 / NP; ++r) mx = fmaxf(fmaxf(x[0][r], x[1][r]), mx);
+                for (int r = i * 16 / NP; r < (i + 1) * 16 / NP; ++r) mx = fmaxf(fmaxf(x[0][r], x[1][r]), mx);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
-        raise(max_x32(mx) * p.c);
+        if constexpr (HIDE) {
+            hide(jj + 1, x);
+            raise(largest(x));
+        } else {
+            raise(max_x32(mx) * p.c);
+        }
     };
-    // tiles whose successor, too, every query of the workgroup sees whole, then the rest
+    // tiles that every query of the workgroup sees whole, then the rest
     const int nfull = min(max(gmin, 0) / kKeys, ntile);
     int j = 0;
     {
         f32x16_t x[2];
         for (; j + 2 < nfull; j += 2) {
-            step(j, s, x);
-            step(j + 1, x, s);
+            step(j, s, x, std::false_type{});
+            step(j + 1, x, s, std::false_type{});
         }
-        if (j + 1 < nfull) {
-            step(j, s, x);
+        for (; j < nfull && j + 1 < ntile; ++j) {
+            step(j, s, x, std::true_type{});
             s[0] = x[0];
             s[1] = x[1];
-            ++j;
         }
     }
     for (; j < ntile; ++j) {
@@ -441,9 +451,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         }
     }
 
-    if (qi >= nq) return;
     l = sum_x32(l);
     if (parts > 1) {
+        if (qi >= nq) return;
         const long long part = (long long)unit * p.nsplit + split;
         const int q = wave * 32 + n;
         float *dst = p.w.o + (part * SH::QB + q) * D + 4 * h;
@@ -458,12 +468,31 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         }
         return;
     }
-    const long long at = (long long)(q0 + qrow) * a.n_heads + kvh * p.G + qhead;
+    // out = o / l (zeros where nothing is visible), by way of LDS: a lane holds
+    // pieces of a row, the stores are whole rows
+    const int at = (q0 + qrow) * a.n_heads + kvh * p.G + qhead;
+    if (a.lse && h == 0 && qi < nq) a.lse[at] = lse_of(m, l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const uint32_t rows_at = lds0 + wave * 32 * S::RB;
+    typedef E e4_t __attribute__((ext_vector_type(4)));
+    wg_barrier();  // every wave is done with the tiles
 #pragma unroll
     for (int c = 0; c < CB; ++c)
 #pragma unroll
-        for (int r = 0; r < 16; r += 4)
-            store_row<T>(a.out, a.lse, at, 8 * c + r / 2 + h, D, f32x4_t{o[c][r], o[c][r + 1], o[c][r + 2], o[c][r + 3]}, m, l);
+        for (int i = 0; i < 4; ++i) {
+            const e4_t x = l == 0.f ? e4_t{}
+                                    : e4_t{E(o[c][4 * i] * inv), E(o[c][4 * i + 1] * inv), E(o[c][4 * i + 2] * inv),
+                                           E(o[c][4 * i + 3] * inv)};
+            lds_write(rows_at + n * S::RB + (((4 * c + i) ^ S::k_swizzle(n)) * 16) + 8 * h, x);
+        }
+    lds_drain();
+#pragma unroll
+    for (int i = 0; i < 32 * S::CPR / 64; ++i) {
+        const int row = (i * 64 + lane) / S::CPR, ch = lane % S::CPR;
+        const u32x4v_t x = lds_read<u32x4v_t>(rows_at + row * S::RB + ((ch ^ S::k_swizzle(row)) * 16));
+        const long long dst = __shfl(at, row);
+        if (wq0 + row < nq) *reinterpret_cast<u32x4v_t *>(static_cast<E *>(a.out) + dst * D + 8 * ch) = x;
+    }
 }
 
 // The units whose keys were split: workgroup (unit, y) merges the partials of
