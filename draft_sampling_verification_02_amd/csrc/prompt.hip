@@ -64,7 +64,7 @@ struct PromptShape {
     static constexpr int QB = kPromptQueries;
     static constexpr int LPT = kKeys * S::CPR / NT;          // loads a thread issues for K (and for V)
     static constexpr int LDS = 4 * S::BYTES;                  // two K tiles, two V tiles
-    static constexpr int EU = D >= 256 ? 1 : 2;  // waves a SIMD
+    static constexpr int EU = D >= 256 ? 1 : D == 64 ? 3 : 2;  // waves a SIMD
     static_assert(LPT * NT == kKeys * S::CPR && LDS <= 160 * 1024, "tile loads");
 };
 
@@ -348,10 +348,10 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         turn(jj);
         const uint32_t kb = k_base(lds0 + ((jj + 1) & 1) * S::BYTES), vb = v_base(lds0 + (2 + (jj & 1)) * S::BYTES);
         const float ms = m == kNegInf ? 0.f : m;
-        // operands held: reads run one (K) and two (V) steps ahead, one more at
-        // D = 64, whose steps are shorter (measured: D = 128 1966 against 1947 us at
-        // 16384 tokens with one more, D = 64 203 against 224 us at 8192)
-        constexpr int KA = D == 64 ? 3 : 2, VA = KA + 1;
+        // operands held: reads run one (K) and two (V) steps ahead (one more of each
+        // is 1% slower at D = 128, and at D = 64 costs the third wave of a SIMD its
+        // registers: 163 against 175 us at 8192 tokens, 16/4 heads)
+        constexpr int KA = 2, VA = 3;
         V8 ka[KA][2], va[VA], pf[4];
         auto read_k = [&](int k) __device__ {
             ka[k % KA][0] = k_frag(kb, 0, k);
