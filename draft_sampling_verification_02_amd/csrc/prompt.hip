@@ -496,27 +496,35 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
 }
 
 // The units whose keys were split: workgroup (unit, y) merges the partials of
-// 32 of its queries in their order, D / 4 threads a query.
+// 1024 / D of its queries in their order, D / 4 threads a query, eight loads in
+// flight.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p) {
-    constexpr int QB = kPromptQueries, TPQ = D / 4;
+    constexpr int QB = kPromptQueries, TPQ = D / 4, FLY = 8;
     const int4 unit = p.w.meta[blockIdx.x];
     const int parts = unit.x;
     if (parts <= 1) return;
-    const int c4 = threadIdx.x % TPQ;
-    for (int q = blockIdx.y * 32 + threadIdx.x / TPQ; q < int(blockIdx.y) * 32 + 32; q += 256 / TPQ) {
-        const int qi = unit.w * QB + q;
-        if (qi >= unit.z) return;
-        float m = kNegInf, l = 0.f;
-        f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < parts; ++i) {
-            const long long part = (long long)blockIdx.x * p.nsplit + i;
-            merge_partial(m, l, o, p.w.ml[part * 2 * QB + q], p.w.ml[part * 2 * QB + QB + q],
-                          *reinterpret_cast<const f32x4_t *>(p.w.o + (part * QB + q) * D + 4 * c4));
+    const int c4 = threadIdx.x % TPQ, q = blockIdx.y * (256 / TPQ) + threadIdx.x / TPQ;
+    const int qi = unit.w * QB + q;
+    if (qi >= unit.z) return;
+    float m = kNegInf, l = 0.f;
+    f32x4_t o = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < parts; i0 += FLY) {
+        float pm[FLY], pl[FLY];
+        f32x4_t po[FLY];
+#pragma unroll
+        for (int i = 0; i < FLY; ++i) {
+            const long long part = (long long)blockIdx.x * p.nsplit + min(i0 + i, parts - 1);
+            pm[i] = p.w.ml[part * 2 * QB + q];
+            pl[i] = p.w.ml[part * 2 * QB + QB + q];
+            po[i] = *reinterpret_cast<const f32x4_t *>(p.w.o + (part * QB + q) * D + 4 * c4);
         }
-        const int row = qi / p.G, kvh = blockIdx.x % p.a.n_kv_heads;
-        store_row<T>(p.a.out, p.a.lse, (long long)(unit.y + row) * p.a.n_heads + kvh * p.G + (qi - row * p.G), c4, D, o, m, l);
+#pragma unroll
+        for (int i = 0; i < FLY; ++i)
+            if (i0 + i < parts) merge_partial(m, l, o, pm[i], pl[i], po[i]);
     }
+    const int row = qi / p.G, kvh = blockIdx.x % p.a.n_kv_heads;
+    store_row<T>(p.a.out, p.a.lse, (long long)(unit.y + row) * p.a.n_heads + kvh * p.G + (qi - row * p.G), c4, D, o, m, l);
 }
 
 template <typename T, int D>
@@ -524,7 +532,7 @@ hipError_t launch_prompt_typed(const PromptParams &p, hipStream_t s) {
     const unsigned units = unsigned(p.slots) * p.a.n_kv_heads;
     launch_kernel("prompt_attention", prompt_kernel<T, D>, dim3(units * p.nsplit), dim3(64 * kPromptWaves), s, p);
     if (p.nsplit > 1)
-        launch_kernel("prompt_join", prompt_join_kernel<T, D>, dim3(units, kPromptQueries / 32), dim3(256), s, p);
+        launch_kernel("prompt_join", prompt_join_kernel<T, D>, dim3(units, kPromptQueries * D / 1024), dim3(256), s, p);
     return hipGetLastError();
 }
 
