@@ -720,7 +720,10 @@ size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv
     size_t bytes = 0;
     for (const bool e4 : {false, true}) {
         size_t need = 0;
-        paged_carve(nullptr, paged_plan(max_rows, n_heads, n_kv_heads, head_dim, e4, 1, DSPARK_MAX_CACHE_TOKENS), head_dim, &need);
+        // the largest grid, whatever the batch
+        const PagedSizes z{DSPARK_MAX_ROWS, DSPARK_MAX_BATCH, DSPARK_MAX_CACHE_TOKENS, max_rows, n_heads, n_kv_heads,
+                           head_dim, e4};
+        paged_carve(nullptr, paged_plan(z), head_dim, &need);
         bytes = need > bytes ? need : bytes;
     }
     return bytes;
@@ -743,8 +746,9 @@ int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int
     if (!row_stride_ok(q_stride, n_heads, head_dim)) return DSPARK_ERR_ARG;
     st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
     if (st != DSPARK_OK) return st;
-    const PagedPlan plan = paged_plan(max_rows, n_heads, n_kv_heads, head_dim, cache_dtype == DSPARK_E4M3, B,
-                                      (long long)max_pages * page_size);
+    const PagedSizes z{n_rows, B, (long long)max_pages * page_size, max_rows, n_heads, n_kv_heads, head_dim,
+                       cache_dtype == DSPARK_E4M3};
+    const PagedPlan plan = paged_plan(z);
     size_t need = 0;
     paged_carve(nullptr, plan, head_dim, &need);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;

@@ -272,10 +272,14 @@ struct PagedPlan {
     int waves;     // of a workgroup
     int grid;      // workgroups
     int whole;     // 1: a workgroup takes whole (request, head, query group) segments, nothing to join
+    int long_runs; // a segment may have many partials
 };
-// table_tokens: max_pages * page_size, the longest a request can be
-PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long requests,
-                     long long table_tokens);
+struct PagedSizes {
+    long long n_rows, requests, table_tokens;  // table_tokens: max_pages * page_size, the longest a request can be
+    int max_rows, n_heads, n_kv_heads, head_dim;
+    bool e4;
+};
+PagedPlan paged_plan(const PagedSizes &z);
 struct PagedWork {
     int4 *meta;       // [grid] the segment a workgroup left unfinished at its end
     float *ml;        // [2 grid, 2, queries] partial maxima and sums

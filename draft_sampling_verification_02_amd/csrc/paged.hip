@@ -25,6 +25,8 @@
 // start or end inside a segment: it then leaves a partial result (maximum, sum,
 // unnormalised product), and paged_join merges a segment's partials in their
 // order, so results do not depend on timing.
+#include <algorithm>
+
 #include "attend.hpp"
 #include "dspark.h"
 #include "internal.hpp"
@@ -38,7 +40,6 @@ constexpr int kUnit = 128;        // tokens of a work unit: a tile for each of f
 constexpr int kMinUnits = 2;      // units a workgroup takes at least
 constexpr int kWholeTokens = 512;   // tables up to this long are not split,
 constexpr int kWideTokens = 1024;   // nor up to this by eight waves a segment
-constexpr int kJoinQueries = 4;   // queries of a join workgroup
 
 typedef __attribute__((address_space(4))) const int32_t *ConstInts;  // read by scalar loads
 
@@ -586,19 +587,20 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
     }
 }
 
-// The segments that workgroups left unfinished: workgroup (i, y) merges
-// kJoinQueries queries of the segment that workgroup i started and its
-// successors went on with, in their order.  64 threads a query take the
-// partials in turn, D / 4 threads each.
-template <typename T, int D, int QB>
-__global__ __launch_bounds__(64 * kJoinQueries) void paged_join_kernel(PagedParams p) {
-    constexpr int TPP = D / 4, LANES = 64 / TPP;  // threads a partial, partials in flight
+// The segments that workgroups left unfinished: workgroup (i, y) merges KQ
+// queries of the segment that workgroup i started and its successors went on
+// with, in an order that the split alone fixes.  256 / KQ threads a query take
+// the partials in turn, D / 4 threads each, four loads in flight.
+template <typename T, int D, int QB, int KQ>
+__global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p) {
+    constexpr int TPQ = 256 / KQ, TPP = D / 4, LANES = TPQ / TPP;  // threads a query, a partial; partials in turn
+    __shared__ float red[KQ == 1 ? 4 : 1][D + 2];
     const int4 seg = p.w.meta[blockIdx.x];
     if (seg.x == 0) return;
     const Request rq = request_of<QB>(p, seg.y);
-    const int lane = threadIdx.x & 63, q = blockIdx.y * kJoinQueries + (threadIdx.x >> 6);
+    const int lane = threadIdx.x % TPQ, q = blockIdx.y * KQ + threadIdx.x / TPQ;
     const int qi = seg.w * QB + q;
-    if (qi >= rq.rows * p.G) return;
+    if (qi >= rq.rows * p.G) return;  // (uniform where the waves of a query meet below)
     const int grp = lane / TPP, c4 = lane % TPP;
     const int parts = seg.x + 1;
     float m = kNegInf, l = 0.f;
@@ -625,6 +627,22 @@ __global__ __launch_bounds__(64 * kJoinQueries) void paged_join_kernel(PagedPara
         const f32x4_t o2 = f32x4_t{__shfl_xor(o[0], s), __shfl_xor(o[1], s), __shfl_xor(o[2], s), __shfl_xor(o[3], s)};
         merge_partial(m, l, o, m2, l2, o2);
     }
+    if constexpr (KQ == 1) {
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) < TPP) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) red[wave][4 * c4 + i] = o[i];
+            if (c4 == 0) {
+                red[wave][D] = m;
+                red[wave][D + 1] = l;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x >= TPP) return;
+        for (int w = 1; w < 4; ++w)
+            merge_partial(m, l, o, red[w][D], red[w][D + 1],
+                          f32x4_t{red[w][4 * c4], red[w][4 * c4 + 1], red[w][4 * c4 + 2], red[w][4 * c4 + 3]});
+    }
     if (grp == 0)
         store_row<T>(p.a.out, p.a.lse, (long long)(rq.row0 + qi / p.G) * p.a.n_heads + seg.z * p.G + qi % p.G, c4, D, o, m, l);
 }
@@ -645,9 +663,13 @@ hipError_t launch_paged_typed(const PagedParams &pp, const PagedPlan &plan, hipS
             done = true;
         }
     if (!done) launch_kernel("paged_attention", paged_kernel<T, E4, D, NQ, 4>, grid, dim3(256), s, pp);
-    if (!plan.whole)
-        launch_kernel("paged_join", paged_join_kernel<T, D, 16 * NQ>, dim3(plan.grid - 1, 16 * NQ / kJoinQueries),
-                      dim3(64 * kJoinQueries), s, pp);
+    if (!plan.whole && plan.grid > 1) {
+        // long runs of partials (few segments): a workgroup a query; else four
+        if (plan.long_runs)
+            launch_kernel("paged_join", paged_join_kernel<T, D, 16 * NQ, 1>, dim3(plan.grid - 1, 16 * NQ), dim3(256), s, pp);
+        else
+            launch_kernel("paged_join", paged_join_kernel<T, D, 16 * NQ, 4>, dim3(plan.grid - 1, 4 * NQ), dim3(256), s, pp);
+    }
     return hipGetLastError();
 }
 
@@ -678,21 +700,25 @@ hipError_t launch_paged_dim(const PagedParams &pp, const PagedPlan &plan, hipStr
 // The query blocks cover a request's rows times its group where they fit
 // (16 to 64 queries; 32 at D = 256, whose accumulators are twice as long);
 // more rows take several groups, which read the cache again.
-PagedPlan paged_plan(int max_rows, int n_heads, int n_kv_heads, int head_dim, bool e4, long long requests,
-                     long long table_tokens) {
+PagedPlan paged_plan(const PagedSizes &z) {
     PagedPlan p{};
-    const long long queries = (long long)max_rows * (n_heads / n_kv_heads);
-    const int most = head_dim >= 256 ? 2 : 4;
+    const long long queries = (long long)z.max_rows * (z.n_heads / z.n_kv_heads);
+    const int most = z.head_dim >= 256 ? 2 : 4;
     p.qblocks = queries <= 16 ? 1 : (queries <= 32 || most == 2 ? 2 : 4);
     p.waves = 4;
-    p.grid = 256 * paged_per_cu(e4, head_dim, p.qblocks, 4);
-    p.whole = table_tokens <= kWholeTokens;
+    p.grid = 256 * paged_per_cu(z.e4, z.head_dim, p.qblocks, 4);
+    p.whole = z.table_tokens <= kWholeTokens;
     // few short segments: eight waves each, and no second launch
-    if (table_tokens > kUnit && table_tokens <= kWideTokens && requests * n_kv_heads <= 256 &&
-        paged_per_cu(e4, head_dim, p.qblocks, 8) >= 1) {
+    if (z.table_tokens > kUnit && z.table_tokens <= kWideTokens && z.requests * z.n_kv_heads <= 256 &&
+        paged_per_cu(z.e4, z.head_dim, p.qblocks, 8) >= 1) {
         p.whole = 1;
         p.waves = 8;
     }
+    // no more workgroups than there can be work for
+    const long long segments = z.n_rows * z.n_heads / (16 * p.qblocks) + z.requests * z.n_kv_heads;
+    const long long units = p.whole ? segments : segments * ((z.table_tokens + kUnit - 1) / kUnit);
+    p.grid = int(std::min<long long>(p.grid, p.whole ? units : (units + kMinUnits - 1) / kMinUnits));
+    p.long_runs = segments * 8 <= p.grid;
     return p;
 }
 
@@ -714,7 +740,7 @@ hipError_t launch_paged(const PagedArgs &a, const PagedPlan &plan, const PagedWo
     p.pshift = log2_of(a.page_size);
     p.whole = plan.whole;
     p.unit = kUnit;
-    const long long segments = (long long)a.n_rows * a.n_heads / (16 * plan.qblocks) + (long long)a.B * a.n_kv_heads;
+    const long long segments = (long long)a.n_rows * a.n_heads / (16 * plan.qblocks) + (long long)a.B * a.n_kv_heads;  // at most
     const long long tokens = (long long)a.max_pages * a.page_size;
     while (segments * (tokens / p.unit + 1) > INT32_MAX) p.unit *= 2;
     p.c = a.scale * kLog2e;
