@@ -116,6 +116,11 @@ struct ProbType<T, true> {
     // needs bfloat16's exponent
     using type = TypeBf16;
 };
+// float16 rows over an 8-bit cache: bfloat16 would leave the probabilities
+// three bits short of the rows' own rounding, so a second bfloat16 carries the
+// rest of each (2^-16 in all) through a second product
+template <typename T, bool E4>
+constexpr bool kTwoTerms = E4 && std::is_same<T, TypeF16>::value;
 
 // LDS of a workgroup of nw waves and how many share a compute unit.
 constexpr int paged_body(bool e4, int d, int nq, int nw) {
@@ -414,7 +419,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
 
             // ---- running maximum, probabilities
             const bool masked = t + kTokens > lim_min || bad_now != 0;
-            P8 pf[NQ];
+            P8 pf[NQ], pr_rest[kTwoTerms<T, E4> ? NQ : 1];
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 if (masked) {
@@ -450,6 +455,10 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                 }
                 using E = typename PT::E;
                 pf[q] = P8{E(pr[0]), E(pr[1]), E(pr[2]), E(pr[3]), E(pr[4]), E(pr[5]), E(pr[6]), E(pr[7])};
+                if constexpr (kTwoTerms<T, E4>) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pr_rest[q][e] = E(pr[e] - float(pf[q][e]));
+                }
             }
 
             // ---- products with V
@@ -518,7 +527,10 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
             for (int c = 0; c < CB; ++c) {
                 const P8 vf = v_frag(vbase, c);
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) o[q][c] = mma16(vf, pf[q], o[q][c]);
+                for (int q = 0; q < NQ; ++q) {
+                    o[q][c] = mma16(vf, pf[q], o[q][c]);
+                    if constexpr (kTwoTerms<T, E4>) o[q][c] = mma16(vf, pr_rest[q], o[q][c]);
+                }
             }
             lds_drain();
             if (more) issue_v(i + 1, na, nb);

@@ -474,7 +474,8 @@ size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv
  * that sees no token gives zeros and lse = -inf.  Infinities and NaN in tokens
  * a row does not see, or in unused slots, do not reach it.  Scores, softmax
  * sums and products are kept in float32; probabilities enter the V product in
- * the rows' type (bfloat16 for 8-bit caches).
+ * the rows' type (over 8-bit caches in bfloat16, for float16 rows in two
+ * bfloat16 terms).
  *   q           device [n_rows, n_heads, head_dim] of `dtype`, row stride q_stride
  *   n_heads     a multiple of n_kv_heads, at most DSPARK_MAX_HEADS
  *   max_rows    >= 1: how many rows a request usually has at most (1 for

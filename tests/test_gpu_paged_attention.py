@@ -25,7 +25,8 @@ def _expect(pg, q, rows, lens, G, causal, scale, dtype, off0=0, table_tokens=Non
     out = torch.full((N, Hq, D), math.nan, dtype=torch.float64)
     lse = torch.full((N, Hq), math.nan, dtype=torch.float64)
     tol, ltol = torch.zeros_like(out), torch.zeros_like(lse)
-    up = U[BF] if pg.cache == E4 else U[dtype]
+    # over 8 bits: bfloat16 probabilities, with a second term beside float16 rows
+    up = (U[BF] if dtype == BF else U[BF] ** 2) if pg.cache == E4 else U[dtype]
     at = off0
     for b, (r, past) in enumerate(zip(rows, lens)):
         total = past + r if past >= 0 else 0
