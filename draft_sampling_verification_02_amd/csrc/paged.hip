@@ -13,18 +13,31 @@
 // What bounds it: the cache is read once, 4 D bytes (2 D + 2 in 8 bits) a
 // token and head against 4 D G flops for G queries -- memory, for any group a
 // request of a round has.  So the kernel is built to keep loads in flight: a
-// workgroup of four independent waves, each streaming its own tiles of 32
-// tokens through a ring of LDS buffers with direct loads (no registers held,
-// no barriers), K refilled as soon as its scores are taken, V as soon as its
-// product is.  G query heads times the request's rows share every tile.
+// workgroup of four independent waves, each streaming tiles of 32 tokens
+// through an LDS buffer of its own with direct loads (no registers held, no
+// barriers), K refilled as soon as its scores are taken, V as soon as its
+// product is; two to three workgroups share a compute unit, so that one wave's
+// arithmetic runs under the others' loads.  (Two tiles a wave in flight and
+// half the workgroups measured the same for single rows, and 470 against 413 us
+// for the verify rows of 256 requests, whose arithmetic is longer.)  G query
+// heads times the request's rows share every tile.
 //
 // Work is the concatenation of all (request, head, query group) segments, cut
 // into units of 128 tokens and dealt to the workgroups in equal contiguous
 // ranges, whatever the requests' lengths (each workgroup finds its range from
 // the lengths on the device, so a captured call follows them).  A range may
 // start or end inside a segment: it then leaves a partial result (maximum, sum,
-// unnormalised product), and paged_join merges a segment's partials in their
-// order, so results do not depend on timing.
+// unnormalised product), and paged_join merges a segment's partials in an
+// order that the split alone fixes, so results do not depend on timing.  Short
+// tables are not split: a workgroup takes whole segments, and one launch does.
+//
+// Measured (MI355X; 32 query and 8 key-value heads, D = 128, pages of 16):
+// 256 requests, one row, 16 to 8192 tokens, bfloat16: 726 us for 4.20 GB,
+// 5.8 TB/s (no LDS bank conflicts); the same with 1 to 6 rows and up to 4096
+// tokens 402 us for 2.05 GB, 5.1 TB/s; four requests of 60,000 to 131,000 tokens
+// over 8 bits, 64 query heads: 119 us for 620 MB, 5.2 TB/s; one request of 500
+// tokens 10 us, of 8000 tokens 11 + 4 us, where the chain of dependent loads
+// (lengths, page, tile) is what there is to wait for: 7 us with a single token.
 #include <algorithm>
 
 #include "attend.hpp"
@@ -38,8 +51,19 @@ namespace {
 constexpr int kTokens = 32;       // tokens of a wave's tile
 constexpr int kUnit = 128;        // tokens of a work unit: a tile for each of four waves
 constexpr int kMinUnits = 2;      // units a workgroup takes at least
-constexpr int kWholeTokens = 512;   // tables up to this long are not split,
-constexpr int kWideTokens = 1024;   // nor up to this by eight waves a segment
+// Tables up to kWholeTokens are not split: a workgroup walks whole segments, of
+// eight waves where there are at most kFewSegments of them.  Measured, us a call
+// (32/8 heads, D = 128, one row, all requests of the length; split / whole by
+// four waves / by eight):
+//   8 segments:    500 tokens 11.9 / 10.8 / 9.3     1000: 12.5 / 15.6 / 12.4    2000: 12.2 / 24.7 / 18.1
+//   64 segments:   500        12.4 / 11.5 / 10.1    1000: 14.3 / 16.6 / 13.5    2000: 18.8 / 26.3 / 18.9
+//   256 segments:  500        19.1 / 15.5 / 16.1    1000: 32.7 / 28.0 / 28.2    2000: 54.9 / 49.3 / 49.6
+//   1024 segments: 500        55.1 / 52.4 / 58.1    1000: 97.0 / 93.9 / 97.3    2000: 182 / 180 / 181
+// and with lengths from 16 up to 1000 tokens: 256 segments 22.1 / 18.9 / 18.1,
+// 1024 segments 67.8 / 61.8 / 62.4, 2048 segments 115.9 / 120.0 / 117.3; up to
+// 500: 17.6 / 12.6 / 12.1, 41.3 / 34.7 / 40.1 and 78.1 / 69.2 / 76.7.
+constexpr int kWholeTokens = 1024;
+constexpr int kFewSegments = 128;
 
 typedef __attribute__((address_space(4))) const int32_t *ConstInts;  // read by scalar loads
 
@@ -691,7 +715,7 @@ hipError_t launch_paged_queries(const PagedParams &pp, const PagedPlan &plan, hi
         case 1: return launch_paged_typed<T, E4, D, 1>(pp, plan, s);
         case 2: return launch_paged_typed<T, E4, D, 2>(pp, plan, s);
         default:
-            if constexpr (D < 256)
+            if constexpr (D < (E4 ? 128 : 256))
                 return launch_paged_typed<T, E4, D, 4>(pp, plan, s);
             else
                 return hipErrorInvalidValue;
@@ -715,21 +739,27 @@ hipError_t launch_paged_dim(const PagedParams &pp, const PagedPlan &plan, hipStr
 PagedPlan paged_plan(const PagedSizes &z) {
     PagedPlan p{};
     const long long queries = (long long)z.max_rows * (z.n_heads / z.n_kv_heads);
-    const int most = z.head_dim >= 256 ? 2 : 4;
+    // Every block of queries walks the keys again, so the fewest blocks win until
+    // the registers of 64 queries leave too few waves.  Us a call in blocks of
+    // 16 / 32 / 64 queries (64 requests behind 2000 tokens, 8 key heads, D = 128):
+    // 24 queries 200 / 121 / 124, 40 281 / 214 / 127, 68 448 / 304 / 228; from an
+    // 8-bit cache 24 105 / 75 / 135, 40 143 / 125 / 138, 68 232 / 168 / 249, and
+    // with D = 64 48 queries 84 / 87 / 75.
+    const int most = z.head_dim >= (z.e4 ? 128 : 256) ? 2 : 4;
     p.qblocks = queries <= 16 ? 1 : (queries <= 32 || most == 2 ? 2 : 4);
     p.waves = 4;
     p.grid = 256 * paged_per_cu(z.e4, z.head_dim, p.qblocks, 4);
     p.whole = z.table_tokens <= kWholeTokens;
-    // few short segments: eight waves each, and no second launch
-    if (z.table_tokens > kUnit && z.table_tokens <= kWideTokens && z.requests * z.n_kv_heads <= 256 &&
-        paged_per_cu(z.e4, z.head_dim, p.qblocks, 8) >= 1) {
-        p.whole = 1;
+    if (p.whole && z.table_tokens > kUnit && z.requests * z.n_kv_heads <= kFewSegments &&
+        paged_per_cu(z.e4, z.head_dim, p.qblocks, 8) >= 1)
         p.waves = 8;
-    }
     // no more workgroups than there can be work for
     const long long segments = z.n_rows * z.n_heads / (16 * p.qblocks) + z.requests * z.n_kv_heads;
     const long long units = p.whole ? segments : segments * ((z.table_tokens + kUnit - 1) / kUnit);
     p.grid = int(std::min<long long>(p.grid, p.whole ? units : (units + kMinUnits - 1) / kMinUnits));
+    // Eight or more partials a segment: a workgroup a query, which reads them side
+    // by side (one request of 32,000 tokens: join 9.2 -> 4.1 us); else four
+    // queries share one (64 requests of 1 to 6 rows: 4.7 against 8.2 us).
     p.long_runs = segments * 8 <= p.grid;
     return p;
 }

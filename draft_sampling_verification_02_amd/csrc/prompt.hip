@@ -10,15 +10,28 @@
 //
 // What bounds it: 4 D flops for every (query, key) pair against 16-bit K and V
 // tiles that a whole workgroup shares -- the matrix units, with the
-// exponentials of the softmax beside them.  A workgroup of up to four waves
-// takes 32 queries a wave: a query is a (row, head of the group) pair, heads
-// fastest, so that the heads of a group share the K and V tiles and a
-// workgroup covers few rows (the causal diagonal wastes little).  Tiles of 64
-// tokens come in by direct loads through a ring of LDS buffers, one barrier a
-// tile.  Two waves a SIMD: one's softmax runs beside the other's products.
-// Workgroups of one key-value head are neighbours modulo the XCDs where the
-// head count allows it, and the last rows of a sequence, which see the most
-// keys, go first.
+// exponentials of the softmax beside them, and the clock, which falls to
+// 1.7 GHz under this load (as it does under a large library product).  A
+// workgroup of four waves takes 32 queries a wave: a query is a (row, head of
+// the group) pair, heads fastest, so that the heads of a group share the K and
+// V tiles and a workgroup covers few rows (the causal diagonal wastes little).
+// Tiles of 64 tokens come in by direct loads, two K and two V buffers, one
+// barrier a tile.  The products of tile j + 1 with the queries are taken
+// beside the exponentials of tile j in one instruction stream, in steps laid
+// out by hand (the compiler's own order left the matrix units waiting on LDS
+// reads); two workgroups share a compute unit, so that one's start and end run
+// beside the other's middle.  Workgroups of one key-value head are neighbours
+// modulo the XCDs where the head count allows it, and the last rows of a
+// sequence, which see the most keys, go first.  Where the query blocks do not
+// fill the chip, their keys are split and prompt_join merges the parts.
+//
+// Measured (MI355X, bfloat16, 32 query and 8 key-value heads, D = 128): one
+// prompt of 16384 tokens 1914 us, 1149 TFLOP/s, matrix units busy 64% of
+// 1.72 GHz (a 16384-cubed library product reaches 1386 TFLOP/s, 73% of
+// 1.71 GHz); 16 prompts of 100 to 4100 tokens 943-1065 us over the boxes, 890 to
+// 1005 TFLOP/s, the rest being starts, ends and diagonal tiles.  16/4 heads at
+// 8192 tokens: D = 64 163 us, 843 TFLOP/s; D = 256 626 us, 879 TFLOP/s (one
+// wave a SIMD: the accumulators take half its registers).
 #include <algorithm>
 
 #include "attend.hpp"
@@ -32,7 +45,6 @@ namespace {
 constexpr int kKeys = 64;      // tokens of a tile
 constexpr int kPromptWaves = 4;                      // of a workgroup
 constexpr int kPromptQueries = 32 * kPromptWaves;    // queries of a workgroup
-constexpr int kPromptTarget = 640;                   // workgroups a split call aims at
 constexpr int kMinTiles = 2;                         // tiles of a split at least
 constexpr float kSlack = 8.f;  // growth of the running maximum that is left alone, base-2 units
 
@@ -547,15 +559,30 @@ hipError_t launch_prompt_dim(const PromptParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Query blocks that do not fill the chip (two workgroups a compute unit) have
-// their keys split, as far as the keys go.
+// Into how many ranges the keys of a query block are cut.  A block of T tiles
+// takes about 0.85 us a tile (D = 128, in proportion for others) while there are
+// at most 512 blocks (two a compute unit), and in proportion more beyond; a cut
+// adds a launch, 5 us, and writes and reads 64 KiB a part.  The cheapest cut is
+// taken; the average sequence stands for all, as lengths are on the device.
+// Measured, us a call in 1 / 2 / 4 / 8 / 16 parts (D = 128): 18 rows behind 4000
+// keys, 8/1 heads 39.7 / 26.1 / 18.8 / 14.6 / 13.8; four times 64 rows behind
+// 2000, 32/8 heads 32.8 / 25.4 / 23.7 / 27.1 / 36.7; one prompt of 2048 rows, 8/8
+// heads 37.8 / 31.0 / 29.3 / 40.8 / 58.8; of 4096 68.5 / 59.3 / 65.9; of 1024
+// rows, 32/8 heads 24.3 / 30.5 / 39.3; of 512 14.9 / 18.1 / 19.7.
 PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim) {
     PromptPlan p{};
     p.slots = int((long long)n_rows * (n_heads / n_kv_heads) / kPromptQueries + B);
-    const long long units = (long long)p.slots * n_kv_heads;
-    const long long want = units >= kPromptTarget / 2 ? 1 : (kPromptTarget + units - 1) / units;
-    const long long most = 2LL * n_kv_rows / B / (kMinTiles * kKeys);  // twice the average sequence
-    p.nsplit = int(std::max(1LL, std::min(std::min(want, most), 64LL)));
+    const double units = (p.slots - 0.5 * B) * n_kv_heads;  // half of the last blocks are there on average
+    const double tiles = double(n_kv_rows) / B / kKeys, wide = head_dim / 128.0;
+    double best = 1e30;
+    for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+        if (s > 1 && tiles < s * kMinTiles) break;
+        const double cost = 0.85 * wide * tiles / s * std::max(1.0, units * s / 512) + (s > 1 ? 5 + 0.033 * wide * units * s : 0.0);
+        if (cost < best) {
+            best = cost;
+            p.nsplit = s;
+        }
+    }
     return p;
 }
 
