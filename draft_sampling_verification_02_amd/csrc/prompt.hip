@@ -30,7 +30,7 @@
 // 1.72 GHz (a 16384-cubed library product reaches 1386 TFLOP/s, 73% of
 // 1.71 GHz); 16 prompts of 100 to 4100 tokens 943-1065 us over the boxes, 890 to
 // 1005 TFLOP/s, the rest being starts, ends and diagonal tiles.  16/4 heads at
-// 8192 tokens: D = 64 163 us, 843 TFLOP/s; D = 256 626 us, 879 TFLOP/s (one
+// 8192 tokens: D = 64 168 us, 818 TFLOP/s; D = 256 626 us, 879 TFLOP/s (one
 // wave a SIMD: the accumulators take half its registers).
 #include <algorithm>
 
@@ -76,7 +76,9 @@ struct PromptShape {
     static constexpr int QB = kPromptQueries;
     static constexpr int LPT = kKeys * S::CPR / NT;          // loads a thread issues for K (and for V)
     static constexpr int LDS = 4 * S::BYTES;                  // two K tiles, two V tiles
-    static constexpr int EU = D >= 256 ? 1 : D == 64 ? 3 : 2;  // waves a SIMD
+    // Waves a SIMD.  (Three at D = 64 spill: 164 against 168 us at 8192 tokens, but
+    // 13.3 against 11.2 us for 32 prompts of up to 200 rows, 16/4 heads.)
+    static constexpr int EU = D >= 256 ? 1 : 2;
     static_assert(LPT * NT == kKeys * S::CPR && LDS <= 160 * 1024, "tile loads");
 };
 
@@ -361,8 +363,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         const uint32_t kb = k_base(lds0 + ((jj + 1) & 1) * S::BYTES), vb = v_base(lds0 + (2 + (jj & 1)) * S::BYTES);
         const float ms = m == kNegInf ? 0.f : m;
         // operands held: reads run one (K) and two (V) steps ahead (one more of each
-        // is 1% slower at D = 128, and at D = 64 costs the third wave of a SIMD its
-        // registers: 163 against 175 us at 8192 tokens, 16/4 heads)
+        // is 1% slower at D = 128 and the same at D = 64)
         constexpr int KA = 2, VA = 3;
         V8 ka[KA][2], va[VA], pf[4];
         auto read_k = [&](int k) __device__ {
