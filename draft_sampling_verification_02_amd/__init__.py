@@ -624,6 +624,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
 def _requests(row_offsets, n_rows, page_table, device):
     """Checks the request arrays; returns (B, max_pages)."""
     int32 = _torch().int32
+    if not isinstance(page_table, _torch().Tensor):
+        raise TypeError("page_table: expected a torch tensor")
     if page_table.dim() != 2:
         raise ValueError("page_table: [B, max_pages]")
     B, max_pages = page_table.shape
@@ -723,6 +725,8 @@ def _attention_outputs(q, lse, out, every_row, stream):
         if lse:
             shapes["lse"] = (shape[:2], torch.float32)
         out = _new_outputs(shapes, dev, every_row, stream)
+    elif lse and "lse" not in out:
+        out.update(_new_outputs({"lse": (shape[:2], torch.float32)}, dev, every_row, stream))
     _dense(out["out"], "out", q.dtype, shape, dev)
     if "lse" in out:
         _dense(out["lse"], "lse", torch.float32, shape[:2], dev)
@@ -733,6 +737,8 @@ def _attention_workspace(nbytes, device, workspace, out, stream):
     if workspace is not None:
         out["workspace"] = workspace
     ws = out.get("workspace")
+    if ws is not None:
+        _dense(ws, "workspace", _torch().uint8, getattr(ws, "shape", None), device)
     if nbytes and (ws is None or ws.numel() < nbytes):  # 0 bytes: the call reports why
         with _torch().cuda.stream(stream):
             ws = out["workspace"] = _workspace(nbytes, device, None)
@@ -753,7 +759,7 @@ def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_of
     values).  max_rows: rows a request usually has at most (None: the average,
     rounded up); scale: None = D^-1/2.  Returns {"out"[, "lse"], "workspace"};
     pass ``out`` (a previous result) to reuse its buffers."""
-    if out is not None and stream is None:
+    if out is not None and stream is None and (not lse or "lse" in out):
         st = (_short or _load_marshal()).paged_attention(
             q, k_cache, v_cache, cache_len, page_table, row_offsets, k_scale, v_scale, scale, causal, max_rows,
             out["out"], out.get("lse"), workspace if workspace is not None else out.get("workspace"))
@@ -796,7 +802,7 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
     kv_offsets[b + 1] - 1 of k and v (None: the same rows).  Its query rows are
     the last positions of its keys.  scale: None = D^-1/2.  Returns {"out"[,
     "lse"], "workspace"}; pass ``out`` (a previous result) to reuse its buffers."""
-    if out is not None and stream is None:
+    if out is not None and stream is None and (not lse or "lse" in out):
         st = (_short or _load_marshal()).prompt_attention(
             q, k, v, row_offsets, kv_offsets, scale, causal, out["out"], out.get("lse"),
             workspace if workspace is not None else out.get("workspace"))
@@ -813,6 +819,8 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
     n_kv, Hkv, d = k.shape
     if v.shape != k.shape or d != D:
         raise ValueError(f"k/v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [rows, heads, {D}]")
+    if not isinstance(row_offsets, torch.Tensor):
+        raise TypeError("row_offsets: expected a torch tensor")
     B = row_offsets.numel() - 1
     _dense(row_offsets, "row_offsets", torch.int32, (B + 1,), dev)
     if kv_offsets is not None:

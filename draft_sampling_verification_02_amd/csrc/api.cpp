@@ -624,6 +624,12 @@ int cache_geometry(int dtype, const int32_t *row_offsets, int n_rows, int B, int
     return DSPARK_OK;
 }
 
+// K and V of a write or read in pieces of 16 bytes: a launch holds fewer than
+// 2^32 threads, each with four of them.
+bool cache_launchable(int n_rows, int n_kv_heads, int head_dim) {
+    return int64_t(n_rows) * 2 * n_kv_heads * (head_dim / 8) < (int64_t(1) << 34) - 1024;
+}
+
 int cache_buffers(const void *k_cache, const void *v_cache, const uint8_t *k_scale, const uint8_t *v_scale,
                   int cache_dtype) {
     if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return DSPARK_ERR_ARG;
@@ -639,6 +645,12 @@ int head_geometry(int n_rows, int n_heads, int n_kv_heads) {
     return DSPARK_OK;
 }
 
+// Query blocks of a prompt call, all sequences' last ones counted whole: a
+// launch holds fewer than 2^32 threads, 256 a block.
+bool prompt_launchable(int B, int n_rows, int n_heads, int n_kv_heads) {
+    return int64_t(n_rows) * n_heads / 128 + (int64_t(B) + 1) * n_kv_heads < (1 << 24);
+}
+
 bool scale_ok(float scale) { return scale > 0.f && scale <= 3.4e38f; }
 
 }  // namespace
@@ -652,6 +664,7 @@ int dspark_kv_write(const void *k, const void *v, int64_t k_stride, int64_t v_st
     int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
                             page_size);
     if (st != DSPARK_OK) return st;
+    if (!cache_launchable(n_rows, n_kv_heads, head_dim)) return DSPARK_ERR_ARG;
     if (n_rows == 0) return DSPARK_OK;
     if (!k || !v || !cache_len || !page_table || !aligned16(k) || !aligned16(v)) return DSPARK_ERR_ARG;
     if (!row_stride_ok(k_stride, n_kv_heads, head_dim) || !row_stride_ok(v_stride, n_kv_heads, head_dim))
@@ -689,6 +702,7 @@ int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_sc
     int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
                             page_size);
     if (st != DSPARK_OK) return st;
+    if (!cache_launchable(n_rows, n_kv_heads, head_dim)) return DSPARK_ERR_ARG;
     if (n_rows == 0) return DSPARK_OK;
     if (!k_out || !v_out || !page_table || !aligned16(k_out) || !aligned16(v_out)) return DSPARK_ERR_ARG;
     st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
@@ -784,7 +798,7 @@ size_t dspark_prompt_attention_workspace_size(int B, int n_rows, int n_kv_rows, 
                                               int head_dim) {
     if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || n_kv_rows < 0 ||
         n_kv_rows > DSPARK_MAX_ROWS || head_geometry(n_rows, n_heads, n_kv_heads) != DSPARK_OK ||
-        !head_dim_supported(head_dim))
+        !prompt_launchable(B, n_rows, n_heads, n_kv_heads) || !head_dim_supported(head_dim))
         return 0;
     size_t bytes = 0;
     prompt_carve(nullptr, prompt_plan(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim), n_kv_heads, head_dim, &bytes);
@@ -801,6 +815,7 @@ int dspark_prompt_attention(const void *q, const void *k, const void *v, int64_t
         return DSPARK_ERR_ARG;
     const int st = head_geometry(n_rows, n_heads, n_kv_heads);
     if (st != DSPARK_OK) return st;
+    if (!prompt_launchable(B, n_rows, n_heads, n_kv_heads)) return DSPARK_ERR_ARG;
     if (dtype != DSPARK_BF16 && dtype != DSPARK_F16 && dtype != DSPARK_F32 && dtype != DSPARK_E4M3)
         return DSPARK_ERR_ARG;
     if ((dtype != DSPARK_BF16 && dtype != DSPARK_F16) || !head_dim_supported(head_dim)) return DSPARK_ERR_UNSUPPORTED;

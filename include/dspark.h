@@ -433,6 +433,11 @@ int dspark_acceptance_rnn(const float *target, int n_target_rows, const int32_t 
  * head_dim is 64, 128 or 256, otherwise DSPARK_ERR_UNSUPPORTED.  Row types are
  * DSPARK_BF16 or DSPARK_F16; a cache has the rows' type or DSPARK_E4M3
  * (otherwise DSPARK_ERR_UNSUPPORTED).  n_rows = 0 is valid and does nothing.
+ * One launch takes all of a call: n_rows * n_heads is below 2^31, the K and V
+ * of a write or read are below 256 GiB, and n_rows * n_heads / 128 + (B + 1) *
+ * n_kv_heads of a prompt call is below 2^24 (otherwise DSPARK_ERR_ARG).  Calls
+ * that may overlap in time, on two streams or in two captured graphs, need a
+ * workspace each.
  * The device current at the call must be the one that holds the buffers and
  * owns `stream`. */
 

@@ -186,3 +186,34 @@ def test_binding_checks_scales_outputs_and_offsets():
         ds.dspark_prompt_attention(g["q"], _t((4, 2, 64)), _t((4, 2, 128)), _t((3,), torch.int32))
     with pytest.raises(TypeError, match="q"):
         ds.dspark_prompt_attention(_t((4, 4, 64), torch.float32), g["k"], g["k"], _t((3,), torch.int32))
+
+
+def test_calls_past_one_launch_are_refused():
+    # 2^34 pieces of 16 bytes
+    assert _write(n=1 << 18, Hkv=1024, D=256, ks=1 << 18, vs=1 << 18) == ARG
+    assert _read(n=1 << 18, Hkv=1024, D=256) == ARG
+    wide = dict(Hq=256, Hkv=256, D=64, qs=256 * 64, ks=256 * 64, vs=256 * 64)
+    assert _prompt(B=65536, n=8, nkv=9, **wide) == ARG
+    assert ds.dspark_prompt_attention_workspace_size(65536, 8, 9, 256, 256, 64) == 0
+    assert _prompt(B=65534, n=8, nkv=9, ws=None, **wide) == WORKSPACE
+    assert ds.dspark_prompt_attention_workspace_size(65534, 8, 9, 256, 256, 64) > 0
+
+
+def test_binding_names_a_workspace_that_does_not_fit():
+    bf, i32 = torch.bfloat16, torch.int32
+    q, k = torch.zeros(4, 8, 64, dtype=bf), torch.zeros(4, 2, 64, dtype=bf)
+    off = torch.tensor([0, 4], dtype=i32)
+    cache, table = torch.zeros(3, 2, 16, 64, dtype=bf), torch.zeros(4, 2, dtype=i32)
+    calls = [lambda **kw: ds.dspark_prompt_attention(q, k, k, off, **kw),
+             lambda **kw: ds.dspark_paged_attention(q, cache, cache, torch.zeros(4, dtype=i32), table, **kw)]
+    for call in calls:
+        with pytest.raises(TypeError, match="workspace"):
+            call(workspace=torch.zeros(1 << 20, dtype=torch.float32))
+        with pytest.raises(TypeError, match="workspace"):
+            call(workspace=4096)
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
+    with pytest.raises(TypeError, match="row_offsets"):
+        ds.dspark_prompt_attention(q, k, k, None)
+    with pytest.raises(TypeError, match="page_table"):
+        ds.dspark_paged_attention(q, cache, cache, torch.zeros(4, dtype=i32), None)
