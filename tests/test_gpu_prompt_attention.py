@@ -190,3 +190,16 @@ def test_two_calls_at_once_and_new_outputs_on_the_calls_stream():
         for r in got:
             assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
             assert bool((r["out"][:50] == 0).all()) and bool((r["out"][450:] == 0).all())
+
+
+def test_a_reused_result_gains_the_lse_it_lacks():
+    ds = _ds()
+    torch.manual_seed(5)
+    off = torch.tensor([0, 70, 100], dtype=torch.int32, device="cuda")
+    q, k = (torch.randn(101, h, 64, device="cuda").to(torch.bfloat16) for h in (8, 2))
+    want = ds.dspark_prompt_attention(q, k, k, off, lse=True)
+    res = ds.dspark_prompt_attention(q, k, k, off)
+    assert "lse" not in res
+    again = ds.dspark_prompt_attention(q, k, k, off, lse=True, out=res)
+    assert again is res and torch.equal(res["lse"][:100], want["lse"][:100]) and torch.equal(res["out"], want["out"])
+    assert bool((res["lse"][100] == 0).all())
