@@ -195,22 +195,6 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     };
     auto issue_k = [&](int j) __device__ { issue(a.k, a.k_stride, kst, koff, lds0 + (j & 1) * S::BYTES, j * kKeys); };
     auto issue_v = [&](int j) __device__ { issue(a.v, a.v_stride, vst, voff, lds0 + (2 + (j & 1)) * S::BYTES, j * kKeys); };
-    if (ntile > 0) {
-        issue_k(0);
-        if (ntile > 1) issue_k(1);
-        issue_v(0);
-    }
-
-    V8 qf[KS];
-    {
-        const E *src = static_cast<const E *>(a.q) + (long long)(q0 + qrow) * a.q_stride + (kvh * p.G + qhead) * D + 8 * h;
-#pragma unroll
-        for (int k = 0; k < KS; ++k) qf[k] = *reinterpret_cast<const V8 *>(src + 16 * k);
-        // plain register values from here on: the loop must not wait for these
-        // loads again, which would wait for every tile in flight
-#pragma unroll
-        for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(qf[k]));
-    }
 
     // ---- read addresses ----------------------------------------------------
     // K fragment (32 tokens from row r0, step k): chunk 2 k + h of row r0 + n;
@@ -245,6 +229,33 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         const uint32_t at = HELD ? base + vheld[HELD ? c : 0] : base ^ (64 * c);
         return join4<V8>(lds_read_tr16(at, r0 * S::RB), lds_read_tr16(at, (r0 + 8) * S::RB));
     };
+
+    // ---- the first tiles and the queries, by way of the second K and V buffers
+    // (whole rows a load; read straight into registers, every load touches 32
+    // rows: 64 prompts of 200 to 300 rows 107 against 101 us, 32 of up to 200 rows
+    // at D = 64 11.2 against 10.6).  A wave's 32 query rows fill half a buffer,
+    // laid out as K rows are.
+    V8 qf[KS];
+    if (ntile > 0) {
+        const int row0 = min(wq0, nq - 1) / p.G;
+        const E *first = static_cast<const E *>(a.q) + (long long)(q0 + row0) * a.q_stride + (long long)kvh * p.G * D;
+        const uint32_t own = uint32_t(qrow - row0) * uint32_t(a.q_stride * 2) + uint32_t(qhead * D * 2);
+        const uint32_t qlds = lds0 + (wave < NW / 2 ? 1 : 3) * S::BYTES + wave % (NW / 2) * 32 * S::RB;
+        constexpr int RPI = 1024 / S::RB;  // rows a load covers
+#pragma unroll
+        for (int j = 0; j < 32 / RPI; ++j) {
+            const int row = j * RPI + lane / S::CPR;
+            const uint32_t off = uint32_t(__shfl(int(own), row)) + ((lane % S::CPR) ^ S::k_swizzle(row)) * 16;
+            dma16(uniform(qlds + j * 1024), off, uniform(reinterpret_cast<const uint8_t *>(first)));
+        }
+        issue_k(0);
+        issue_v(0);
+        vm_wait<SH::LPT>();
+#pragma unroll
+        for (int k = 0; k < KS; ++k) qf[k] = lds_read<V8>(qlds + (kread ^ (32 * k)));
+        wg_barrier();  // K of tile 0 is in, every wave has its queries
+        if (ntile > 1) issue_k(1);
+    }
 
     float m = kNegInf, l = 0.f;
     f32x16_t o[CB];
@@ -347,8 +358,6 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     };
 
     if (ntile > 0) {
-        vm_wait<0>();
-        wg_barrier();
         scores(0, s);
         hide(0, s);
         raise(largest(s));
@@ -504,7 +513,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         const int row = (i * 64 + lane) / S::CPR, ch = lane % S::CPR;
         const u32x4v_t x = lds_read<u32x4v_t>(rows_at + row * S::RB + ((ch ^ S::k_swizzle(row)) * 16));
         const long long dst = __shfl(at, row);
-        if (wq0 + row < nq) *reinterpret_cast<u32x4v_t *>(static_cast<E *>(a.out) + dst * D + 8 * ch) = x;
+        // not read again here: non-temporal (64 prompts of 512 rows: 252 -> 248 us)
+        if (wq0 + row < nq) __builtin_nontemporal_store(x, reinterpret_cast<u32x4v_t *>(static_cast<E *>(a.out) + dst * D + 8 * ch));
     }
 }
 
