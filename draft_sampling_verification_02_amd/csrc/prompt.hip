@@ -26,11 +26,11 @@
 // fill the chip, their keys are split and prompt_join merges the parts.
 //
 // Measured (MI355X, bfloat16, 32 query and 8 key-value heads, D = 128): one
-// prompt of 16384 tokens 1914 us, 1149 TFLOP/s, matrix units busy 64% of
+// prompt of 16384 tokens 1908 us, 1153 TFLOP/s, matrix units busy 64% of
 // 1.72 GHz (a 16384-cubed library product reaches 1386 TFLOP/s, 73% of
-// 1.71 GHz); 16 prompts of 100 to 4100 tokens 943-1065 us over the boxes, 890 to
-// 1005 TFLOP/s, the rest being starts, ends and diagonal tiles.  16/4 heads at
-// 8192 tokens: D = 64 168 us, 818 TFLOP/s; D = 256 626 us, 879 TFLOP/s (one
+// 1.71 GHz); 16 prompts of 100 to 4100 tokens 931-1040 us over the boxes, 910 to
+// 1018 TFLOP/s, the rest being starts, ends and diagonal tiles.  16/4 heads at
+// 8192 tokens: D = 64 164 us, 838 TFLOP/s; D = 256 582-624 us, 880 to 945 TFLOP/s (one
 // wave a SIMD: the accumulators take half its registers).
 #include <algorithm>
 
@@ -570,16 +570,23 @@ hipError_t launch_prompt_dim(const PromptParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Into how many ranges the keys of a query block are cut.  A block of T tiles
-// takes about 0.85 us a tile (D = 128, in proportion for others) while there are
-// at most 512 blocks (two a compute unit), and in proportion more beyond; a cut
+// Into how many ranges the keys of a query block are cut.  A chain of T tiles
+// takes about 0.8, 1.2 or 2 us a tile (D = 64, 128, 256) while there are at most
+// 512 blocks (the diagonal halves most), and in proportion more beyond; a cut
 // adds a launch, 5 us, and writes and reads 64 KiB a part.  The cheapest cut is
 // taken; the average sequence stands for all, as lengths are on the device.
-// Measured, us a call in 1 / 2 / 4 / 8 / 16 parts (D = 128): 18 rows behind 4000
-// keys, 8/1 heads 39.7 / 26.1 / 18.8 / 14.6 / 13.8; four times 64 rows behind
-// 2000, 32/8 heads 32.8 / 25.4 / 23.7 / 27.1 / 36.7; one prompt of 2048 rows, 8/8
-// heads 37.8 / 31.0 / 29.3 / 40.8 / 58.8; of 4096 68.5 / 59.3 / 65.9; of 1024
-// rows, 32/8 heads 24.3 / 30.5 / 39.3; of 512 14.9 / 18.1 / 19.7.
+// Measured, us a call in 1 / 2 / 3 / 4 / 8 / 16 parts, > < the rule's:
+//   18 rows behind 4000 keys, 8/1 heads, D = 128   39.7 /  26.1  / 21.2 /  18.8  / 14.6 / 13.8 (32 parts 14.6, > 24 <)
+//   four times 64 rows behind 2000, 32/8 heads     32.8 /  25.4  / 24.0 / >23.7< / 27.1 / 36.7
+//   one prompt of 2048 rows, 8/8 heads             37.8 / >31.0< / 28.6 /  29.3  / 40.8 / 58.8
+//   of 4096                                        68.5 / >59.3< / 61.7 /  65.9
+//   of 1024, 32/8 heads                           >24.3</  30.5  / 35.3 /  39.3
+//   of 512, 32/8 heads                            >14.9</  18.1  / 19.3 /  19.7
+//   of 4096, 8/8 heads, D = 64                     49.6 / >37.9< / 38.3 /  39.0  / 53.4
+//   of 2048, 16/4 heads, D = 64                   >27.6</  26.5  / 28.5 /  30.6  / 49.6
+//   of 4096, 8/1 heads, D = 256                     128 / > 109< /  121 /   136  /  201
+//   of 1024, 8/8 heads, D = 256                    39.3 /  32.0  />29.0</  27.1  / 40.4
+//   of 2048, 16/4 heads, D = 256                  >68.4</  72.5  / 86.9 /   106  /  166
 PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim) {
     PromptPlan p{};
     p.slots = int((long long)n_rows * (n_heads / n_kv_heads) / kPromptQueries + B);
@@ -588,7 +595,7 @@ PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_h
     double best = 1e30;
     for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
         if (s > 1 && tiles < s * kMinTiles) break;
-        const double cost = 0.85 * wide * tiles / s * std::max(1.0, units * s / 512) + (s > 1 ? 5 + 0.033 * wide * units * s : 0.0);
+        const double cost = (0.4 + 0.8 * wide) * tiles / s * std::max(1.0, units * s / 512) + (s > 1 ? 5 + 0.033 * wide * units * s : 0.0);
         if (cost < best) {
             best = cost;
             p.nsplit = s;
