@@ -94,6 +94,13 @@ def test_few_rows_behind_a_long_prefix():
     _run([18, 1, 40], [2100, 3000, 41], 2, 8, 64)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_prompts_of_few_heads_are_cut_and_joined(D, causal):
+    # blocks near the diagonal's start have fewer parts than the plan, one sequence has a single tile
+    _run([700, 3, 1301], None, 1, 3, D, causal=causal, seed=D, lead=2, tail=3)
+
+
 def test_more_rows_than_keys_leave_rows_empty():
     _run([40, 70, 3], [10, 0, 3], 2, 2, 64)
 
