@@ -152,6 +152,54 @@ def test_values_of_one_bad_value_reach_exactly_the_rows_that_see_it():
     check("out", r["out"], o, tol)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_bad_values_where_the_keys_are_cut(D):
+    # the diagonal lies in the last part: an infinite value there, NaN past the sequence's end
+    ds = _ds()
+    n, L = 18, 2000
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn((m, h, D), generator=g).to(BF) for m, h in ((n, 4), (L + 20, 1), (L + 20, 1)))
+    seen = L - n + 7  # rows from 7 on see it
+    v[seen, 0, 5] = -math.inf
+    k[L:], v[L:] = math.nan, math.nan
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets([n]).cuda(),
+                                   kv_offsets=torch.tensor([0, L], dtype=torch.int32, device="cuda"), lse=True)
+    torch.cuda.synchronize()
+    v[seen, 0, 5] = 0.0
+    o, z, tol, lt = attend(q.double(), k[:L].double(), v[:L].double(), [L - n + i + 1 for i in range(n)], D ** -0.5, U[BF],
+                           U[BF])
+    o[7:, :, 5] = -math.inf
+    check("out", r["out"], o, tol)
+    check("lse", r["lse"], z, lt)
+
+
+def test_a_captured_call_with_cut_keys_follows_its_offsets():
+    ds = _ds()
+    g = torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn((m, h, 128), generator=g).to(BF).cuda() for m, h in ((40, 8), (3000, 1), (3000, 1)))
+    off, kvoff = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 20, 40], [0, 1500, 3000]))
+    res = ds.dspark_prompt_attention(q, k, v, off, kv_offsets=kvoff, lse=True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ds.dspark_prompt_attention(q, k, v, off, kv_offsets=kvoff, lse=True, out=res)
+    for a, b in (([0, 20, 40], [0, 1500, 3000]), ([0, 3, 40], [0, 2900, 3000]), ([0, 0, 40], [0, 10, 3000]),
+                 ([0, 39, 40], [0, 70, 71]), ([0, 20, 40], [0, 1500, 3000])):
+        off.copy_(torch.tensor(a, dtype=torch.int32))
+        kvoff.copy_(torch.tensor(b, dtype=torch.int32))
+        want = ds.dspark_prompt_attention(q, k, v, off, kv_offsets=kvoff, lse=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(res["out"], want["out"]) and torch.equal(res["lse"], want["lse"])
+        for i in range(2):
+            rows, keys = a[i + 1] - a[i], b[i + 1] - b[i]
+            lim = [min(keys, max(0, keys - rows + j + 1)) for j in range(rows)]
+            o, z, tol, lt = attend(q[a[i]:a[i + 1]].cpu().double(), k[b[i]:b[i + 1]].cpu().double(),
+                                   v[b[i]:b[i + 1]].cpu().double(), lim, 128 ** -0.5, U[BF], U[BF])
+            check(f"out {a} {i}", res["out"][a[i]:a[i + 1]], o, tol)
+            check(f"lse {a} {i}", res["lse"][a[i]:a[i + 1]], z, lt)
+
+
 def test_same_bits_on_every_call_stream_and_graph_replay():
     ds = _ds()
     g = torch.Generator().manual_seed(5)
