@@ -320,9 +320,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         if (j + 1 < ntile) issue_v(j + 1);
     };
     // Infinities or NaN among V rows that some queries must not see: the queries
-    // that see them get their share here, then they leave the tile.  Every wave
-    // of the workgroup comes here.
-    auto take_out_bad = [&](int t, uint32_t vbuf, const V8 *pf) __device__ {
+    // that see them get their share of them here, and then they leave the tile.
+    auto give_bad_shares = [&](int t, uint32_t vbuf, const V8 *pf) __device__ {
 #pragma unroll 1
         for (int k = 0; k < kKeys; ++k) {
             // token k is element e of fragment k / 16, lane half (k / 4) % 2;
@@ -343,6 +342,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
                     }
                 }
         }
+    };
+    // (every wave of the workgroup comes here)
+    auto clean = [&](uint32_t vbuf) __device__ {
         wg_barrier();
 #pragma unroll 1
         for (int i = tid; i < kKeys * S::CPR; i += SH::NT) {
@@ -457,13 +459,20 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             wg_barrier();
             bad = found_bad == j + 1;
         }
-        if (t >= wmax && !bad) continue;
+        if (t >= wmax) {
+            // none of the wave's queries sees the tile, and s still holds an earlier one's
+            // scores: they must not enter the sums again
+            if (bad) clean(vbuf);
+            continue;
+        }
         const float ms = m == kNegInf ? 0.f : m;
         V8 pf[4];
 #pragma unroll
         for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
-        if (bad) take_out_bad(t, vbuf, pf);
-        if (t >= wmax) continue;
+        if (bad) {
+            give_bad_shares(t, vbuf, pf);
+            clean(vbuf);
+        }
         const uint32_t vb = v_base(vbuf);
 #pragma unroll
         for (int f = 0; f < 4; ++f) product(vb, pf, f);

@@ -258,3 +258,47 @@ def test_a_reused_result_gains_the_lse_it_lacks():
     again = ds.dspark_prompt_attention(q, k, k, off, lse=True, out=res)
     assert again is res and torch.equal(res["lse"][:100], want["lse"][:100]) and torch.equal(res["out"], want["out"])
     assert bool((res["lse"][100] == 0).all())
+
+
+# (rows, keys, Hkv, G, rows of V, counted from the last key, that hold the bad value)
+STRADDLING = [
+    ([200], None, 1, 1, [100, 10]),                 # 128 rows a block: the four waves end in three tiles
+    ([70, 200, 130], None, 2, 3, [100, 40, 10]),    # a block's rows start anywhere
+    ([200, 90], [216, 107], 1, 4, [70, 33]),        # 32 rows a block behind a prefix that is no multiple of them
+    ([150], [3000], 1, 1, [100, 10]),               # cut keys, the diagonal over several tiles
+]
+
+
+@pytest.mark.parametrize("rows,keys,Hkv,G,back", STRADDLING)
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_bad_values_of_later_tiles_leave_earlier_rows_alone(rows, keys, Hkv, G, back, bad, dtype, D):
+    # channel 5 of some V rows is bad: the rows that see one have that channel
+    # bad and nothing else, the rows before them nothing at all
+    ds = _ds()
+    lens = keys or rows
+    print(f"prompt: rows={rows} keys={keys} Hkv={Hkv} G={G} D={D} {dtype} bad={bad}", flush=True)
+    need = ds.dspark_prompt_attention_workspace_size(len(rows), sum(rows), sum(lens), Hkv * G, Hkv, D)
+    assert (need > 256) == (max(lens) >= 3000)  # the last case is cut and joined
+    g = torch.Generator().manual_seed(D)
+    q = torch.randn((sum(rows), Hkv * G, D), generator=g).to(dtype)
+    k, v = (torch.randn((sum(lens), Hkv, D), generator=g).to(dtype) for _ in range(2))
+    clean, at = v.clone(), 0
+    for L in lens:
+        at += L
+        for x in back:
+            if x <= L:
+                v[at - x, :, 5], clean[at - x, :, 5] = bad, 0.0
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets(rows).cuda(),
+                                   kv_offsets=None if keys is None else offsets(keys).cuda(), lse=True)
+    torch.cuda.synchronize()
+    at = kat = 0
+    for b, (n, L) in enumerate(zip(rows, lens)):
+        o, z, tol, lt = attend(q[at:at + n].double(), k[kat:kat + L].double(), clean[kat:kat + L].double(),
+                               [L - n + i + 1 for i in range(n)], D ** -0.5, U[dtype], U[dtype])
+        first = max(0, n - max(x for x in back if x <= L))  # the first row that sees a bad one
+        o[first:, :, 5] = bad
+        check(f"out of {b}", r["out"][at:at + n], o, tol)
+        check(f"lse of {b}", r["lse"][at:at + n], z, lt)
+        at, kat = at + n, kat + L
