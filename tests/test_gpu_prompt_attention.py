@@ -302,3 +302,34 @@ def test_bad_values_of_later_tiles_leave_earlier_rows_alone(rows, keys, Hkv, G, 
         check(f"out of {b}", r["out"][at:at + n], o, tol)
         check(f"lse of {b}", r["lse"][at:at + n], z, lt)
         at, kat = at + n, kat + L
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_blocks_with_different_numbers_of_parts_are_joined(dtype, D, causal):
+    # 2400 rows of one and two heads: the first blocks of a causal prompt have
+    # one part, the last ones all; a short sequence beside it has a single tile
+    ds = _ds()
+    for G, rows in ((1, [2390, 5]), (2, [3, 2400])):
+        N, lead = sum(rows) + 3, 1
+        assert ds.dspark_prompt_attention_workspace_size(2, N, N, G, 1, D) > 256, "the keys are cut"
+        print(f"prompt: rows={rows} G={G} D={D} {dtype} causal={causal}", flush=True)
+        g = torch.Generator().manual_seed(D + G)
+        q, k, v = (torch.randn((N, h, D), generator=g).to(dtype) for h in (G, 1, 1))
+        out = {"out": torch.full((N, G, D), 7.0, dtype=dtype, device="cuda"), "lse": torch.full((N, G), 7.0, device="cuda")}
+        r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets(rows, lead).cuda(), causal=causal, out=out)
+        torch.cuda.synchronize()
+        at = lead
+        for n in rows:
+            pick = sorted({i for i in (0, 1, 2, 4, 62, 63, 64, 65, 126, 127, 128, 129, 700, 1023, 1024, 1500, 2000, 2303,
+                                       n - 65, n - 64, n - 2, n - 1) if 0 <= i < n})
+            lim = [i + 1 if causal else n for i in pick]
+            own = slice(at, at + n)
+            o, z, tol, lt = attend(q[own][pick].double(), k[own].double(), v[own].double(), lim, D ** -0.5, U[dtype], U[dtype])
+            check("out", r["out"][own][pick], o, tol)
+            check("lse", r["lse"][own][pick], z, lt)
+            assert bool(torch.isfinite(r["out"][own]).all())
+            at += n
+        for n in ("out", "lse"):
+            assert bool((r[n][:lead] == 7.0).all()) and bool((r[n][at:] == 7.0).all())
