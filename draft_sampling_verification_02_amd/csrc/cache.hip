@@ -86,7 +86,8 @@ __device__ __forceinline__ RowPlace place_row(const CacheArgs &a, int pshift, in
         }
         b = lo;
         if (b >= a.B) return p;
-        first = a.row_offsets[b];
+        // clamped as everywhere (its end needs no clamp: r is a row of the call)
+        first = max(a.row_offsets[b], 0);
         if (first > r) return p;
     }
     if (b < 0 || b >= a.B) return p;

@@ -186,3 +186,33 @@ def test_many_rows_of_many_requests():
     assert torch.equal(kd.cpu(), kc) and torch.equal(vd.cpu(), vc)
     r = ds.dspark_kv_read(kd, vd, table.cuda(), N, row_offsets=off.cuda(), first=pd)
     assert torch.equal(r["k"].cpu(), k) and torch.equal(r["v"].cpu(), v)
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("low,high", [(-5, 200), (-2 ** 31, 2 ** 31 - 1)])
+def test_offsets_outside_the_rows_count_as_clamped(low, high, cache):
+    # requests that start before the first row or end behind the last: rows go
+    # where they go with the offsets clamped into [0, n_rows], in a write, a
+    # read and an attention over the cache
+    ds = _ds()
+    Hkv, D, page, n = 2, 64, 16, 12
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((n, Hkv, D), generator=g).to(BF).cuda() for _ in range(2))
+    q = torch.randn((n, 2 * Hkv, D), generator=g).to(BF).cuda()
+    past = torch.tensor([4, 30, 0, 9], dtype=torch.int32, device="cuda")
+    table = torch.randperm(16, generator=g).to(torch.int32).view(4, 4).cuda()
+    results = []
+    for off in ([low, 3, 9, 9, high], [0, 3, 9, 9, n]):
+        off = torch.tensor(off, dtype=torch.int32, device="cuda")
+        kc, vc = (torch.full((16, Hkv, page, D), 3.0, device="cuda").to(cache) for _ in range(2))
+        sc = {x: torch.full((16, Hkv, page), 77, dtype=torch.uint8, device="cuda") for x in ("k_scale", "v_scale")} if cache == E4 else {}
+        ds.dspark_kv_write(k, v, kc, vc, past, table, row_offsets=off, **sc)
+        back = ds.dspark_kv_read(kc, vc, table, n, row_offsets=off, first=past, **sc)
+        att = ds.dspark_paged_attention(q, kc, vc, past, table, row_offsets=off, lse=True, **sc)
+        torch.cuda.synchronize()
+        results.append([_bits(kc), _bits(vc), _bits(back["k"]), _bits(back["v"]), _bits(att["out"]), att["lse"].cpu()]
+                       + [x.cpu() for x in sc.values()])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    if cache == BF:
+        assert torch.equal(back["k"], k) and torch.equal(back["v"], v)
