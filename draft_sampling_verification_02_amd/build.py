@@ -70,12 +70,12 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
         marshal = ex.submit(_compile_marshal, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        marshal.result()
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objs
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
+        cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objs
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(LIB + ".tmp", LIB)
+        marshal.result()  # last: the C library needs neither torch nor the host compiler
     return LIB
 
 
