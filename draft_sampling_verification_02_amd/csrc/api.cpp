@@ -651,7 +651,8 @@ bool prompt_launchable(int B, int n_rows, int n_heads, int n_kv_heads) {
     return int64_t(n_rows) * n_heads / 128 + (int64_t(B) + 1) * n_kv_heads < (1 << 24);
 }
 
-bool scale_ok(float scale) { return scale > 0.f && scale <= 3.4e38f; }
+// the kernels multiply by scale * log2(e), which has to be finite
+bool scale_ok(float scale) { return scale > 0.f && scale <= 2.3e38f; }
 
 }  // namespace
 

@@ -486,7 +486,7 @@ size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv
  *   max_rows    >= 1: how many rows a request usually has at most (1 for
  *               decoding, gamma + 1 for verification).  It only picks the
  *               kernel: requests may have more or fewer.
- *   scale       > 0, finite (usually head_dim^-1/2)
+ *   scale       > 0, at most 2.3e38 (usually head_dim^-1/2)
  *   out         device [n_rows, n_heads, head_dim] of `dtype`, dense, 16-byte aligned
  *   lse_out     device [n_rows, n_heads] float32 or NULL
  *   workspace   device, >= dspark_paged_attention_workspace_size bytes

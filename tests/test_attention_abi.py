@@ -217,3 +217,10 @@ def test_binding_names_a_workspace_that_does_not_fit():
         ds.dspark_prompt_attention(q, k, k, None)
     with pytest.raises(TypeError, match="page_table"):
         ds.dspark_paged_attention(q, cache, cache, torch.zeros(4, dtype=i32), None)
+
+
+@pytest.mark.parametrize("scale", [2.31e38, 2.4e38, 3.4e38])
+def test_scales_whose_base_2_form_overflows_are_refused(scale):
+    # the kernels work in units of scale * log2(e), which would be infinite from 2.36e38 on: 0 * inf where a score is 0
+    assert _paged(scale=scale) == ARG and _prompt(scale=scale) == ARG
+    assert _paged(scale=2.29e38, ws=None) == WORKSPACE and _prompt(scale=2.29e38, ws=None) == WORKSPACE
