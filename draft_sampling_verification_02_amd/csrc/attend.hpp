@@ -178,19 +178,6 @@ __device__ __forceinline__ void widen4(u32x2_t w, float *v) {
     v[2] = b.x;
     v[3] = b.y;
 }
-// element e of fragment f of N (both may vary: selects, no memory)
-template <typename T, int N>
-__device__ __forceinline__ float element(const typename T::V8 *frag, int f, int e) {
-    uint32_t x = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const u32x4v_t w = __builtin_bit_cast(u32x4v_t, frag[i]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x = f == i && (e >> 1) == q ? w[q] : x;
-    }
-    const float2 v = widen<T>(x);
-    return (e & 1) ? v.y : v.x;
-}
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin_huge_valf(); }
 // a pair of 16-bit values, and four e4m3 values, with zeros in the place of what is not finite
 template <typename T>

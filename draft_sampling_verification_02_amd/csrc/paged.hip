@@ -345,16 +345,19 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
             dma16(uniform(qlds + j * 1024), static_cast<const uint8_t *>(a.q) + 2 * src);
         }
         int pa = 0, pb = 0, na = 0, nb = 0;  // pages of the tile at hand and of the next one
-        if (tiles > 0) {
-            pa = page_of(tile_at(0));
-            pb = page_of(tile_at(0) + 16);
-            issue_k(0, pa, pb);
-            issue_v(0, pa, pb);
-        }
-        if (tiles > 1) {
-            na = page_of(tile_at(1));
-            nb = page_of(tile_at(1) + 16);
-        }
+        auto issue_first = [&]() __device__ {
+            if (tiles > 0) {
+                pa = page_of(tile_at(0));
+                pb = page_of(tile_at(0) + 16);
+                issue_k(0, pa, pb);
+                issue_v(0, pa, pb);
+            }
+            if (tiles > 1) {
+                na = page_of(tile_at(1));
+                nb = page_of(tile_at(1) + 16);
+            }
+        };
+        issue_first();
         if (tiles > 0)
             vm_wait<SH::KL + SH::VL>();
         else
@@ -380,188 +383,220 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
 
         float m[NQ], l[NQ];
         f32x4_t o[NQ][CB];
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-            m[q] = kNegInf;
-            l[q] = 0.f;
-#pragma unroll
-            for (int c = 0; c < CB; ++c) o[q][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        }
-
-        for (int i = 0; i < tiles; ++i) {
-            const int t = tile_at(i);
-            const int bad_now = int(bad_page(pa)) | int(bad_page(pb)) << 1;  // the tile's halves on pages outside the cache
-            const bool more = i + 1 < tiles;
-            int fa = 0, fb = 0;  // pages of the tile after next, on their way
-            if (i + 2 < tiles) {
-                fa = page_of(tile_at(i + 2));
-                fb = page_of(tile_at(i + 2) + 16);
-            }
-            // ---- scores: s[q][half][r] is token 16 half + 4 g + r, query n
-            vm_wait<SH::VL>();
-            const uint32_t kbase = fresh(ring + kread);
-            f32x4_t s[NQ][2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) s[q][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int k = 0; k < KSTEP; ++k) {
-                    const u32x4v_t x = lds_read<u32x4v_t>(kbase ^ (64 * k), 16 * hf * S::RB);
-                    if constexpr (E4) {
-                        V8 lo, hi;
-                        e4m3_to8(u32x2_t{x[0], x[1]}, lo);
-                        e4m3_to8(u32x2_t{x[2], x[3]}, hi);
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(lo, qf[q][2 * k], s[q][hf]);
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(hi, qf[q][2 * k + 1], s[q][hf]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q)
-                            s[q][hf] = mma16(__builtin_bit_cast(V8, x), qf[q][k], s[q][hf]);
-                    }
-                }
-            }
-            float vs[2][4];
-            if constexpr (E4) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t kw = lds_read<uint32_t>(ring + 2 * S::BYTES + 16 * hf + 4 * g);
-                    const uint32_t vw = lds_read<uint32_t>(ring + 2 * S::BYTES + 32 + 16 * hf + 4 * g);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float ks = scale_of((kw >> (8 * r)) & 255);
-                        vs[hf][r] = scale_of((vw >> (8 * r)) & 255);
-#pragma unroll
-                        for (int q = 0; q < NQ; ++q) s[q][hf][r] *= ks;
-                    }
-                }
-            }
-            lds_drain();
-            if (more) issue_k(i + 1, na, nb);
-
-            // ---- running maximum, probabilities
-            const bool masked = t + kTokens > lim_min || bad_now != 0;
-            P8 pf[NQ], pr_rest[kTwoTerms<T, E4> ? NQ : 1];
+        auto clear = [&]() __device__ {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
-                if (masked) {
+                m[q] = kNegInf;
+                l[q] = 0.f;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (t + 16 * hf + 4 * g + r >= lim[q] || ((bad_now >> hf) & 1)) s[q][hf][r] = kNegInf;
+                for (int c = 0; c < CB; ++c) o[q][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            }
+        };
+        clear();
+
+        // This wave's tiles, whose first is on its way (CAREFUL: with every one looked over).
+        auto walk = [&](auto careful_tag) __device__ __attribute__((always_inline)) {
+            constexpr bool CAREFUL = decltype(careful_tag)::value;
+            for (int i = 0; i < tiles; ++i) {
+                const int t = tile_at(i);
+                const int bad_now = int(bad_page(pa)) | int(bad_page(pb)) << 1;  // the tile's halves on pages outside the cache
+                const bool more = i + 1 < tiles;
+                int fa = 0, fb = 0;  // pages of the tile after next, on their way
+                if (i + 2 < tiles) {
+                    fa = page_of(tile_at(i + 2));
+                    fb = page_of(tile_at(i + 2) + 16);
                 }
-                float mx = fmaxf(fmaxf(fmaxf(s[q][0][0], s[q][0][1]), fmaxf(s[q][0][2], s[q][0][3])),
-                                 fmaxf(fmaxf(s[q][1][0], s[q][1][1]), fmaxf(s[q][1][2], s[q][1][3])));
-                mx = max_x16(max_x32(mx)) * p.c;
-                const float mn = fmaxf(m[q], mx);
-                if (__any(mn > m[q])) {
-                    const float al = fast_exp2(m[q] - (mn == kNegInf ? 0.f : mn));
-                    l[q] *= al;
+                // ---- scores: s[q][half][r] is token 16 half + 4 g + r, query n
+                vm_wait<SH::VL>();
+                const uint32_t kbase = fresh(ring + kread);
+                f32x4_t s[NQ][2];
 #pragma unroll
-                    for (int c = 0; c < CB; ++c) o[q][c] *= al;
-                    m[q] = mn;
-                }
-                const float ms = mn == kNegInf ? 0.f : mn;
-                float pr[8];
+                for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) pr[e] = fast_exp2(__builtin_fmaf(s[q][e >> 2][e & 3], p.c, -ms));
-                l[q] += ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
-                if constexpr (E4) {
+                    for (int q = 0; q < NQ; ++q) s[q][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // a masked token's scale may be anything: its product stays zero
-                        const float x = pr[e] * vs[e >> 2][e & 3];
-                        pr[e] = masked && s[q][e >> 2][e & 3] == kNegInf ? 0.f : x;
+                    for (int k = 0; k < KSTEP; ++k) {
+                        const u32x4v_t x = lds_read<u32x4v_t>(kbase ^ (64 * k), 16 * hf * S::RB);
+                        if constexpr (E4) {
+                            V8 lo, hi;
+                            e4m3_to8(u32x2_t{x[0], x[1]}, lo);
+                            e4m3_to8(u32x2_t{x[2], x[3]}, hi);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(lo, qf[q][2 * k], s[q][hf]);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(hi, qf[q][2 * k + 1], s[q][hf]);
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q)
+                                s[q][hf] = mma16(__builtin_bit_cast(V8, x), qf[q][k], s[q][hf]);
+                        }
                     }
                 }
-                using E = typename PT::E;
-                pf[q] = P8{E(pr[0]), E(pr[1]), E(pr[2]), E(pr[3]), E(pr[4]), E(pr[5]), E(pr[6]), E(pr[7])};
-                if constexpr (kTwoTerms<T, E4>) {
+                float vs[2][4];
+                if constexpr (E4) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) pr_rest[q][e] = E(pr[e] - float(pf[q][e]));
-                }
-            }
-
-            // ---- products with V
-            if (more)
-                vm_wait<SH::KL>();
-            else
-                vm_wait<0>();
-            const uint32_t vbuf = ring + S::BYTES;
-            const uint32_t vbase = fresh(vbuf + vread);
-            if (masked) {
-                // rows that no query sees (past the request's end, pages outside the cache) may hold anything
-#pragma unroll 1
-                for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
-                    const int row = slot / S::CPR;
-                    if (t + row >= rq.L || ((bad_now >> (row >> 4)) & 1)) lds_write(vbuf + slot * 16, u32x4v_t{0, 0, 0, 0});
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t kw = lds_read<uint32_t>(ring + 2 * S::BYTES + 16 * hf + 4 * g);
+                        const uint32_t vw = lds_read<uint32_t>(ring + 2 * S::BYTES + 32 + 16 * hf + 4 * g);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float ks = scale_of((kw >> (8 * r)) & 255);
+                            vs[hf][r] = scale_of((vw >> (8 * r)) & 255);
+#pragma unroll
+                            for (int q = 0; q < NQ; ++q) s[q][hf][r] *= ks;
+                        }
+                    }
                 }
                 lds_drain();
-                // A row that some queries see and others must not is harmless where it is finite, as the others'
-                // probabilities are zero; 0 * v tells.  What is not finite is taken out of the tile: the queries
-                // that see it get their share of it here.
-                if (t + kTokens > lim_min && lim_min < rq.L) {
-                    const P8 zero = {};
-                    f32x4_t z = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                if (more) issue_k(i + 1, na, nb);
+
+                // ---- running maximum, probabilities
+                const bool masked = t + kTokens > lim_min || bad_now != 0;
+                P8 pf[NQ], pr_rest[kTwoTerms<T, E4> ? NQ : 1];
 #pragma unroll
-                    for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbase, c), zero, z);
-                    if (__any(!(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f))) {
+                for (int q = 0; q < NQ; ++q) {
+                    if (masked) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                if (t + 16 * hf + 4 * g + r >= lim[q] || ((bad_now >> hf) & 1)) s[q][hf][r] = kNegInf;
+                    }
+                    float mx = fmaxf(fmaxf(fmaxf(s[q][0][0], s[q][0][1]), fmaxf(s[q][0][2], s[q][0][3])),
+                                     fmaxf(fmaxf(s[q][1][0], s[q][1][1]), fmaxf(s[q][1][2], s[q][1][3])));
+                    mx = max_x16(max_x32(mx)) * p.c;
+                    const float mn = fmaxf(m[q], mx);
+                    if (__any(mn > m[q])) {
+                        const float al = fast_exp2(m[q] - (mn == kNegInf ? 0.f : mn));
+                        l[q] *= al;
+#pragma unroll
+                        for (int c = 0; c < CB; ++c) o[q][c] *= al;
+                        m[q] = mn;
+                    }
+                    const float ms = mn == kNegInf ? 0.f : mn;
+                    float pr[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pr[e] = fast_exp2(__builtin_fmaf(s[q][e >> 2][e & 3], p.c, -ms));
+                    l[q] += ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
+                    if constexpr (E4) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            // a masked token's scale may be anything: its product stays zero
+                            const float x = pr[e] * vs[e >> 2][e & 3];
+                            pr[e] = masked && s[q][e >> 2][e & 3] == kNegInf ? 0.f : x;
+                        }
+                    }
+                    using E = typename PT::E;
+                    pf[q] = P8{E(pr[0]), E(pr[1]), E(pr[2]), E(pr[3]), E(pr[4]), E(pr[5]), E(pr[6]), E(pr[7])};
+                    if constexpr (kTwoTerms<T, E4>) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) pr_rest[q][e] = E(pr[e] - float(pf[q][e]));
+                    }
+                }
+
+                // ---- products with V
+                if (more)
+                    vm_wait<SH::KL>();
+                else
+                    vm_wait<0>();
+                const uint32_t vbuf = ring + S::BYTES;
+                const uint32_t vbase = fresh(vbuf + vread);
+                if (CAREFUL || masked) {
+                    // rows that no query sees (past the request's end, pages outside the cache) may hold anything
 #pragma unroll 1
-                        for (int k = 0; k < kTokens; ++k) {
-                            // token k is element e of lane group (k / 4) % 4; the lane holds channels 16 c + 4 g ..
-                            const int e = (k & 3) + 4 * (k >> 4), from = ((k >> 2) & 3) * 16 + n;
-                            const uint32_t row = vbuf + k * S::RB + (E4 ? 4 * g : 8 * (g & 1));
-                            const int sw = S::v_swizzle(k);
+                    for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
+                        const int row = slot / S::CPR;
+                        if (t + row >= rq.L || ((bad_now >> (row >> 4)) & 1)) lds_write(vbuf + slot * 16, u32x4v_t{0, 0, 0, 0});
+                    }
+                    lds_drain();
+                    // A row that some queries see and others must not is harmless where it is finite, as the others'
+                    // probabilities are zero; 0 * v tells.  What is not finite is taken out of the tile: the queries
+                    // that see it get their share of it here.  (The share's probability is taken anew in 32 bits: rounded
+                    // to float16 it may be zero, and 0 * inf is NaN.  8-bit values that are not finite are NaN anyway.)
+                    if (CAREFUL || (t + kTokens > lim_min && lim_min < rq.L)) {
+                        const P8 zero = {};
+                        f32x4_t z = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q) {
-                                const float pk = __shfl(element<PT, 1>(&pf[q], 0, e), from);
-                                const bool sees = t + k < lim[q];
+                        for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbase, c), zero, z);
+                        if (__any(!(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f))) {
+#pragma unroll 1
+                            for (int k = 0; k < kTokens; ++k) {
+                                // token k is element e of lane group (k / 4) % 4; the lane holds channels 16 c + 4 g ..
+                                const int e = (k & 3) + 4 * (k >> 4), from = ((k >> 2) & 3) * 16 + n;
+                                const uint32_t row = vbuf + k * S::RB + (E4 ? 4 * g : 8 * (g & 1));
+                                const int sw = S::v_swizzle(k);
 #pragma unroll
-                                for (int c = 0; c < CB; ++c) {
-                                    asm volatile("" : : : "memory");  // read four values at a time: registers are short
-                                    float v[4];
-                                    if constexpr (E4)
-                                        e4m3_to4(lds_read<uint32_t>(row + ((c ^ sw) * 16)), v);
-                                    else
-                                        widen4<T>(lds_read<u32x2_t>(row + (((2 * c + (g >> 1)) ^ sw) * 16)), v);
-                                    if (__any(sees && !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3])))) {
+                                for (int q = 0; q < NQ; ++q) {
+                                    float pk = 1.f;
+                                    if constexpr (!E4) {
+                                        float score = 0.f;
 #pragma unroll
-                                        for (int r = 0; r < 4; ++r)
-                                            o[q][c][r] += sees && !is_finite(v[r]) ? pk * v[r] : 0.f;
+                                        for (int x = 0; x < 8; ++x) score = x == e ? s[q][x >> 2][x & 3] : score;
+                                        pk = __shfl(fast_exp2(__builtin_fmaf(score, p.c, -(m[q] == kNegInf ? 0.f : m[q]))), from);
+                                    }
+                                    const bool sees = t + k < lim[q];
+#pragma unroll
+                                    for (int c = 0; c < CB; ++c) {
+                                        asm volatile("" : : : "memory");  // read four values at a time: registers are short
+                                        float v[4];
+                                        if constexpr (E4)
+                                            e4m3_to4(lds_read<uint32_t>(row + ((c ^ sw) * 16)), v);
+                                        else
+                                            widen4<T>(lds_read<u32x2_t>(row + (((2 * c + (g >> 1)) ^ sw) * 16)), v);
+                                        if (__any(sees && !(is_finite(v[0]) && is_finite(v[1]) && is_finite(v[2]) && is_finite(v[3])))) {
+#pragma unroll
+                                            for (int r = 0; r < 4; ++r)
+                                                o[q][c][r] += sees && !is_finite(v[r]) ? pk * v[r] : 0.f;
+                                        }
                                     }
                                 }
                             }
-                        }
-                        lds_drain();
+                            lds_drain();
 #pragma unroll 1
-                        for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
-                            u32x4v_t w = lds_read<u32x4v_t>(vbuf + slot * 16);
+                            for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
+                                u32x4v_t w = lds_read<u32x4v_t>(vbuf + slot * 16);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) w[x] = E4 ? finite_e4m3(w[x]) : finite_pair<T>(w[x]);
-                            lds_write(vbuf + slot * 16, w);
+                                for (int x = 0; x < 4; ++x) w[x] = E4 ? finite_e4m3(w[x]) : finite_pair<T>(w[x]);
+                                lds_write(vbuf + slot * 16, w);
+                            }
+                            lds_drain();
                         }
-                        lds_drain();
                     }
                 }
-            }
 #pragma unroll
-            for (int c = 0; c < CB; ++c) {
-                const P8 vf = v_frag(vbase, c);
+                for (int c = 0; c < CB; ++c) {
+                    const P8 vf = v_frag(vbase, c);
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    o[q][c] = mma16(vf, pf[q], o[q][c]);
-                    if constexpr (kTwoTerms<T, E4>) o[q][c] = mma16(vf, pr_rest[q], o[q][c]);
+                    for (int q = 0; q < NQ; ++q) {
+                        o[q][c] = mma16(vf, pf[q], o[q][c]);
+                        if constexpr (kTwoTerms<T, E4>) o[q][c] = mma16(vf, pr_rest[q], o[q][c]);
+                    }
                 }
+                lds_drain();
+                if (more) issue_v(i + 1, na, nb);
+                pa = na;
+                pb = nb;
+                na = fa;
+                nb = fb;
             }
-            lds_drain();
-            if (more) issue_v(i + 1, na, nb);
-            pa = na;
-            pb = nb;
-            na = fa;
-            nb = fb;
+        };
+        walk(std::false_type{});
+        // A float16 probability below 2^-25 is zero, and 0 * inf is NaN where the
+        // row should be infinite.  A wave that finds NaN beside good sums walks its
+        // tiles again, all of them looked over.  (bfloat16 has the range of the sums.)
+        if constexpr (!E4 && std::is_same<T, TypeF16>::value) {
+            bool nan = false;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                for (int c = 0; c < CB; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) nan |= lim[q] > 0 && o[q][c][r] != o[q][c][r] && is_finite(l[q]);
+            if (__any(nan)) {
+                issue_first();
+                clear();
+                walk(std::true_type{});
+            }
         }
 
         // ---- the waves' results through LDS ------------------------------

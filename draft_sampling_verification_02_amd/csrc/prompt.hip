@@ -92,7 +92,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     using E = typename T::E;
     constexpr int KS = D / 16, CB = D / 32;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[SH::LDS];
-    __shared__ int found[5], found_bad;
+    __shared__ int found[5], found_bad, found_nan;
 
     const PromptArgs &a = p.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     auto slot_of = [&](int off, int i) __device__ { return int((long long)off * p.G / SH::QB) + i; };
     if (tid == 0) {
         found[0] = -1;
-        found_bad = 0;
+        found_bad = found_nan = 0;
     }
     __syncthreads();
     for (int i = tid; i < a.B; i += SH::NT) {
@@ -258,10 +258,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         if (ntile > 1) issue_k(1);
     }
 
-    float m = kNegInf, l = 0.f;
+    float m, l;
     f32x16_t o[CB];
-#pragma unroll
-    for (int c = 0; c < CB; ++c) o[c] = f32x16_t{};
 
     // ---- the walk, one tile ahead: while the scores of tile j become
     // probabilities and meet V, the products of tile j + 1 with the queries run
@@ -319,15 +317,21 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         if (j + 2 < ntile) issue_k(j + 2);
         if (j + 1 < ntile) issue_v(j + 1);
     };
-    // Infinities or NaN among V rows that some queries must not see: the queries
-    // that see them get their share of them here, and then they leave the tile.
-    auto give_bad_shares = [&](int t, uint32_t vbuf, const V8 *pf) __device__ {
+    // What is not finite in a tile of V: the queries that see it get their share
+    // of it here, and then it leaves the tile.  The share's probability is taken
+    // anew in 32 bits: rounded to float16 it may be zero, and 0 * inf is NaN.  (What
+    // is called twice and holds the sums has to be inlined, or they go to memory.)
+    auto give_bad_shares = [&](int t, uint32_t vbuf) __device__ __attribute__((always_inline)) {
+        const float ms = m == kNegInf ? 0.f : m;
 #pragma unroll 1
         for (int k = 0; k < kKeys; ++k) {
-            // token k is element e of fragment k / 16, lane half (k / 4) % 2;
+            // token k is s[k / 32][4 ((k / 8) % 4) + k % 4] of lane half (k / 4) % 2;
             // the lane holds channels 32 c + 8 i + 4 h .. + 3
-            const int e = (k & 3) + 4 * ((k >> 3) & 1), sw = S::v_swizzle(k);
-            const float pk = __shfl(element<T, 4>(pf, k >> 4, e), n + 32 * ((k >> 2) & 1));
+            const int sw = S::v_swizzle(k), at = 16 * (k >> 5) + 4 * ((k >> 3) & 3) + (k & 3);
+            float score = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) score = e == at ? s[e >> 4][e & 15] : score;
+            const float pk = __shfl(fast_exp2(__builtin_fmaf(score, p.c, -ms)), n + 32 * ((k >> 2) & 1));
             const bool sees = t + k < lim;
 #pragma unroll
             for (int c = 0; c < CB; ++c)
@@ -360,11 +364,19 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         for (int c = 0; c < CB; ++c) o[c] = mma32(v_frag(vb, 16 * f, c), pf[f], o[c]);
     };
 
-    if (ntile > 0) {
-        scores(0, s);
-        hide(0, s);
-        raise(largest(s));
-    }
+    // nothing summed yet, the scores of tile 0
+    auto begin = [&]() __device__ __attribute__((always_inline)) {
+        m = kNegInf;
+        l = 0.f;
+#pragma unroll
+        for (int c = 0; c < CB; ++c) o[c] = f32x16_t{};
+        if (ntile > 0) {
+            scores(0, s);
+            hide(0, s);
+            raise(largest(s));
+        }
+    };
+    begin();
     // Tile j, which every query sees whole, with scores y; the next tile's scores
     // into x (HIDE: some of its keys may be hidden).  The two loops are the two halves of the work on
     // the matrix units; each step carries a share of the softmax and the LDS
@@ -423,6 +435,54 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             raise(max_x32(mx) * p.c);
         }
     };
+    // The tiles from j on one after another (CAREFUL: with every one looked over).
+    auto walk = [&](int j, auto careful_tag) __device__ __attribute__((always_inline)) {
+        constexpr bool CAREFUL = decltype(careful_tag)::value;
+        for (; j < ntile; ++j) {
+            turn(j);
+            const int t = j * kKeys;
+            const uint32_t vbuf = lds0 + (2 + (j & 1)) * S::BYTES;
+            // A V row that some queries must not see is harmless where it is finite,
+            // as their probabilities are zero.  The workgroup looks its tile over,
+            // a share a thread, for the rest.
+            bool bad = false;
+            if (CAREFUL || t + kKeys > gmin) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < SH::LPT; ++i) {
+                    const u32x4v_t w = lds_read<u32x4v_t>(vbuf + ((i * NW + wave) * 64 + lane) * 16);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) top = max_u16x2(top, w[q] & 0x7fff7fffu);
+                }
+                const uint32_t inf = T::kInf;
+                if (__any((top & 0xffffu) >= inf || (top >> 16) >= inf) && lane == 0) found_bad = j + 1;
+                wg_barrier();
+                bad = found_bad == j + 1;
+            }
+            if (t >= wmax) {
+                // none of the wave's queries sees the tile, and s still holds an earlier one's
+                // scores: they must not enter the sums again
+                if (bad) clean(vbuf);
+                continue;
+            }
+            if (bad) {
+                give_bad_shares(t, vbuf);
+                clean(vbuf);
+            }
+            const float ms = m == kNegInf ? 0.f : m;
+            V8 pf[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
+            const uint32_t vb = v_base(vbuf);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) product(vb, pf, f);
+            if (j + 1 < ntile && t + kKeys < wmax) {
+                scores(j + 1, s);
+                hide(j + 1, s);
+                raise(largest(s));
+            }
+        }
+    };
     // tiles that every query of the workgroup sees whole, then the rest
     const int nfull = min(max(gmin, 0) / kKeys, ntile);
     int j = 0;
@@ -438,52 +498,31 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             s[1] = x[1];
         }
     }
-    for (; j < ntile; ++j) {
-        turn(j);
-        const int t = j * kKeys;
-        const uint32_t vbuf = lds0 + (2 + (j & 1)) * S::BYTES;
-        // A V row that some queries must not see is harmless where it is finite,
-        // as their probabilities are zero.  The workgroup looks its tile over,
-        // a share a thread, for the rest.
-        bool bad = false;
-        if (t + kKeys > gmin) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < SH::LPT; ++i) {
-                const u32x4v_t w = lds_read<u32x4v_t>(vbuf + ((i * NW + wave) * 64 + lane) * 16);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) top = max_u16x2(top, w[q] & 0x7fff7fffu);
-            }
-            const uint32_t inf = T::kInf;
-            if (__any((top & 0xffffu) >= inf || (top >> 16) >= inf) && lane == 0) found_bad = j + 1;
-            wg_barrier();
-            bad = found_bad == j + 1;
-        }
-        if (t >= wmax) {
-            // none of the wave's queries sees the tile, and s still holds an earlier one's
-            // scores: they must not enter the sums again
-            if (bad) clean(vbuf);
-            continue;
-        }
-        const float ms = m == kNegInf ? 0.f : m;
-        V8 pf[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
-        if (bad) {
-            give_bad_shares(t, vbuf, pf);
-            clean(vbuf);
-        }
-        const uint32_t vb = v_base(vbuf);
-#pragma unroll
-        for (int f = 0; f < 4; ++f) product(vb, pf, f);
-        if (j + 1 < ntile && t + kKeys < wmax) {
-            scores(j + 1, s);
-            hide(j + 1, s);
-            raise(largest(s));
-        }
-    }
+    walk(j, std::false_type{});
 
     l = sum_x32(l);
+    // A float16 probability below 2^-25 is zero, and 0 * inf is NaN where the row
+    // should be infinite.  A workgroup that finds NaN beside a good sum walks its
+    // tiles again, all of them looked over.  (bfloat16 has the range of the sums.)
+    if constexpr (std::is_same<T, TypeF16>::value) {
+        bool nan = false;
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) nan |= o[c][r] != o[c][r];
+        if (__any(nan && is_finite(l) && qi < nq) && lane == 0) found_nan = 1;
+        wg_barrier();  // and every wave is done with the tiles
+        if (found_nan) {
+            issue_k(0);
+            issue_v(0);
+            vm_wait<SH::LPT>();
+            wg_barrier();
+            if (ntile > 1) issue_k(1);
+            begin();
+            walk(0, std::true_type{});
+            l = sum_x32(l);
+        }
+    }
     if (parts > 1) {
         if (qi >= nq) return;
         const long long part = (long long)unit * p.nsplit + split;

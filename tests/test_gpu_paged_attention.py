@@ -281,3 +281,34 @@ def test_two_calls_at_once_on_two_streams():
         for r in got:
             assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
             assert bool((r["out"][:1] == 0).all()) and bool((r["out"][13:] == 0).all())
+
+
+@pytest.mark.parametrize("width", [None, 80])  # walked whole, and split and joined
+@pytest.mark.parametrize("rows,G", [([1, 1], 4), ([12, 3], 5)])
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinities_reach_rows_that_hardly_weigh_them(width, rows, G, dtype, D):
+    # scores spread over some 60 units, so that most probabilities are far below
+    # float16's smallest value: a visible infinity still makes its channel
+    # infinite, and infinities of both signs make it NaN
+    ds = _ds()
+    Hkv, page, lens = 2, 16, [700, 333]
+    print(f"paged: rows={rows} G={G} D={D} {dtype} width={width}", flush=True)
+    pg = Paged([p + r for p, r in zip(lens, rows)], Hkv, D, page, dtype, dtype, 8, width=width)
+    marks = [(3, 5, math.inf), (300, 9, -math.inf), (81, 9, math.inf), (20, D - 1, math.inf), (75, 11, math.nan)]
+    for b, last in enumerate([lens[0] + rows[0] - 1, lens[1]]):
+        for t, c, x in marks + [(last, 13, -math.inf)]:  # seen by the last row only, and by all rows but those before the newest
+            pg.buf["v"][int(pg.table[b, t // page]), :, t % page, c] = x
+            pg.tokens["v"][b][t, :, c] = 0.0
+    q = (8.0 / 1.5 * torch.randn((sum(rows), Hkv * G, D), generator=torch.Generator().manual_seed(2))).to(dtype)
+    dev = pg.on("cuda")
+    off = None if rows == [1, 1] else offsets(rows).cuda()
+    r = ds.dspark_paged_attention(q.cuda(), dev["k_cache"], dev["v_cache"], torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                  dev["page_table"], row_offsets=off, lse=True)
+    torch.cuda.synchronize()
+    out, lse, tol, lt = _expect(pg, q, rows, lens, G, True, D ** -0.5, dtype)
+    for t, c, x in marks:
+        out[:, :, c] += x  # inf - inf is NaN
+    out[rows[0] - 1:, :, 13] = -math.inf
+    check("out", r["out"], out, tol)
+    check("lse", r["lse"], lse, lt)

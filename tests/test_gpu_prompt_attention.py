@@ -333,3 +333,40 @@ def test_blocks_with_different_numbers_of_parts_are_joined(dtype, D, causal):
             at += n
         for n in ("out", "lse"):
             assert bool((r[n][:lead] == 7.0).all()) and bool((r[n][at:] == 7.0).all())
+
+
+@pytest.mark.parametrize("rows,keys,Hkv,G", [([300], None, 1, 1), ([90, 200], None, 2, 3), ([50], [3000], 1, 4)])
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_infinities_reach_rows_that_hardly_weigh_them(rows, keys, Hkv, G, dtype, D):
+    # scores spread over some 60 units, so that most probabilities are far below
+    # float16's smallest value: a visible infinity still makes its channel
+    # infinite, and infinities of both signs make it NaN
+    ds = _ds()
+    lens = keys or rows
+    print(f"prompt: rows={rows} keys={keys} Hkv={Hkv} G={G} D={D} {dtype}", flush=True)
+    need = ds.dspark_prompt_attention_workspace_size(len(rows), sum(rows), sum(lens), Hkv * G, Hkv, D)
+    assert (need > 256) == (max(lens) >= 3000)
+    g = torch.Generator().manual_seed(D)
+    q = torch.randn((sum(rows), Hkv * G, D), generator=g).to(dtype)
+    k, v = (torch.randn((sum(lens), Hkv, D), generator=g).to(dtype) for _ in range(2))
+    marks = [(3, 5, math.inf), (70, 9, -math.inf), (81, 9, math.inf), (20, D - 1, math.inf), (75, 11, math.nan)]  # token, channel, value
+    clean, at = v.clone(), 0
+    for L in lens:
+        for t, c, x in marks:
+            v[at + t, :, c], clean[at + t, :, c] = x, 0.0
+        at += L
+    scale = 8.0 * D ** -0.5
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets(rows).cuda(),
+                                   kv_offsets=None if keys is None else offsets(keys).cuda(), scale=scale, lse=True)
+    torch.cuda.synchronize()
+    at = kat = 0
+    for b, (n, L) in enumerate(zip(rows, lens)):
+        o, z, tol, lt = attend(q[at:at + n].double(), k[kat:kat + L].double(), clean[kat:kat + L].double(),
+                               [L - n + i + 1 for i in range(n)], scale, U[dtype], U[dtype])
+        for t, c, x in marks:
+            first = max(0, n - L + t)  # the first row that sees token t
+            o[first:, :, c] += x  # inf - inf is NaN
+        check(f"out of {b}", r["out"][at:at + n], o, tol)
+        check(f"lse of {b}", r["lse"][at:at + n], z, lt)
+        at, kat = at + n, kat + L
