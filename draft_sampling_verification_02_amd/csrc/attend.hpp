@@ -223,6 +223,19 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
     return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
 }
 
+// Exponents of a softmax are fma(score, c, -m), the product unrounded, which is
+// one instruction; m is itself a rounded product, so that the largest exponent
+// is not 0 but m's rounding error: half a step of m.  From kFar on (half a step:
+// 1/16) that would grow past any range of the probabilities, to zeros or
+// infinities for all: there the products are rounded first.
+constexpr float kFar = 1048576.f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m != kNegInf; }
+__device__ __forceinline__ float far_exponent(float score, float c, float m) {
+#pragma clang fp contract(off)
+    const float product = score * c;
+    return product - (m == kNegInf ? 0.f : m);
+}
+
 // The natural logsumexp from the running maximum (base-2 units) and sum.
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? kNegInf : (m + fast_log2(l)) * kLn2;

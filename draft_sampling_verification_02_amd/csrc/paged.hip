@@ -382,12 +382,15 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
         const int lim_min = uniform(a.causal ? min(rq.L, rq.past + (grp * QB) / p.G + 1) : rq.L);
 
         float m[NQ], l[NQ];
+        bool far[NQ];  // the maximum of one of the 16 queries is far from zero
         f32x4_t o[NQ][CB];
+        auto reference = [&](int q) __device__ { return far[q] || m[q] == kNegInf ? 0.f : m[q]; };
         auto clear = [&]() __device__ {
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 m[q] = kNegInf;
                 l[q] = 0.f;
+                far[q] = false;
 #pragma unroll
                 for (int c = 0; c < CB; ++c) o[q][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
             }
@@ -472,11 +475,18 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
 #pragma unroll
                         for (int c = 0; c < CB; ++c) o[q][c] *= al;
                         m[q] = mn;
+                        far[q] = __any(is_far(mn));
                     }
-                    const float ms = mn == kNegInf ? 0.f : mn;
+                    if (far[q]) {  // scores far from zero become exponents at once
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) s[q][hf][r] = far_exponent(s[q][hf][r], p.c, mn);
+                    }
+                    const float ms = reference(q), cs = far[q] ? 1.f : p.c;
                     float pr[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) pr[e] = fast_exp2(__builtin_fmaf(s[q][e >> 2][e & 3], p.c, -ms));
+                    for (int e = 0; e < 8; ++e) pr[e] = fast_exp2(__builtin_fmaf(s[q][e >> 2][e & 3], cs, -ms));
                     l[q] += ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
                     if constexpr (E4) {
 #pragma unroll
@@ -532,7 +542,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                                         float score = 0.f;
 #pragma unroll
                                         for (int x = 0; x < 8; ++x) score = x == e ? s[q][x >> 2][x & 3] : score;
-                                        pk = __shfl(fast_exp2(__builtin_fmaf(score, p.c, -(m[q] == kNegInf ? 0.f : m[q]))), from);
+                                        pk = __shfl(fast_exp2(__builtin_fmaf(score, far[q] ? 1.f : p.c, -reference(q))), from);
                                     }
                                     const bool sees = t + k < lim[q];
 #pragma unroll

@@ -258,7 +258,8 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         if (ntile > 1) issue_k(1);
     }
 
-    float m, l;
+    float m, l, cs = p.c;  // maximum and sum; what scores are multiplied by
+    bool far = false;      // the maximum of a query of the wave is far from zero
     f32x16_t o[CB];
 
     // ---- the walk, one tile ahead: while the scores of tile j become
@@ -292,7 +293,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     // the sums keep their scale until the maximum has grown by kSlack (base-2
     // units): probabilities stay below 2^kSlack, far from any type's range, and
     // the products are rarely rescaled
-    auto raise = [&](float mx) __device__ {
+    auto raise = [&](float mx, f32x16_t *x) __device__ {
         if (__any(mx > m + kSlack)) {
             const float mn = fmaxf(m, mx);
             const float al = fast_exp2(m - (mn == kNegInf ? 0.f : mn));
@@ -300,12 +301,22 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
 #pragma unroll
             for (int c = 0; c < CB; ++c) o[c] *= al;
             m = mn;
+            far = __any(is_far(m));
+        }
+        // (scores far from zero become exponents at once)
+        cs = far ? 1.f : p.c;
+        if (far) {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[tb][r] = far_exponent(x[tb][r], p.c, m);
         }
     };
+    auto reference = [&]() __device__ { return far || m == kNegInf ? 0.f : m; };
     auto probabilities = [&](const f32x16_t *x, float ms, int f, V8 &pf) __device__ {
         float e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = fast_exp2(__builtin_fmaf(x[f >> 1][8 * (f & 1) + i], p.c, -ms));
+        for (int i = 0; i < 8; ++i) e[i] = fast_exp2(__builtin_fmaf(x[f >> 1][8 * (f & 1) + i], cs, -ms));
         l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
         pf = V8{E(e[0]), E(e[1]), E(e[2]), E(e[3]), E(e[4]), E(e[5]), E(e[6]), E(e[7])};
     };
@@ -322,7 +333,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     // anew in 32 bits: rounded to float16 it may be zero, and 0 * inf is NaN.  (What
     // is called twice and holds the sums has to be inlined, or they go to memory.)
     auto give_bad_shares = [&](int t, uint32_t vbuf) __device__ __attribute__((always_inline)) {
-        const float ms = m == kNegInf ? 0.f : m;
+        const float ms = reference();
 #pragma unroll 1
         for (int k = 0; k < kKeys; ++k) {
             // token k is s[k / 32][4 ((k / 8) % 4) + k % 4] of lane half (k / 4) % 2;
@@ -331,7 +342,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             float score = 0.f;
 #pragma unroll
             for (int e = 0; e < 32; ++e) score = e == at ? s[e >> 4][e & 15] : score;
-            const float pk = __shfl(fast_exp2(__builtin_fmaf(score, p.c, -ms)), n + 32 * ((k >> 2) & 1));
+            const float pk = __shfl(fast_exp2(__builtin_fmaf(score, cs, -ms)), n + 32 * ((k >> 2) & 1));
             const bool sees = t + k < lim;
 #pragma unroll
             for (int c = 0; c < CB; ++c)
@@ -368,12 +379,13 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     auto begin = [&]() __device__ __attribute__((always_inline)) {
         m = kNegInf;
         l = 0.f;
+        far = false;
 #pragma unroll
         for (int c = 0; c < CB; ++c) o[c] = f32x16_t{};
         if (ntile > 0) {
             scores(0, s);
             hide(0, s);
-            raise(largest(s));
+            raise(largest(s), s);
         }
     };
     begin();
@@ -385,7 +397,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         constexpr bool HIDE = decltype(hide_tag)::value;
         turn(jj);
         const uint32_t kb = k_base(lds0 + ((jj + 1) & 1) * S::BYTES), vb = v_base(lds0 + (2 + (jj & 1)) * S::BYTES);
-        const float ms = m == kNegInf ? 0.f : m;
+        const float ms = reference();
         // operands held: reads run one (K) and two (V) steps ahead (one more of each
         // is 1% slower at D = 128 and the same at D = 64)
         constexpr int KA = 2, VA = 3;
@@ -409,7 +421,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
 #pragma unroll
             for (int i = 0; i < EPS; ++i) {
                 const int e = k * EPS + i;
-                const float pr = fast_exp2(__builtin_fmaf(y[e >> 4][e & 15], p.c, -ms));
+                const float pr = fast_exp2(__builtin_fmaf(y[e >> 4][e & 15], cs, -ms));
                 sum += pr;
                 pf[e >> 3][e & 7] = E(pr);
             }
@@ -430,9 +442,9 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         }
         if constexpr (HIDE) {
             hide(jj + 1, x);
-            raise(largest(x));
+            raise(largest(x), x);
         } else {
-            raise(max_x32(mx) * p.c);
+            raise(max_x32(mx) * p.c, x);
         }
     };
     // The tiles from j on one after another (CAREFUL: with every one looked over).
@@ -469,7 +481,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
                 give_bad_shares(t, vbuf);
                 clean(vbuf);
             }
-            const float ms = m == kNegInf ? 0.f : m;
+            const float ms = reference();
             V8 pf[4];
 #pragma unroll
             for (int f = 0; f < 4; ++f) probabilities(s, ms, f, pf[f]);
@@ -479,7 +491,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             if (j + 1 < ntile && t + kKeys < wmax) {
                 scores(j + 1, s);
                 hide(j + 1, s);
-                raise(largest(s));
+                raise(largest(s), s);
             }
         }
     };

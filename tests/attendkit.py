@@ -150,3 +150,24 @@ def offsets(rows, lead=0):
     for r in rows:
         off.append(off[-1] + r)
     return torch.tensor(off, dtype=torch.int32)
+
+
+def far_inputs(rows, keys, Hq, Hkv, D, dtype, seed):
+    """q, k, v and a scale whose scores are exact in 32 bits: multiples of 2^30
+    for rows 0, 3, .., of 8 for rows 1, 4, .. and zeros for the others."""
+    g = torch.Generator().manual_seed(seed)
+    q, k = torch.zeros(rows, Hq, D), torch.zeros(keys, Hkv, D)
+    q[0::3, :, 0], q[1::3, :, 0] = 2.0 ** 15, 2.0 ** -12
+    k[:, :, 0] = 2.0 ** 8 * torch.randint(-7, 8, (keys, Hkv), generator=g).float()
+    v = torch.randn(keys, Hkv, D, generator=g)
+    return q.to(dtype), k.to(dtype), v.to(dtype), 128.0
+
+
+def far_tolerances(out, lse, tol, lse_tol, v, u_out):
+    """Tolerances of rows 0, 3, ..: a score is exact, and a step of it is 2^30, so
+    a probability is 1 or 0; what is left is the sum of at most n equal terms,
+    its division, and the roundings of the results."""
+    n = v.shape[0]
+    tol[0::3] = (n + 4) * U32 * v.abs().max() + u_out * out[0::3].abs()
+    lse_tol[0::3] = 8 * U32 * lse[0::3].abs()
+    return tol, lse_tol

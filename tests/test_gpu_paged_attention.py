@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from attendkit import U, Paged, attend, check, offsets
+from attendkit import U, Paged, attend, check, dequantise, far_inputs, far_tolerances, offsets, quantise
 
 pytestmark = pytest.mark.gpu
 
@@ -312,3 +312,31 @@ def test_infinities_reach_rows_that_hardly_weigh_them(width, rows, G, dtype, D):
     out[rows[0] - 1:, :, 13] = -math.inf
     check("out", r["out"], out, tol)
     check("lse", r["lse"], lse, lt)
+
+
+@pytest.mark.parametrize("rows,past", [(1, 300), (3, 5000), (40, 700), (40, 2000)])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4), (FH, E4)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_far_from_zero(rows, past, dtype, cache, D):
+    # scores of 2^30 and more beside ordinary ones: half a step of a 32-bit
+    # maximum is more than the range of the probabilities
+    ds = _ds()
+    page, Hkv, L = 16, 2, past + rows
+    pages = -(-L // page)
+    q, k, v, scale = far_inputs(rows, pages * page, 6, Hkv, D, dtype, D + rows)
+    paged = lambda x: x.reshape(pages, page, *x.shape[1:]).transpose(1, 2).contiguous().cuda()
+    if cache == E4:
+        (kq, ks), (vq, vs) = quantise(k), quantise(v)
+        k, v = dequantise(kq, ks), dequantise(vq, vs)
+        args = dict(k_cache=paged(kq.float().to(E4)), v_cache=paged(vq.float().to(E4)), k_scale=paged(ks), v_scale=paged(vs))
+    else:
+        args = dict(k_cache=paged(k), v_cache=paged(v))
+    r = ds.dspark_paged_attention(q.cuda(), cache_len=torch.tensor([past], dtype=torch.int32, device="cuda"),
+                                  page_table=torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+                                  row_offsets=offsets([rows]).cuda(), scale=scale, lse=True, **args)
+    torch.cuda.synchronize()
+    up = (U[BF] if dtype == BF else U[BF] ** 2) if cache == E4 else U[dtype]
+    o, z, tol, lt = attend(q.double(), k[:L].double(), v[:L].double(), [past + i + 1 for i in range(rows)], scale, up, U[dtype])
+    tol, lt = far_tolerances(o, z, tol, lt, v, U[dtype])
+    check("out", r["out"], o, tol)
+    check("lse", r["lse"], z, lt)

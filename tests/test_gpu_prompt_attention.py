@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from attendkit import U, attend, check, offsets
+from attendkit import U, attend, check, far_inputs, far_tolerances, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -370,3 +370,24 @@ def test_infinities_reach_rows_that_hardly_weigh_them(rows, keys, Hkv, G, dtype,
         check(f"out of {b}", r["out"][at:at + n], o, tol)
         check(f"lse of {b}", r["lse"][at:at + n], z, lt)
         at, kat = at + n, kat + L
+
+
+@pytest.mark.parametrize("rows,keys,G", [(200, 200, 1), (70, 90, 3), (40, 3000, 2)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_far_from_zero(rows, keys, G, causal, dtype, D):
+    # scores of 2^30 and more beside ordinary ones: half a step of a 32-bit
+    # maximum is more than the range of the probabilities
+    ds = _ds()
+    q, k, v, scale = far_inputs(rows, keys, G, 1, D, dtype, D + rows)
+    need = ds.dspark_prompt_attention_workspace_size(1, rows, keys, G, 1, D)
+    assert (need > 256) == (keys >= 3000)
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets([rows]).cuda(), kv_offsets=offsets([keys]).cuda(),
+                                   scale=scale, causal=causal, lse=True)
+    torch.cuda.synchronize()
+    o, z, tol, lt = attend(q.double(), k.double(), v.double(), [keys - rows + i + 1 if causal else keys for i in range(rows)],
+                           scale, U[dtype], U[dtype])
+    tol, lt = far_tolerances(o, z, tol, lt, v, U[dtype])
+    check("out", r["out"], o, tol)
+    check("lse", r["lse"], z, lt)
