@@ -236,7 +236,18 @@ __device__ __forceinline__ float far_exponent(float score, float c, float m) {
     return product - (m == kNegInf ? 0.f : m);
 }
 
-// The natural logsumexp from the running maximum (base-2 units) and sum.
+// The reference of a softmax whose probabilities are of type T: the maximum, for
+// float16, whose range is narrow, lowered by `lift` (far from zero that would be
+// lost in the maximum's own rounding).
+template <typename T>
+__device__ __forceinline__ float lowered(float mx, float lift) {
+    if constexpr (std::is_same<T, TypeF16>::value)
+        return fabsf(mx) < kFar ? mx - lift : mx;
+    else
+        return mx;
+}
+
+// The natural logsumexp from the reference (base-2 units) and the sum.
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? kNegInf : (m + fast_log2(l)) * kLn2;
 }

@@ -146,6 +146,11 @@ struct ProbType<T, true> {
 template <typename T, bool E4>
 constexpr bool kTwoTerms = E4 && std::is_same<T, TypeF16>::value;
 
+// float16 probabilities are held up to 2^14 times as large: relative to the
+// largest, float16 then keeps its eleven bits down to 2^-28 instead of 2^-14,
+// where a long cache's many small shares would be lost.
+constexpr float kLift = 14.f;
+
 // LDS of a workgroup of nw waves and how many share a compute unit.
 constexpr int paged_body(bool e4, int d, int nq, int nw) {
     const int ring = nw * (2 * kTokens * (e4 ? d : 2 * d) + (e4 ? 256 : 0));
@@ -467,7 +472,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                     }
                     float mx = fmaxf(fmaxf(fmaxf(s[q][0][0], s[q][0][1]), fmaxf(s[q][0][2], s[q][0][3])),
                                      fmaxf(fmaxf(s[q][1][0], s[q][1][1]), fmaxf(s[q][1][2], s[q][1][3])));
-                    mx = max_x16(max_x32(mx)) * p.c;
+                    mx = lowered<PT>(max_x16(max_x32(mx)) * p.c, kLift);
                     const float mn = fmaxf(m[q], mx);
                     if (__any(mn > m[q])) {
                         const float al = fast_exp2(m[q] - (mn == kNegInf ? 0.f : mn));
@@ -591,7 +596,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
             }
         };
         walk(std::false_type{});
-        // A float16 probability below 2^-25 is zero, and 0 * inf is NaN where the
+        // A small enough float16 probability is zero, and 0 * inf is NaN where the
         // row should be infinite.  A wave that finds NaN beside good sums walks its
         // tiles again, all of them looked over.  (bfloat16 has the range of the sums.)
         if constexpr (!E4 && std::is_same<T, TypeF16>::value) {

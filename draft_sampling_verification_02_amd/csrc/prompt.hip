@@ -47,7 +47,14 @@ constexpr int kKeys = 64;      // tokens of a tile
 constexpr int kPromptWaves = 4;                      // of a workgroup
 constexpr int kPromptQueries = 32 * kPromptWaves;    // queries of a workgroup
 constexpr int kMinTiles = 2;                         // tiles of a split at least
-constexpr float kSlack = 8.f;  // growth of the running maximum that is left alone, base-2 units
+// Growth of the running maximum that is left alone, base-2 units; and how far
+// the softmax's reference lies below a float16 row's maximum.  Held 2^11 times as
+// large, float16 probabilities keep their eleven bits down to 2^-25 of the
+// largest instead of 2^-14, where the many small shares of a long prompt would be
+// lost; with the slack they stay below 2^16.
+template <typename T>
+constexpr float kSlack = std::is_same<T, TypeF16>::value ? 4.f : 8.f;
+constexpr float kLift = 11.f;
 
 struct PromptParams {
     PromptArgs a;
@@ -288,13 +295,12 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         float mx = fmaxf(x[0][0], x[1][0]);
 #pragma unroll
         for (int r = 1; r < 16; ++r) mx = fmaxf(fmaxf(x[0][r], x[1][r]), mx);
-        return max_x32(mx) * p.c;
+        return lowered<T>(max_x32(mx) * p.c, kLift);
     };
-    // the sums keep their scale until the maximum has grown by kSlack (base-2
-    // units): probabilities stay below 2^kSlack, far from any type's range, and
-    // the products are rarely rescaled
+    // the sums keep their scale until the maximum has grown by kSlack: probabilities
+    // stay inside any type's range, and the products are rarely rescaled
     auto raise = [&](float mx, f32x16_t *x) __device__ {
-        if (__any(mx > m + kSlack)) {
+        if (__any(mx > m + kSlack<T>)) {
             const float mn = fmaxf(m, mx);
             const float al = fast_exp2(m - (mn == kNegInf ? 0.f : mn));
             l *= al;
@@ -444,7 +450,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             hide(jj + 1, x);
             raise(largest(x), x);
         } else {
-            raise(max_x32(mx) * p.c, x);
+            raise(lowered<T>(max_x32(mx) * p.c, kLift), x);
         }
     };
     // The tiles from j on one after another (CAREFUL: with every one looked over).
@@ -513,7 +519,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     walk(j, std::false_type{});
 
     l = sum_x32(l);
-    // A float16 probability below 2^-25 is zero, and 0 * inf is NaN where the row
+    // A small enough float16 probability is zero, and 0 * inf is NaN where the row
     // should be infinite.  A workgroup that finds NaN beside a good sum walks its
     // tiles again, all of them looked over.  (bfloat16 has the range of the sums.)
     if constexpr (std::is_same<T, TypeF16>::value) {

@@ -46,7 +46,7 @@ def dequantise(q: torch.Tensor, s: torch.Tensor) -> torch.Tensor:
     return q.double() * torch.exp2(s.double() - 127.0)[..., None]
 
 
-def attend(q, k, v, limits, scale, u_prob, u_out):
+def attend(q, k, v, limits, scale, u_prob, u_out, lift=0):
     """q [R, Hq, D] float64 against k, v [L, Hkv, D]; row i sees tokens t < limits[i].
     Returns (out, lse, out_tol, lse_tol).
 
@@ -58,7 +58,8 @@ def attend(q, k, v, limits, scale, u_prob, u_out):
     terms in 32 bits by L U32.  All of them weigh |v|: out is off by at most
     (u_prob + 2 (es + ...)) sum p|v|, and by u_out |out| from its own rounding.
     A float16 probability below 2^-14 is off by up to 2^-25 absolute instead,
-    against a sum of at least 1 in the same units."""
+    against a sum of at least 1 in the same units (of 2^lift, where the largest
+    probability is held as 2^lift at least)."""
     R, Hq, D = q.shape
     G = Hq // k.shape[1]
     out = torch.zeros(R, Hq, D, dtype=torch.float64)
@@ -78,7 +79,7 @@ def attend(q, k, v, limits, scale, u_prob, u_out):
         es = (D + 8) * U32 * scale * torch.einsum("hd,nhd->hn", q[i].abs(), kk.abs()).max(1).values
         es = es + 4 * U32 * s.abs().max(1).values + 8 * U32
         A = torch.einsum("hn,nhd->hd", p, vv.abs())
-        small = 2.0 ** -25 * vv.abs().sum(0) / torch.exp(z - s.max(1).values)[:, None] if u_prob == U[torch.float16] else 0.0
+        small = 2.0 ** (-25 - lift) * vv.abs().sum(0) / torch.exp(z - s.max(1).values)[:, None] if u_prob == U[torch.float16] else 0.0
         tol[i] = (u_prob + 2 * (es + n * U32))[:, None] * A + small + u_out * out[i].abs()
         lse_tol[i] = es + n * U32 + 4 * U32 * z.abs()
     return out, lse, tol * 1.01 + 1e-30, lse_tol * 1.01 + 1e-30

@@ -340,3 +340,32 @@ def test_scores_far_from_zero(rows, past, dtype, cache, D):
     tol, lt = far_tolerances(o, z, tol, lt, v, U[dtype])
     check("out", r["out"], o, tol)
     check("lse", r["lse"], z, lt)
+
+
+@pytest.mark.parametrize("rows,past", [(1, 700), (1, 9000), (9, 500), (9, 9000)])  # walked whole, and split and joined
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_small_float16_probabilities_count(rows, past, D):
+    # one key stands 26 powers of two above all others, whose values alone make
+    # the output: each is below float16's smallest half step beside the first one's 1
+    ds = _ds()
+    g = torch.Generator().manual_seed(D)
+    page, L = 16, past + rows
+    pages = -(-L // page)
+    q = 0.01 * torch.randn((rows, 4, D), generator=g)
+    q[:, :, 0] = 4.0
+    k = 0.05 * torch.randn((pages * page, 2, D), generator=g)
+    k[:, :, 0] = 0.0
+    k[0, :, 0] = 26.0 * math.log(2.0) / 4.0
+    v = 64.0 + 64.0 * torch.rand((pages * page, 2, D), generator=g)
+    v[0] = 0.0
+    q, k, v = q.to(FH), k.to(FH), v.to(FH)
+    kc, vc = (x.reshape(pages, page, 2, D).transpose(1, 2).contiguous().cuda() for x in (k, v))
+    r = ds.dspark_paged_attention(q.cuda(), kc, vc, torch.tensor([past], dtype=torch.int32, device="cuda"),
+                                  torch.arange(pages, dtype=torch.int32, device="cuda")[None], row_offsets=offsets([rows]).cuda(),
+                                  scale=1.0, lse=True)
+    torch.cuda.synchronize()
+    o, z, tol, lt = attend(q.double(), k[:L].double(), v[:L].double(), [past + i + 1 for i in range(rows)], 1.0, U[FH], U[FH],
+                           lift=14)
+    assert bool((tol < 0.01 * o.abs()).all())
+    check("out", r["out"], o, tol)
+    check("lse", r["lse"], z, lt)

@@ -391,3 +391,33 @@ def test_scores_far_from_zero(rows, keys, G, causal, dtype, D):
     tol, lt = far_tolerances(o, z, tol, lt, v, U[dtype])
     check("out", r["out"], o, tol)
     check("lse", r["lse"], z, lt)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("keys", [150, 700, 4100])  # walked by one workgroup, cut and joined
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_small_float16_probabilities_count(D, keys, causal):
+    # one key stands 26 powers of two above all others, whose values
+    # alone make the output: each is below float16's smallest half step beside
+    # the first one's 1
+    ds = _ds()
+    g = torch.Generator().manual_seed(D)
+    rows = 40
+    need = ds.dspark_prompt_attention_workspace_size(1, rows, keys, 2, 1, D)
+    assert (need > 256) == (keys >= 700)
+    q = 0.01 * torch.randn((rows, 2, D), generator=g)
+    q[:, :, 0] = 4.0
+    k = 0.05 * torch.randn((keys, 1, D), generator=g)
+    k[:, :, 0] = 0.0
+    k[0, :, 0] = 26.0 * math.log(2.0) / 4.0
+    v = 64.0 + 64.0 * torch.rand((keys, 1, D), generator=g)
+    v[0] = 0.0
+    q, k, v = q.to(FH), k.to(FH), v.to(FH)
+    r = ds.dspark_prompt_attention(q.cuda(), k.cuda(), v.cuda(), offsets([rows]).cuda(), kv_offsets=offsets([keys]).cuda(),
+                                   scale=1.0, causal=causal, lse=True)
+    torch.cuda.synchronize()
+    o, z, tol, lt = attend(q.double(), k.double(), v.double(), [keys - rows + i + 1 if causal else keys for i in range(rows)],
+                           1.0, U[FH], U[FH], lift=11)
+    assert bool((tol < 0.01 * o.abs()).all())
+    check("out", r["out"], o, tol)
+    check("lse", r["lse"], z, lt)
