@@ -682,7 +682,7 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     type, bfloat16 for a float8_e4m3fn cache); rows of no request keep what
     ``out`` holds (zeros in a new result)."""
     torch = _torch()
-    if out is not None and stream is None and dtype is out["k"].dtype and n_rows == out["k"].shape[0]:
+    if out is not None and stream is None and dtype is getattr(out["k"], "dtype", 0) and n_rows == out["k"].shape[0]:
         st = (_short or _load_marshal()).kv_read(k_cache, v_cache, page_table, row_offsets, first, k_scale, v_scale,
                                                    out["k"], out["v"])
         if st is not None:
