@@ -133,3 +133,66 @@ def test_prompts_then_rounds(cache):
     torch.cuda.synchronize()
     k, v = history(torch.tensor(sum(tokens, [])))
     assert torch.equal(back["k"].cpu().double(), k) and torch.equal(back["v"].cpu().double(), v)
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_a_captured_round_follows_the_lengths(cache):
+    # the write of a round's rows and their attention, captured once and replayed
+    # while rows, offsets and lengths change on the device, with eager work of
+    # the same operators between the replays
+    import draft_sampling_verification_02_amd as ds
+    ds.load_library()
+    g = torch.Generator().manual_seed(9)
+    B, Hq, Hkv, D, page, width, N = 5, 8, 2, 64, 16, 90, 24
+    dev = "cuda"
+    table = torch.randperm(B * width, generator=g).to(torch.int32).reshape(B, width).to(dev)
+    kc, vc = (torch.full((B * width, Hkv, page, D), float("nan"), dtype=torch.float32, device=dev).to(cache) for _ in range(2))
+    sc = {} if cache == BF else {n: torch.zeros((B * width, Hkv, page), dtype=torch.uint8, device=dev) for n in ("k_scale", "v_scale")}
+    held = lambda x: x.double() if cache == BF else dequantise(*quantise(x))
+    lens = [1200, 0, 37, 500, 64]
+    past_k, past_v = ([torch.randn((n, Hkv, D), generator=g).to(BF) for n in lens] for _ in range(2))
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+    ds.dspark_kv_write(torch.cat(past_k).to(dev), torch.cat(past_v).to(dev), kc, vc, torch.zeros(B, dtype=torch.int32, device=dev),
+                       table, row_offsets=off, **sc)
+    q, k, v = (torch.randn((N, h, D), generator=g).to(BF).to(dev) for h in (Hq, Hkv, Hkv))
+    cache_len = torch.tensor(lens, dtype=torch.int32, device=dev)
+    roff = torch.tensor([0, 1, 2, 3, 4, 5], dtype=torch.int32, device=dev)
+    kept = torch.zeros(B, dtype=torch.int32, device=dev)
+
+    def step(**kw):
+        ds.dspark_kv_write(k, v, kc, vc, cache_len, table, row_offsets=roff, **sc)
+        return ds.dspark_paged_attention(q, kc, vc, cache_len, table, row_offsets=roff, lse=True, max_rows=6, **sc, **kw)
+
+    res = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out=res)
+        cache_len.add_(kept)
+    for rnd, rows in enumerate(([1, 2, 6, 0, 3], [6, 6, 1, 1, 6], [0, 0, 0, 24, 0], [5, 1, 2, 3, 4], [1, 1, 1, 1, 1])):
+        new = [torch.randn((N, h, D), generator=g).to(BF) for h in (Hq, Hkv, Hkv)]
+        for dst, src in zip((q, k, v), new):
+            dst.copy_(src)
+        roff.copy_(torch.tensor(np.concatenate([[0], np.cumsum(rows)]), dtype=torch.int32))
+        stay = [min(r, 1 + (rnd + b) % 3) for b, r in enumerate(rows)]
+        kept.copy_(torch.tensor(stay, dtype=torch.int32))
+        before = cache_len.clone()
+        res["out"].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert cache_len.tolist() == [x + y for x, y in zip(before.tolist(), stay)]
+        eager = ds.dspark_paged_attention(q, kc, vc, before, table, row_offsets=roff, lse=True, max_rows=6, **sc)
+        ds.dspark_prompt_attention(q, k, v, roff)
+        torch.cuda.synchronize()
+        n = sum(rows)
+        assert torch.equal(eager["out"][:n], res["out"][:n]) and torch.equal(eager["lse"][:n], res["lse"][:n])
+        assert bool((res["out"][n:] == 7.0).all())
+        at = 0
+        for b, r in enumerate(rows):
+            kk, vv = (torch.cat([p[b], x[at:at + r]]) for p, x in ((past_k, new[1]), (past_v, new[2])))
+            o, z, tol, lt = attend(new[0][at:at + r].double(), held(kk), held(vv), [len(past_k[b]) + i + 1 for i in range(r)],
+                                   D ** -0.5, U[BF], U[BF])
+            check(f"replay {rnd} request {b} out", res["out"][at:at + r], o, tol)
+            check(f"replay {rnd} request {b} lse", res["lse"][at:at + r], z, lt)
+            past_k[b], past_v[b] = kk[:len(past_k[b]) + stay[b]], vv[:len(past_v[b]) + stay[b]]
+            at += r
