@@ -318,12 +318,6 @@ __global__ __launch_bounds__(kCacheThreads, 8) void kv_read_kernel(CacheParams p
     }
 }
 
-int log2_of(int x) {
-    int s = 0;
-    while ((1 << s) < x) ++s;
-    return s;
-}
-
 template <typename T, bool E4>
 void launch_cache_typed(const CacheParams &p, bool write, bool many, int blocks, hipStream_t s) {
     const dim3 grid(blocks), block(kCacheThreads);

@@ -1,5 +1,5 @@
 // internal.hpp -- declarations shared by the host entry points (api.cpp) and
-// the kernel translation units (draft.hip, verify.hip, debug.hip).
+// the kernel translation units.
 #pragma once
 
 #include <hip/hip_ext.h>
@@ -249,6 +249,13 @@ struct StsArgs {
 hipError_t launch_sts(const StsArgs &a, const StsPlan &p, const StsWork &w, hipStream_t s);
 
 // ---- paged key-value cache and attention --------------------------------
+
+// exponent of a power of two
+inline int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
 
 // One cache call: rows [n_rows, Hkv, D] against the slots of a paged cache.
 struct CacheArgs {

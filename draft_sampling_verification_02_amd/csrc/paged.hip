@@ -733,12 +733,6 @@ __global__ __launch_bounds__(256) void paged_join_kernel(PagedParams p) {
         store_row<T>(p.a.out, p.a.lse, (long long)(rq.row0 + qi / p.G) * p.a.n_heads + seg.z * p.G + qi % p.G, c4, D, o, m, l);
 }
 
-int log2_of(int x) {
-    int s = 0;
-    while ((1 << s) < x) ++s;
-    return s;
-}
-
 template <typename T, bool E4, int D, int NQ>
 hipError_t launch_paged_typed(const PagedParams &pp, const PagedPlan &plan, hipStream_t s) {
     const dim3 grid(plan.grid);
