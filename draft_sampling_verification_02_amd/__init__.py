@@ -758,7 +758,8 @@ def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_of
     cache (see dspark_kv_write, which must have written the rows' own keys and
     values).  max_rows: rows a request usually has at most (None: the average,
     rounded up); scale: None = D^-1/2.  Returns {"out"[, "lse"], "workspace"};
-    pass ``out`` (a previous result) to reuse its buffers."""
+    pass ``out`` (a previous result) to reuse its buffers.  A workspace that is
+    too small for the call is replaced by a new one, which the result holds."""
     if out is not None and stream is None and (not lse or "lse" in out):
         st = (_short or _load_marshal()).paged_attention(
             q, k_cache, v_cache, cache_len, page_table, row_offsets, k_scale, v_scale, scale, causal, max_rows,
@@ -801,7 +802,8 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
     rows row_offsets[b] .. row_offsets[b + 1] - 1 of q and kv_offsets[b] ..
     kv_offsets[b + 1] - 1 of k and v (None: the same rows).  Its query rows are
     the last positions of its keys.  scale: None = D^-1/2.  Returns {"out"[,
-    "lse"], "workspace"}; pass ``out`` (a previous result) to reuse its buffers."""
+    "lse"], "workspace"}; pass ``out`` (a previous result) to reuse its buffers,
+    and a workspace as for dspark_paged_attention."""
     if out is not None and stream is None and (not lse or "lse" in out):
         st = (_short or _load_marshal()).prompt_attention(
             q, k, v, row_offsets, kv_offsets, scale, causal, out["out"], out.get("lse"),

@@ -5,11 +5,11 @@
 // one head are one contiguous run, which is what the attention streams.  Row i
 // of request b stands at position pos = start_b + i, in page
 // page_table[b][pos / page_size], slot pos % page_size.  In an 8-bit cache the
-// D values of one (token, head) are x 2^-e rounded to e4m3 (to nearest, ties
-// to even: at most 2^-4 of the value, and nothing below 2^-9 2^e survives),
-// e the smallest integer >= -126 with max|x| <= 448 2^e.  A power of two
-// moves only exponents: the scaling is exact, so the value's own rounding is
-// the only one, and a scale is one byte (e + 127).
+// D values of one (token, head) are x 2^-e rounded to e4m3 (to nearest, ties to
+// even: off by at most 2^-4 of the value, or by 2^-10 2^e below 2^-6 2^e, where
+// the steps are 2^-9 2^e), e the smallest integer >= -126 with max|x| <= 448 2^e.
+// A power of two moves only exponents: the scaling is exact, so the value's own
+// rounding is the only one, and a scale is one byte (e + 127).
 //
 // Both kernels are bound by memory: every row is read once and written once.
 // A work item is 16 bytes of the 16-bit side (8 values); a workgroup takes a

@@ -7,8 +7,10 @@
 //   every token of the request otherwise),
 //   out = sum_t exp(s_t - lse) v_t,  lse = log sum_t exp(s_t).
 // One pass over the cache carries the running maximum and sum; everything is
-// accumulated in 32 bits, and the probabilities are rounded to 16 bits (2^-9
-// relative for bfloat16) only as they enter the V product.
+// accumulated in 32 bits, and the probabilities are rounded to 16 bits (by up to
+// 2^-8 of each for bfloat16, 2^-11 for float16) only as they enter the V product:
+// outputs are 2.0e-3 from the definition on average, 1.6e-3 of it their own
+// rounding (float16: 2.3e-4 and 2.0e-4).
 //
 // What bounds it: the cache is read once, 4 D bytes (2 D + 2 in 8 bits) a
 // token and head against 4 D G flops for G queries -- memory, for any group a
@@ -34,7 +36,7 @@
 // Measured (MI355X; 32 query and 8 key-value heads, D = 128, pages of 16):
 // 256 requests, one row, 16 to 8192 tokens, bfloat16: 726 us for 4.20 GB,
 // 5.8 TB/s (no LDS bank conflicts); the same with 1 to 6 rows and up to 4096
-// tokens 402 us for 2.05 GB, 5.1 TB/s; four requests of 60,000 to 131,000 tokens
+// tokens 406 us for 2.05 GB, 5.0 TB/s; four requests of 60,000 to 131,000 tokens
 // over 8 bits, 64 query heads: 119 us for 620 MB, 5.2 TB/s; one request of 500
 // tokens 10 us, of 8000 tokens 11 + 4 us, where the chain of dependent loads
 // (lengths, page, tile) is what there is to wait for: 7 us with a single token.
@@ -142,7 +144,8 @@ struct ProbType<T, true> {
 };
 // float16 rows over an 8-bit cache: bfloat16 would leave the probabilities
 // three bits short of the rows' own rounding, so a second bfloat16 carries the
-// rest of each (2^-16 in all) through a second product
+// rest of each (2^-16 in all) through a second product (the verify rows of 256
+// requests, up to 4096 tokens, D = 128: 268 us, 258 for bfloat16 rows)
 template <typename T, bool E4>
 constexpr bool kTwoTerms = E4 && std::is_same<T, TypeF16>::value;
 

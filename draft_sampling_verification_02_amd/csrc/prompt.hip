@@ -30,8 +30,8 @@
 // matrix units busy 64% of 1.72 GHz (a 16384-cubed library product reaches 1386
 // TFLOP/s, 73% of 1.71 GHz); 16 prompts of 100 to 4100 tokens 931-1040 us over
 // the boxes, 910 to 1018 TFLOP/s, the rest being starts, ends and diagonal
-// tiles.  16/4 heads at 8192 tokens: D = 64 164 us, 838 TFLOP/s; D = 256
-// 582-624 us, 880 to 945 TFLOP/s (one wave a SIMD: the accumulators take half
+// tiles.  16/4 heads at 8192 tokens: D = 64 163-170 us, 808 to
+// 843 TFLOP/s; D = 256 564-624 us, 880 to 975 TFLOP/s (one wave a SIMD: the accumulators take half
 // its registers).
 #include <algorithm>
 
@@ -643,7 +643,7 @@ hipError_t launch_prompt_dim(const PromptParams &p, hipStream_t s) {
 // adds a launch, 5 us, and writes and reads 64 KiB a part.  The cheapest cut is
 // taken; the average sequence stands for all, as lengths are on the device.
 // Measured, us a call in 1 / 2 / 3 / 4 / 8 / 16 parts, > < the rule's:
-//   18 rows behind 4000 keys, 8/1 heads, D = 128   39.7 /  26.1  / 21.2 /  18.8  / 14.6 / 13.8 (32 parts 14.6, > 24 <)
+//   18 rows behind 4000 keys, 8/1 heads, D = 128   39.7 /  26.1  / 21.2 /  18.8  / 14.6 / 13.8 (32 parts 14.6, > 24 <: 15.7 in another run)
 //   four times 64 rows behind 2000, 32/8 heads     32.8 /  25.4  / 24.0 / >23.7< / 27.1 / 36.7
 //   one prompt of 2048 rows, 8/8 heads             37.8 / >31.0< / 28.6 /  29.3  / 40.8 / 58.8
 //   of 4096                                        68.5 / >59.3< / 61.7 /  65.9
@@ -654,6 +654,9 @@ hipError_t launch_prompt_dim(const PromptParams &p, hipStream_t s) {
 //   of 4096, 8/1 heads, D = 256                     128 / > 109< /  121 /   136  /  201
 //   of 1024, 8/8 heads, D = 256                    39.3 /  32.0  />29.0</  27.1  / 40.4
 //   of 2048, 16/4 heads, D = 256                  >68.4</  72.5  / 86.9 /   106  /  166
+// The rule's choice is up to 14% off the best measured one where 18 rows are all
+// there is to do, and up to 8% elsewhere; and it cuts nothing where a batch of
+// short prompts holds a long one.
 PromptPlan prompt_plan(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads, int head_dim) {
     PromptPlan p{};
     p.slots = int((long long)n_rows * (n_heads / n_kv_heads) / kPromptQueries + B);

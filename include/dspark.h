@@ -476,11 +476,13 @@ size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv
  * or t < cache_len[b] + rows of b (causal = 0: the rows see each other, as in a
  * parallel draft stage).  The rows' own keys and values must be in the cache
  * (dspark_kv_write of the same rows, before this call on the stream).  A row
- * that sees no token gives zeros and lse = -inf.  Infinities and NaN in tokens
- * a row does not see, or in unused slots, do not reach it.  Scores, softmax
- * sums and products are kept in float32; probabilities enter the V product in
- * the rows' type (over 8-bit caches in bfloat16, for float16 rows in two
- * bfloat16 terms).
+ * that sees no token (or none with a score above -inf) gives zeros and lse =
+ * -inf.  Infinities and NaN in tokens a row does not see, or in unused slots, do
+ * not reach it; infinities of V that it sees make their channel infinite (NaN
+ * where both signs meet, or where the probability is below float32's range).
+ * Scores, softmax sums and products are kept in float32; probabilities enter the
+ * V product in the rows' type (over 8-bit caches in bfloat16, for float16 rows in
+ * two bfloat16 terms).
  *   q           device [n_rows, n_heads, head_dim] of `dtype`, row stride q_stride
  *   n_heads     a multiple of n_kv_heads, at most DSPARK_MAX_HEADS
  *   max_rows    >= 1: how many rows a request usually has at most (1 for
