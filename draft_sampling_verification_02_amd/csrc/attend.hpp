@@ -186,6 +186,11 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {
     if (((w >> 16) & 0x7fffu) >= T::kInf) w &= 0xffffu;
     return w;
 }
+// an infinity in the pair
+template <typename T>
+__device__ __forceinline__ bool has_infinity(uint32_t w) {
+    return (w & 0x7fffu) == T::kInf || ((w >> 16) & 0x7fffu) == T::kInf;
+}
 __device__ __forceinline__ uint32_t finite_e4m3(uint32_t w) {
 #pragma unroll
     for (int i = 0; i < 32; i += 8)

@@ -532,11 +532,22 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                     // that see it get their share of it here.  (The share's probability is taken anew in 32 bits: rounded
                     // to float16 it may be zero, and 0 * inf is NaN.  8-bit values that are not finite are NaN anyway.)
                     if (CAREFUL || (t + kTokens > lim_min && lim_min < rq.L)) {
-                        const P8 zero = {};
-                        f32x4_t z = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                        bool odd = false;
+                        if (CAREFUL && !masked) {  // NaN that all see need no care
+#pragma unroll 1
+                            for (int slot = lane; slot < kTokens * S::CPR; slot += 64) {
+                                const u32x4v_t w = lds_read<u32x4v_t>(vbuf + slot * 16);
 #pragma unroll
-                        for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbase, c), zero, z);
-                        if (__any(!(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f))) {
+                                for (int x = 0; x < 4; ++x) odd |= has_infinity<T>(w[x]);
+                            }
+                        } else {
+                            const P8 zero = {};
+                            f32x4_t z = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int c = 0; c < CB; ++c) z = mma16(v_frag(vbase, c), zero, z);
+                            odd = !(z[0] == 0.f && z[1] == 0.f && z[2] == 0.f && z[3] == 0.f);
+                        }
+                        if (__any(odd)) {
 #pragma unroll 1
                             for (int k = 0; k < kTokens; ++k) {
                                 // token k is element e of lane group (k / 4) % 4; the lane holds channels 16 c + 4 g ..

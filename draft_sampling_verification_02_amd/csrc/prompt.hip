@@ -466,14 +466,20 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             bool bad = false;
             if (CAREFUL || t + kKeys > gmin) {
                 uint32_t top = 0;
+                bool infinite = false;
 #pragma unroll
                 for (int i = 0; i < SH::LPT; ++i) {
                     const u32x4v_t w = lds_read<u32x4v_t>(vbuf + ((i * NW + wave) * 64 + lane) * 16);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) top = max_u16x2(top, w[q] & 0x7fff7fffu);
+                    for (int q = 0; q < 4; ++q) {
+                        top = max_u16x2(top, w[q] & 0x7fff7fffu);
+                        if constexpr (CAREFUL) infinite |= has_infinity<T>(w[q]);
+                    }
                 }
                 const uint32_t inf = T::kInf;
-                if (__any((top & 0xffffu) >= inf || (top >> 16) >= inf) && lane == 0) found_bad = j + 1;
+                bool odd = (top & 0xffffu) >= inf || (top >> 16) >= inf;
+                if (CAREFUL && t + kKeys <= gmin) odd = infinite;  // NaN that all see need no care
+                if (__any(odd) && lane == 0) found_bad = j + 1;
                 wg_barrier();
                 bad = found_bad == j + 1;
             }
