@@ -26,10 +26,10 @@
 // fill the chip, their keys are split and prompt_join merges the parts.
 //
 // Measured (MI355X, bfloat16, 32 query and 8 key-value heads, D = 128): one
-// prompt of 16384 tokens 1908-2008 us over the boxes, 1095 to 1153 TFLOP/s,
+// prompt of 16384 tokens 1895-2008 us over several cards, 1095 to 1161 TFLOP/s,
 // matrix units busy 64% of 1.72 GHz (a 16384-cubed library product reaches 1386
 // TFLOP/s, 73% of 1.71 GHz); 16 prompts of 100 to 4100 tokens 931-1040 us over
-// the boxes, 910 to 1018 TFLOP/s, the rest being starts, ends and diagonal
+// the cards, 910 to 1018 TFLOP/s, the rest being starts, ends and diagonal
 // tiles.  16/4 heads at 8192 tokens: D = 64 163-170 us, 808 to
 // 843 TFLOP/s; D = 256 564-624 us, 880 to 975 TFLOP/s (one wave a SIMD: the accumulators take half
 // its registers).
