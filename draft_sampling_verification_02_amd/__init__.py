@@ -24,7 +24,10 @@ __all__ = [
     "dspark_version", "dspark_status_string",
     "dspark_draft_workspace_size", "dspark_draft_sample",
     "dspark_verify_workspace_size", "dspark_verify", "dspark_verify_check",
-    "dspark_kv_write", "dspark_kv_read", "dspark_paged_attention_workspace_size", "dspark_paged_attention",
+    "dspark_logit_rules",
+    "dspark_kv_write", "dspark_kv_read", "dspark_rotary", "dspark_kv_append",
+    "dspark_paged_attention_workspace_size", "dspark_paged_attention",
+    "dspark_window_attention_workspace_size", "dspark_window_attention",
     "dspark_prompt_attention_workspace_size", "dspark_prompt_attention",
     "dspark_schedule", "dspark_debug_random_words", "dspark_debug_gumbel", "dspark_debug_bias_gemm",
     "dspark_profile_enable", "dspark_profile_collect", "dspark_profile_read", "dspark_profile_reset",
@@ -132,6 +135,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                     _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_int, _c_int, _c_int, _c_float, _c_int, _c_void_p, _c_void_p,
                                     _c_void_p, _c_size, _c_void_p], _c_int),
+        "dspark_rotary": ([_c_void_p, _c_void_p, _c_i64, _c_i64, _c_int, _c_void_p, _c_int, _c_void_p, _c_int,
+                           _c_int, _c_int, _c_int, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p, _c_int, _c_float,
+                           _c_void_p, _c_void_p, _c_i64, _c_i64, _c_void_p], _c_int),
+        "dspark_kv_append": ([_c_void_p, _c_void_p, _c_void_p, _c_i64, _c_i64, _c_i64, _c_int, _c_void_p, _c_int,
+                              _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_int, _c_int,
+                              _c_void_p, _c_void_p, _c_int, _c_float, _c_void_p, _c_i64, _c_void_p, _c_void_p,
+                              _c_void_p, _c_void_p, _c_int, _c_int, _c_int, _c_void_p], _c_int),
+        "dspark_window_attention_workspace_size": ([_c_int] * 4, _c_size),
+        "dspark_window_attention": ([_c_void_p, _c_i64, _c_int, _c_void_p, _c_int, _c_int, _c_void_p, _c_void_p,
+                                     _c_int, _c_int, _c_int, _c_int, _c_int, _c_void_p, _c_void_p, _c_void_p,
+                                     _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_void_p,
+                                     _c_void_p, _c_void_p, _c_size, _c_void_p], _c_int),
+        "dspark_logit_rules": ([_c_void_p, _c_i64, _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_void_p, _c_int,
+                                _c_void_p, _c_void_p, _c_void_p, _c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                _c_void_p, _c_void_p, _c_int, _c_void_p, _c_int, _c_i64, _c_void_p, _c_void_p,
+                                _c_i64, _c_void_p], _c_int),
         "dspark_prompt_attention_workspace_size": ([_c_int] * 6, _c_size),
         "dspark_prompt_attention": ([_c_void_p, _c_void_p, _c_void_p, _c_i64, _c_i64, _c_i64, _c_int, _c_void_p,
                                      _c_int, _c_void_p, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_int,
@@ -708,6 +727,114 @@ def dspark_kv_read(k_cache, v_cache, page_table, n_rows: int, *, row_offsets=Non
     return out
 
 
+def _turning(inv_freq, q_norm, k_norm, eps, dtype, D, device):
+    """Checks what a rotation takes beside its rows; returns (inv_freq, rotary_dim, q_norm, k_norm, norm dtype)."""
+    torch = _torch()
+    rot = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor):
+            raise TypeError("inv_freq: expected a torch tensor")
+        rot = 2 * inv_freq.numel()
+        _dense(inv_freq, "inv_freq", torch.float32, (rot // 2,), device)
+    kind = dtype  # of the weights: the rows' type, or float32 (both)
+    for n, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if w is None:
+            continue
+        if getattr(w, "dtype", None) == torch.float32 and (n == "q_norm" or q_norm is None):
+            kind = torch.float32
+        _dense(w, n, kind, (D,), device)
+    return _at(inv_freq), rot, _at(q_norm), _at(k_norm), DSPARK_F32 if kind == torch.float32 else _types()[kind]
+
+
+def dspark_rotary(q, k, inv_freq, *, row_offsets=None, first=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+                  neighbours: bool = False, out: dict | None = None, stream=None) -> dict:
+    """Norms (where q_norm, k_norm [D] are given, of the rows' type or float32) and
+    turns the heads of q [n, Hq, D] and k [n, Hkv, D] (bfloat16 or float16; slices
+    of a fused projection are fine; one may be None) by their positions: row i of
+    request b, rows row_offsets[b] .. row_offsets[b + 1] - 1 (None: one row a
+    request), stands at first[b] + i (None: 0).  inv_freq [rot / 2] float32 (None: no
+    rotation) turns the pairs (m, m + rot / 2), or (2 m, 2 m + 1) with neighbours, of
+    the first rot channels.  Returns {"q", "k"}; pass ``out`` to reuse its rows, or
+    {"q": q, "k": k} to turn them in place.  Rows of no request keep what ``out``
+    holds (zeros in a new result)."""
+    lib = load_library()
+    x = q if q is not None else k
+    if x is None:
+        raise TypeError("q/k: expected a torch tensor")
+    name = "q" if q is not None else "k"
+    dt = _row_dtype(x, name)
+    dev, (n, _, D) = x.device, x.shape if x.dim() == 3 else (0, 0, 0)
+    rows = {}
+    for name, t in (("q", q), ("k", k)):
+        if t is None:
+            rows[name] = (None, 0, 0)
+            continue
+        s = _rows(t, name, x.dtype, None, dev)
+        if t.shape[0] != n or t.shape[2] != D:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{n}, heads, {D}]")
+        rows[name] = (t.data_ptr(), s, t.shape[1])
+    if row_offsets is not None:
+        B = row_offsets.numel() - 1 if isinstance(row_offsets, _torch().Tensor) else 0
+        _dense(row_offsets, "row_offsets", _torch().int32, (B + 1,), dev)
+    else:
+        B = n
+    if first is not None:
+        _dense(first, "first", _torch().int32, (B,), dev)
+    freq, rot, wq, wk, wdt = _turning(inv_freq, q_norm, k_norm, eps, x.dtype, D, dev)
+    if out is None:
+        out = _new_outputs({m: (t.shape, t.dtype) for m, t in (("q", q), ("k", k)) if t is not None}, dev,
+                           row_offsets is None and first is None, stream)
+    to = {}
+    for name, t in (("q", q), ("k", k)):
+        if t is None:
+            to[name] = (None, 0)
+            continue
+        s = _rows(out[name], name, x.dtype, t.shape[1], dev)
+        if out[name].shape != t.shape:
+            raise ValueError(f"{name}: result of shape {tuple(out[name].shape)}, expected {tuple(t.shape)}")
+        to[name] = (out[name].data_ptr(), s)
+    _call_on(dev, stream, "dspark_rotary", lib.dspark_rotary, rows["q"][0], rows["k"][0], rows["q"][1], rows["k"][1], dt,
+             _at(row_offsets), n, _at(first), B, rows["q"][2], rows["k"][2], D, freq, rot, 1 if neighbours else 0, wq, wk,
+             wdt, eps, to["q"][0], to["k"][0], to["q"][1], to["k"][1])
+    return out
+
+
+def dspark_kv_append(q, k, v, inv_freq, k_cache, v_cache, cache_len, page_table, *, row_offsets=None, q_norm=None,
+                     k_norm=None, eps: float = 1e-6, neighbours: bool = False, k_scale=None, v_scale=None,
+                     out: dict | None = None, stream=None) -> dict:
+    """dspark_rotary and dspark_kv_write in one pass: the heads of q and k are normed
+    and turned at positions cache_len[b] + i, the queries (None: no queries) come
+    back as {"q"} (``out`` to reuse its rows, {"q": q} in place), keys and values go
+    into the paged cache.  Arguments as for those two."""
+    lib = load_library()
+    dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
+    dt = _row_dtype(k, "k")
+    ks, vs = _rows(k, "k", k.dtype, Hkv, dev), _rows(v, "v", k.dtype, Hkv, dev)
+    n = k.shape[0]
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError(f"k/v: shapes {tuple(k.shape)} and {tuple(v.shape)}, expected [rows, {Hkv}, {D}]")
+    B, max_pages = _requests(row_offsets, n, page_table, dev)
+    _dense(cache_len, "cache_len", page_table.dtype, (B,), dev)
+    freq, rot, wq, wk, wdt = _turning(inv_freq, q_norm, k_norm, eps, k.dtype, D, dev)
+    qs = os_ = Hq = 0
+    if out is None:
+        out = {}
+    if q is not None:
+        qs, Hq = _rows(q, "q", k.dtype, None, dev), q.shape[1]
+        if q.shape[0] != n or q.shape[2] != D:
+            raise ValueError(f"q: shape {tuple(q.shape)}, expected [{n}, heads, {D}]")
+        if "q" not in out:
+            out.update(_new_outputs({"q": (q.shape, q.dtype)}, dev, False, stream))
+        os_ = _rows(out["q"], "q", q.dtype, Hq, dev)
+        if out["q"].shape != q.shape:
+            raise ValueError(f"q: result of shape {tuple(out['q'].shape)}, expected {tuple(q.shape)}")
+    _call_on(dev, stream, "dspark_kv_append", lib.dspark_kv_append, _at(q), _at(k), _at(v), qs, ks, vs, dt,
+             _at(row_offsets), n, _at(cache_len), _at(page_table), B, max_pages, Hq, Hkv, D, freq, rot,
+             1 if neighbours else 0, wq, wk, wdt, eps, None if q is None else _at(out["q"]), os_, _at(k_cache),
+             _at(v_cache), _at(k_scale), _at(v_scale), cdt, n_pages, ps)
+    return out
+
+
 def _new_outputs(shapes, device, every_row, stream):
     """New buffers {name: (shape, dtype)}, made on the call's stream; rows that
     no request owns are zero."""
@@ -789,6 +916,47 @@ def dspark_paged_attention(q, k_cache, v_cache, cache_len, page_table, *, row_of
 
 
 @functools.lru_cache(maxsize=1024)
+def dspark_window_attention_workspace_size(max_rows: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return load_library().dspark_window_attention_workspace_size(max_rows, n_heads, n_kv_heads, head_dim)
+
+
+def dspark_window_attention(q, k_cache, v_cache, cache_len, page_table, window: int, *, sinks: int = 0,
+                            row_offsets=None, k_scale=None, v_scale=None, scale: float | None = None,
+                            lse: bool = False, max_rows: int | None = None, out: dict | None = None, workspace=None,
+                            stream=None) -> dict:
+    """dspark_paged_attention (causal) through a sliding window: the row at position
+    p sees the `window` newest tokens, itself among them, and the first `sinks`
+    tokens of its request.  Pages that no row of a request sees may be gone from
+    page_table.  Everything else as for dspark_paged_attention."""
+    lib = load_library()
+    dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
+    dt = _row_dtype(q, "q")
+    qs = _rows(q, "q", q.dtype, None, dev)
+    n, Hq, d = q.shape
+    if d != D:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, heads, {D}]")
+    B, max_pages = _requests(row_offsets, n, page_table, dev)
+    _dense(cache_len, "cache_len", page_table.dtype, (B,), dev)
+    out = _attention_outputs(q, lse, out, row_offsets is None, stream)
+    if max_rows is None:
+        max_rows = max(1, -(-n // max(B, 1)))
+    ws, ws_bytes = _attention_workspace(dspark_window_attention_workspace_size(max_rows, Hq, Hkv, D), dev, workspace,
+                                        out, stream)
+    _call_on(dev, stream, "dspark_window_attention", lib.dspark_window_attention, _at(q), qs, dt, _at(row_offsets), n,
+             max_rows, _at(cache_len), _at(page_table), B, max_pages, Hq, Hkv, D, _at(k_cache), _at(v_cache),
+             _at(k_scale), _at(v_scale), cdt, n_pages, ps, _whole(window, "window"), _whole(sinks, "sinks"),
+             D ** -0.5 if scale is None else scale, _at(out["out"]), _at(out.get("lse")), ws, ws_bytes)
+    return out
+
+
+def _whole(x, name):
+    """A number of tokens as the library takes it: no cache holds more than its largest int."""
+    if isinstance(x, bool) or not hasattr(x, "__index__"):
+        raise TypeError(f"{name}: expected a whole number")
+    return max(min(x.__index__(), 2 ** 31 - 1), -1)
+
+
+@functools.lru_cache(maxsize=1024)
 def dspark_prompt_attention_workspace_size(B: int, n_rows: int, n_kv_rows: int, n_heads: int, n_kv_heads: int,
                                            head_dim: int) -> int:
     return load_library().dspark_prompt_attention_workspace_size(B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim)
@@ -835,6 +1003,86 @@ def dspark_prompt_attention(q, k, v, row_offsets, *, kv_offsets=None, scale: flo
     _call_on(dev, stream, "dspark_prompt_attention", lib.dspark_prompt_attention, _at(q), _at(k), _at(v), qs, ks, vs,
              dt, _at(row_offsets), n, _at(kv_offsets), n_kv, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
              1 if causal else 0, _at(out["out"]), _at(out.get("lse")), ws, ws_bytes)
+    return out
+
+
+def dspark_logit_rules(logits, *, row_offsets=None, history=None, history_len=None, prompt_len=None, drafts=None,
+                       repetition=None, frequency=None, presence=None, bias_offsets=None, bias_ids=None,
+                       bias_values=None, masks=None, mask_index=None, out=None, stream=None):
+    """Penalties, biases and grammar masks on a round's target rows: logits [n, V]
+    (bfloat16, float16 or float32; padded rows are fine) in, the float32 rows
+    dspark_verify takes out (``out`` [n, V] if given; ``logits`` itself, in
+    float32, is changed in place).  Request b owns rows row_offsets[b] ..
+    row_offsets[b + 1] - 1 (None: one row a request).  history [B, max_history]
+    int32 holds its tokens, history_len [B] of them, the first prompt_len[b] (None:
+    0) the prompt's; row j also counts the first j of drafts [B, gamma].
+    repetition, frequency, presence [B] float32 (None: 1, 0, 0); bias_offsets [B +
+    1], bias_ids, bias_values: each request's biases; masks [n_masks, >= V / 32]
+    int32 bits of what is allowed and mask_index [n], each row's mask (outside the
+    table: none).  Rows of no request keep what ``out`` holds (zeros in a new result)."""
+    torch = _torch()
+    lib = load_library()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a torch tensor")
+    dt = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16, torch.float16: DSPARK_F16}.get(logits.dtype)
+    if dt is None:
+        raise TypeError("logits: expected a float32, bfloat16 or float16 tensor")
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+
+    def padded(t, name):
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: [rows, V], the entries of a row dense")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+    stride = padded(logits, "logits")
+    n, V = logits.shape
+    if row_offsets is not None:
+        B = row_offsets.numel() - 1 if isinstance(row_offsets, torch.Tensor) else 0
+        _dense(row_offsets, "row_offsets", i32, (B + 1,), dev)
+    else:
+        B = n
+    wide = {"history": 0, "drafts": 0}
+    for name, t in (("history", history), ("drafts", drafts)):
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != 2:
+                raise TypeError(f"{name}: expected a torch tensor [B, tokens]")
+            wide[name] = t.shape[1]
+            _dense(t, name, i32, (B, t.shape[1]), dev)
+    for name, t, kind, size in (("history_len", history_len, i32, B), ("prompt_len", prompt_len, i32, B),
+                                ("repetition", repetition, f32, B), ("frequency", frequency, f32, B),
+                                ("presence", presence, f32, B), ("bias_offsets", bias_offsets, i32, B + 1),
+                                ("mask_index", mask_index, i32, n)):
+        if t is not None:
+            _dense(t, name, kind, (size,), dev)
+    if history is not None and history_len is None:
+        raise ValueError("history_len: needed with history")
+    n_biases = 0
+    if bias_offsets is not None:
+        if not isinstance(bias_ids, torch.Tensor):
+            raise TypeError("bias_ids: expected a torch tensor")
+        n_biases = bias_ids.numel()
+        _dense(bias_ids, "bias_ids", i32, (n_biases,), dev)
+        _dense(bias_values, "bias_values", f32, (n_biases,), dev)
+    n_masks = mask_stride = 0
+    if masks is not None:
+        if mask_index is None:
+            raise ValueError("mask_index: needed with masks")
+        if not isinstance(masks, torch.Tensor) or masks.dim() != 2:
+            raise TypeError("masks: expected a torch tensor [n_masks, words]")
+        n_masks, mask_stride = masks.shape
+        _dense(masks, "masks", i32, (n_masks, mask_stride), dev)
+        if mask_stride < (V + 31) // 32:
+            raise ValueError(f"masks: {mask_stride} words a mask, {(V + 31) // 32} needed")
+    if out is None:
+        out = _new_outputs({"out": ((n, V), f32)}, dev, row_offsets is None, stream)["out"]
+    if not isinstance(out, torch.Tensor) or out.dtype != f32:
+        raise TypeError("out: expected a float32 tensor")
+    if out.device != dev or out.shape != logits.shape:
+        raise ValueError(f"out: {tuple(out.shape)} on {out.device}, expected {tuple(logits.shape)} on {dev}")
+    _call_on(dev, stream, "dspark_logit_rules", lib.dspark_logit_rules, _at(logits), stride, dt, _at(row_offsets), n, B, V,
+             _at(history), wide["history"], _at(history_len), _at(prompt_len), _at(drafts), wide["drafts"],
+             _at(repetition), _at(frequency), _at(presence), _at(bias_offsets), _at(bias_ids), _at(bias_values),
+             n_biases, _at(masks), n_masks, mask_stride, _at(mask_index), _at(out), padded(out, "out"))
     return out
 
 

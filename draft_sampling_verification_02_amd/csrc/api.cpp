@@ -651,6 +651,29 @@ bool prompt_launchable(int B, int n_rows, int n_heads, int n_kv_heads) {
     return int64_t(n_rows) * n_heads / 128 + (int64_t(B) + 1) * n_kv_heads < (1 << 24);
 }
 
+// Sizes and types of a rotation; v_heads: heads of values that are moved beside.
+int rotary_geometry(int dtype, int n_rows, int n_heads, int n_kv_heads, int v_heads, int head_dim, int rotary_dim,
+                    int norm_dtype, float eps) {
+    if (n_heads < 0 || n_heads > DSPARK_MAX_HEADS || n_kv_heads < 0 || n_kv_heads > DSPARK_MAX_HEADS || head_dim < 1 ||
+        rotary_dim < 0 || rotary_dim > head_dim || !(eps >= 0.f && eps <= 3.4e38f))
+        return DSPARK_ERR_ARG;
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F16 && dtype != DSPARK_F32 && dtype != DSPARK_E4M3) return DSPARK_ERR_ARG;
+    if ((dtype != DSPARK_BF16 && dtype != DSPARK_F16) || (norm_dtype != dtype && norm_dtype != DSPARK_F32) ||
+        !head_dim_supported(head_dim) || rotary_dim % 16 != 0)
+        return DSPARK_ERR_UNSUPPORTED;
+    // a launch holds fewer than 2^32 threads, 256 a workgroup
+    if (n_heads + n_kv_heads > 0 && rotary_plan(n_rows, n_heads + n_kv_heads + v_heads, head_dim).blocks >= (1 << 24))
+        return DSPARK_ERR_ARG;
+    return DSPARK_OK;
+}
+
+// Rows that are turned into rows: both there, or no heads at all.
+bool rotary_rows_ok(const void *in, const void *out, int64_t stride, int64_t out_stride, int heads, int head_dim) {
+    if (heads == 0) return true;
+    return in && out && aligned16(in) && aligned16(out) && row_stride_ok(stride, heads, head_dim) &&
+           row_stride_ok(out_stride, heads, head_dim) && (in != out || stride == out_stride);
+}
+
 // the kernels multiply by scale * log2(e), which has to be finite
 bool scale_ok(float scale) { return scale > 0.f && scale <= 2.3e38f; }
 
@@ -730,6 +753,104 @@ int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_sc
     return launch_cache(a, false, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
 }
 
+int dspark_rotary(const void *q, const void *k, int64_t q_stride, int64_t k_stride, int dtype,
+                  const int32_t *row_offsets, int n_rows, const int32_t *first, int B, int n_heads, int n_kv_heads,
+                  int head_dim, const float *inv_freq, int rotary_dim, int neighbours, const void *q_norm,
+                  const void *k_norm, int norm_dtype, float eps, void *q_out, void *k_out, int64_t q_out_stride,
+                  int64_t k_out_stride, void *stream) {
+    if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || (!row_offsets && n_rows != B))
+        return DSPARK_ERR_ARG;
+    int st = rotary_geometry(dtype, n_rows, n_heads, n_kv_heads, 0, head_dim, rotary_dim, norm_dtype, eps);
+    if (st != DSPARK_OK) return st;
+    if (n_heads + n_kv_heads < 1) return DSPARK_ERR_ARG;
+    if (n_rows == 0) return DSPARK_OK;
+    if ((!inv_freq && rotary_dim > 0) || !rotary_rows_ok(q, q_out, q_stride, q_out_stride, n_heads, head_dim) ||
+        !rotary_rows_ok(k, k_out, k_stride, k_out_stride, n_kv_heads, head_dim))
+        return DSPARK_ERR_ARG;
+    RotaryArgs a{};
+    a.c.k = k;
+    a.c.k_stride = k_stride;
+    a.c.k_out = k_out;
+    a.c.dtype = dtype;
+    a.c.row_offsets = row_offsets;
+    a.c.start = first;
+    a.c.B = B;
+    a.c.n_rows = n_rows;
+    a.c.n_kv_heads = n_kv_heads;
+    a.c.head_dim = head_dim;
+    a.q = q;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.n_heads = n_heads;
+    a.inv_freq = inv_freq;
+    a.rot = rotary_dim;
+    a.neighbours = neighbours != 0;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.norm_dtype = norm_dtype;
+    a.eps = eps;
+    const RotaryPlan plan = rotary_plan(n_rows, n_heads + n_kv_heads, head_dim);
+    return launch_rotary(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
+int dspark_kv_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, int dtype, const int32_t *row_offsets, int n_rows, const int32_t *cache_len,
+                     const int32_t *page_table, int B, int max_pages, int n_heads, int n_kv_heads, int head_dim,
+                     const float *inv_freq, int rotary_dim, int neighbours, const void *q_norm, const void *k_norm,
+                     int norm_dtype, float eps, void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+                     uint8_t *k_scale, uint8_t *v_scale, int cache_dtype, int n_pages, int page_size, void *stream) {
+    int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
+                            page_size);
+    if (st != DSPARK_OK) return st;
+    st = rotary_geometry(dtype, n_rows, n_heads, n_kv_heads, n_kv_heads, head_dim, rotary_dim, norm_dtype, eps);
+    if (st != DSPARK_OK) return st;
+    if (n_rows == 0) return DSPARK_OK;
+    if ((!inv_freq && rotary_dim > 0) || !rotary_rows_ok(q, q_out, q_stride, q_out_stride, n_heads, head_dim))
+        return DSPARK_ERR_ARG;
+    if (!k || !v || !cache_len || !page_table || !aligned16(k) || !aligned16(v)) return DSPARK_ERR_ARG;
+    if (!row_stride_ok(k_stride, n_kv_heads, head_dim) || !row_stride_ok(v_stride, n_kv_heads, head_dim))
+        return DSPARK_ERR_ARG;
+    st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
+    if (st != DSPARK_OK) return st;
+    RotaryArgs a{};
+    a.c.k = k;
+    a.c.v = v;
+    a.c.k_stride = k_stride;
+    a.c.v_stride = v_stride;
+    a.c.dtype = dtype;
+    a.c.row_offsets = row_offsets;
+    a.c.start = cache_len;
+    a.c.page_table = page_table;
+    a.c.B = B;
+    a.c.n_rows = n_rows;
+    a.c.max_pages = max_pages;
+    a.c.n_kv_heads = n_kv_heads;
+    a.c.head_dim = head_dim;
+    a.c.k_cache = k_cache;
+    a.c.v_cache = v_cache;
+    a.c.k_scale = k_scale;
+    a.c.v_scale = v_scale;
+    a.c.cache_dtype = cache_dtype;
+    a.c.n_pages = n_pages;
+    a.c.page_size = page_size;
+    a.q = q;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.n_heads = n_heads;
+    a.inv_freq = inv_freq;
+    a.rot = rotary_dim;
+    a.neighbours = neighbours != 0;
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.norm_dtype = norm_dtype;
+    a.eps = eps;
+    const RotaryPlan plan = rotary_plan(n_rows, n_heads + 2 * n_kv_heads, head_dim);
+    return launch_rotary(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
 size_t dspark_paged_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim) {
     if (max_rows < 1 || head_geometry(0, n_heads, n_kv_heads) != DSPARK_OK || !head_dim_supported(head_dim)) return 0;
     size_t bytes = 0;
@@ -795,6 +916,66 @@ int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int
     return launch_paged(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
 }
 
+size_t dspark_window_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim) {
+    return dspark_paged_attention_workspace_size(max_rows, n_heads, n_kv_heads, head_dim);
+}
+
+int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
+                            int max_rows, const int32_t *cache_len, const int32_t *page_table, int B, int max_pages,
+                            int n_heads, int n_kv_heads, int head_dim, const void *k_cache, const void *v_cache,
+                            const uint8_t *k_scale, const uint8_t *v_scale, int cache_dtype, int n_pages,
+                            int page_size, int window, int sinks, float scale, void *out, float *lse_out,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    int st = cache_geometry(dtype, row_offsets, n_rows, B, max_pages, n_kv_heads, head_dim, cache_dtype, n_pages,
+                            page_size);
+    if (st != DSPARK_OK) return st;
+    st = head_geometry(n_rows, n_heads, n_kv_heads);
+    if (st != DSPARK_OK) return st;
+    if (max_rows < 1 || !scale_ok(scale) || window < 1 || sinks < 0) return DSPARK_ERR_ARG;
+    if (n_rows == 0) return DSPARK_OK;
+    if (!q || !cache_len || !page_table || !out || !aligned16(q) || !aligned16(out)) return DSPARK_ERR_ARG;
+    if (!row_stride_ok(q_stride, n_heads, head_dim)) return DSPARK_ERR_ARG;
+    st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
+    if (st != DSPARK_OK) return st;
+    PagedArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.dtype = dtype;
+    a.row_offsets = row_offsets;
+    a.start = cache_len;
+    a.page_table = page_table;
+    a.B = B;
+    a.n_rows = n_rows;
+    a.max_pages = max_pages;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype;
+    a.n_pages = n_pages;
+    a.page_size = page_size;
+    a.scale = scale;
+    a.causal = 1;
+    // no request has more tokens than this
+    a.window = window < DSPARK_MAX_CACHE_TOKENS ? window : DSPARK_MAX_CACHE_TOKENS;
+    a.sinks = sinks < DSPARK_MAX_CACHE_TOKENS ? sinks : DSPARK_MAX_CACHE_TOKENS;
+    a.out = out;
+    a.lse = lse_out;
+    // what a request of the usual number of rows walks at most: sinks and windows in whole tiles
+    const long long table = (long long)max_pages * page_size, walked = (long long)a.window + a.sinks + max_rows + 64;
+    const PagedSizes z{n_rows, B, walked < table ? walked : table, max_rows, n_heads, n_kv_heads, head_dim,
+                       cache_dtype == DSPARK_E4M3};
+    const PagedPlan plan = paged_plan(z);
+    size_t need = 0;
+    paged_carve(nullptr, plan, head_dim, &need);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
+    const PagedWork w = paged_carve(workspace, plan, head_dim, nullptr);
+    return launch_window_rows(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
 size_t dspark_prompt_attention_workspace_size(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads,
                                               int head_dim) {
     if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || n_kv_rows < 0 ||
@@ -853,6 +1034,61 @@ int dspark_prompt_attention(const void *q, const void *k, const void *v, int64_t
     a.out = out;
     a.lse = lse_out;
     return launch_prompt(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+}
+
+// ---------------------------------------------------------------- rules on logits
+
+int dspark_logit_rules(const void *logits, int64_t stride, int dtype, const int32_t *row_offsets, int n_rows, int B,
+                       int V, const int32_t *history, int max_history, const int32_t *history_len,
+                       const int32_t *prompt_len, const int32_t *drafts, int gamma, const float *repetition,
+                       const float *frequency, const float *presence, const int32_t *bias_offsets,
+                       const int32_t *bias_ids, const float *bias_values, int n_biases, const int32_t *masks,
+                       int n_masks, int64_t mask_stride, const int32_t *mask_index, float *out, int64_t out_stride,
+                       void *stream) {
+    if (B < 1 || B > DSPARK_MAX_BATCH || n_rows < 0 || n_rows > DSPARK_MAX_ROWS || (!row_offsets && n_rows != B) ||
+        V < 1 || V > DSPARK_MAX_VOCAB || stride < V || stride > DSPARK_MAX_ROW_STRIDE || out_stride < V ||
+        out_stride > DSPARK_MAX_ROW_STRIDE)
+        return DSPARK_ERR_ARG;
+    if (int64_t(B) * ((V + 4095) / 4096) >= (1 << 23)) return DSPARK_ERR_ARG;  // a launch holds fewer than 2^32 threads
+    if (dtype != DSPARK_BF16 && dtype != DSPARK_F16 && dtype != DSPARK_F32 && dtype != DSPARK_E4M3) return DSPARK_ERR_ARG;
+    if (dtype == DSPARK_E4M3) return DSPARK_ERR_UNSUPPORTED;
+    if (history && (max_history < 0 || !history_len)) return DSPARK_ERR_ARG;
+    if (drafts && (gamma < 0 || gamma > DSPARK_MAX_GAMMA)) return DSPARK_ERR_ARG;
+    if (n_biases < 0 || (bias_offsets && n_biases > 0 && (!bias_ids || !bias_values))) return DSPARK_ERR_ARG;
+    if (masks && (n_masks < 0 || mask_stride < (V + 31) / 32 || mask_stride > DSPARK_MAX_ROW_STRIDE || !mask_index))
+        return DSPARK_ERR_ARG;
+    if (n_rows == 0) return DSPARK_OK;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(logits), to = reinterpret_cast<uintptr_t>(out);
+    if (!logits || !out || at % (dtype == DSPARK_F32 ? 4 : 2) != 0 || to % 4 != 0) return DSPARK_ERR_ARG;
+    if (at == to && (dtype != DSPARK_F32 || stride != out_stride)) return DSPARK_ERR_ARG;
+    RulesArgs a{};
+    a.logits = logits;
+    a.stride = stride;
+    a.dtype = dtype;
+    a.row_offsets = row_offsets;
+    a.n_rows = n_rows;
+    a.B = B;
+    a.V = V;
+    a.history = history;
+    a.history_len = history_len;
+    a.prompt_len = prompt_len;
+    a.max_history = max_history;
+    a.drafts = drafts;
+    a.gamma = gamma;
+    a.repetition = repetition;
+    a.frequency = frequency;
+    a.presence = presence;
+    a.bias_offsets = bias_offsets;
+    a.bias_ids = bias_ids;
+    a.bias_values = bias_values;
+    a.n_biases = n_biases;
+    a.masks = masks;
+    a.mask_index = masks ? mask_index : nullptr;
+    a.n_masks = n_masks;
+    a.mask_stride = mask_stride;
+    a.out = out;
+    a.out_stride = out_stride;
+    return launch_rules(a, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
 }
 
 }  // extern "C"

@@ -273,6 +273,28 @@ struct CacheArgs {
 };
 hipError_t launch_cache(const CacheArgs &a, bool write, hipStream_t s);
 
+// Rows of queries and keys, normed and turned by their positions.  With a cache
+// (c.k_cache) the keys and c.v go into its slots, else the keys to c.k_out.
+struct RotaryArgs {
+    CacheArgs c;
+    const void *q;
+    void *q_out;
+    long long q_stride, q_out_stride, k_out_stride;
+    int n_heads;
+    const float *inv_freq;  // [rot / 2]
+    int rot, neighbours;
+    const void *q_norm, *k_norm;  // [D] of norm_dtype (the rows' or float32), or nullptr
+    int norm_dtype;
+    float eps;
+};
+struct RotaryPlan {
+    long long items, blocks;
+    int per_row, per_block;
+    bool many;
+};
+RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim);
+hipError_t launch_rotary(const RotaryArgs &a, const RotaryPlan &p, hipStream_t s);
+
 // The split of a paged attention call.
 struct PagedPlan {
     int qblocks;   // 16-query blocks a workgroup holds
@@ -305,10 +327,14 @@ struct PagedArgs {
     int cache_dtype, n_pages, page_size;
     float scale;
     int causal;
+    int window, sinks;  // windowed calls only
     void *out;
     float *lse;
 };
 hipError_t launch_paged(const PagedArgs &a, const PagedPlan &p, const PagedWork &w, hipStream_t s);
+
+// The same behind a window (a.window, a.sinks), few rows a request.
+hipError_t launch_window_rows(const PagedArgs &a, const PagedPlan &p, const PagedWork &w, hipStream_t s);
 
 struct PromptArgs {
     const void *q, *k, *v;
@@ -333,6 +359,30 @@ struct PromptWork {
 };
 PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_kv_heads, int head_dim, size_t *bytes);
 hipError_t launch_prompt(const PromptArgs &a, const PromptPlan &p, const PromptWork &w, hipStream_t s);
+
+// ---- rules on logits -----------------------------------------------------
+
+struct RulesArgs {
+    const void *logits;
+    long long stride;  // elements from row to row
+    int dtype;
+    const int32_t *row_offsets;  // [B + 1], or nullptr: one row a request
+    int n_rows, B, V;
+    const int32_t *history, *history_len, *prompt_len;  // [B, max_history], [B], [B] or nullptr (0)
+    int max_history;
+    const int32_t *drafts;  // [B, gamma], or nullptr
+    int gamma;
+    const float *repetition, *frequency, *presence;  // [B], or nullptr (1, 0, 0)
+    const int32_t *bias_offsets, *bias_ids;          // [B + 1], [n_biases]
+    const float *bias_values;
+    int n_biases;
+    const int32_t *masks, *mask_index;  // [n_masks, mask_stride] bits, [n_rows]
+    int n_masks;
+    long long mask_stride;
+    float *out;
+    long long out_stride;
+};
+hipError_t launch_rules(const RulesArgs &a, hipStream_t s);
 
 // ---- diagnostics -----------------------------------------------------
 

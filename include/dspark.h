@@ -392,10 +392,58 @@ int dspark_acceptance_rnn(const float *target, int n_target_rows, const int32_t 
                           float *alpha_out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Rules on logits (in front of dspark_verify: what is drawn has to     */
+/* keep to them)                                                        */
+/* ------------------------------------------------------------------ */
+
+/* Penalties for repeated tokens, biases and grammar masks on the target rows of a
+ * round: logits of any float type in, the float32 rows dspark_verify takes out.
+ * Row j (from 0) of request b, token v:
+ *   z = logits[v]
+ *   v in the request's text (its prompt included), or among the drafts x_1 .. x_j
+ *     in front of the row:  z = z > 0 ? z / repetition[b] : z * repetition[b]
+ *   c > 0 times in the generated part of the text and those drafts:
+ *     z = z - (frequency[b] * c + presence[b])
+ *   z = z + the biases of v
+ *   z = -inf where the row's mask forbids v (whatever the logit, NaN included)
+ * in float32.
+ *   logits      device [n_rows, V] of `dtype` (DSPARK_BF16, DSPARK_F16 or
+ *               DSPARK_F32), row stride `stride` elements (>= V)
+ *   row_offsets device [B + 1] int32, as for the cache entry points (NULL: one row a
+ *               request, n_rows = B); rows of no request are not written
+ *   history     device [B, max_history] int32: the tokens of each request so far, the
+ *               anchor last; the first prompt_len[b] (NULL: 0) are the prompt's, those
+ *               up to history_len[b] are generated.  NULL: no text.
+ *   drafts      device [B, gamma] int32 or NULL: dspark_draft_sample's x
+ *   repetition, frequency, presence   device [B] float32, each may be NULL (1, 0, 0);
+ *               repetition > 0
+ *   bias_offsets, bias_ids, bias_values   device [B + 1] int32, [n_biases] int32 and
+ *               float32: request b owns entries bias_offsets[b] ..
+ *               bias_offsets[b + 1] - 1; a token that stands there twice gets the sum.
+ *               bias_offsets NULL: none
+ *   masks       device [n_masks, mask_stride] int32, mask_stride >= ceil(V / 32): token
+ *               v is allowed where bit v % 32 of word v / 32 is set.  NULL: none
+ *   mask_index  device [n_rows] int32: each row's mask; an index outside [0, n_masks)
+ *               stands for no mask
+ *   out         device [n_rows, V] float32, row stride out_stride (>= V): the logits
+ *               themselves (float32, same stride), or rows that do not overlap them
+ * Token ids outside [0, V) are passed over.  B * ceil(V / 4096) is below 2^23.
+ * Counts are whole numbers and biases are added in their order: outputs are a pure
+ * function of the inputs.  Lengths, offsets and indexes are read on the device, so
+ * a captured call follows them as they change. */
+int dspark_logit_rules(const void *logits, int64_t stride, int dtype, const int32_t *row_offsets, int n_rows, int B,
+                       int V, const int32_t *history, int max_history, const int32_t *history_len,
+                       const int32_t *prompt_len, const int32_t *drafts, int gamma, const float *repetition,
+                       const float *frequency, const float *presence, const int32_t *bias_offsets,
+                       const int32_t *bias_ids, const float *bias_values, int n_biases, const int32_t *masks,
+                       int n_masks, int64_t mask_stride, const int32_t *mask_index, float *out, int64_t out_stride,
+                       void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Paged key-value cache ([CE] 02: the target forward of a round)      */
 /* ------------------------------------------------------------------ */
 
-/* Conventions of the cache and attention entry points.
+/* Conventions of the cache, rotation and attention entry points.
  *
  * Packed rows.  A call works on n_rows rows of B requests; request b owns rows
  * row_offsets[b] .. row_offsets[b + 1] - 1 (device [B + 1] int32, non-decreasing;
@@ -434,8 +482,9 @@ int dspark_acceptance_rnn(const float *target, int n_target_rows, const int32_t 
  * DSPARK_BF16 or DSPARK_F16; a cache has the rows' type or DSPARK_E4M3
  * (otherwise DSPARK_ERR_UNSUPPORTED).  n_rows = 0 is valid and does nothing.
  * One launch takes all of a call: n_rows * n_heads is below 2^31, the K and V
- * of a write or read are below 256 GiB, and n_rows * n_heads / 128 + (B + 1) *
- * n_kv_heads of a prompt call is below 2^24 (otherwise DSPARK_ERR_ARG).  Calls
+ * of a write or read are below 256 GiB, the rows of a rotation or an append
+ * below 512 GiB, and n_rows * n_heads / 128 + (B + 1) * n_kv_heads of a prompt
+ * call is below 2^24 (otherwise DSPARK_ERR_ARG).  Calls
  * that may overlap in time, on two streams or in two captured graphs, need a
  * workspace each.
  * The device current at the call must be the one that holds the buffers and
@@ -460,6 +509,47 @@ int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_sc
                    int cache_dtype, int n_pages, int page_size, const int32_t *row_offsets, int n_rows,
                    const int32_t *first, const int32_t *page_table, int B, int max_pages, int n_kv_heads, int head_dim,
                    void *k_out, void *v_out, int dtype, void *stream);
+
+/* Heads normed and turned by their positions, on their way from the projections
+ * to the attention.  For each head x of a row at position p:
+ *   y = x, or with norm weights w:  y = x w / sqrt(mean(x^2) + eps),
+ *   (y_i, y_j) -> (y_i cos a - y_j sin a, y_j cos a + y_i sin a),  a = p inv_freq[m]
+ * for m < rotary_dim / 2 over the pairs (i, j) = (m, m + rotary_dim / 2), or the
+ * neighbours (2 m, 2 m + 1) where `neighbours` is not 0; channels from rotary_dim
+ * on keep y.  Row i of request b stands at position first[b] + i (first NULL = 0; a
+ * negative first[b] takes the request out: its rows are not written, nor are rows
+ * of no request).  Computed in float32, angles to 2^-53 of their size and 2^-21,
+ * and rounded once.
+ *   q, k        device rows of `dtype` (DSPARK_BF16 or DSPARK_F16), row strides
+ *               q_stride and k_stride; one of the two may be absent (NULL, 0 heads)
+ *   inv_freq    device [rotary_dim / 2] float32 (may be NULL where rotary_dim is 0)
+ *   rotary_dim  0 (no rotation) to head_dim, a multiple of 16
+ *   q_norm, k_norm   device [head_dim] of norm_dtype (`dtype` or DSPARK_F32), one or
+ *               both NULL: no norm
+ *   eps         >= 0, finite
+ *   q_out, k_out     device rows of `dtype`, row strides q_out_stride and
+ *               k_out_stride: q and k themselves (same strides), or rows that
+ *               overlap neither */
+int dspark_rotary(const void *q, const void *k, int64_t q_stride, int64_t k_stride, int dtype,
+                  const int32_t *row_offsets, int n_rows, const int32_t *first, int B, int n_heads, int n_kv_heads,
+                  int head_dim, const float *inv_freq, int rotary_dim, int neighbours, const void *q_norm,
+                  const void *k_norm, int norm_dtype, float eps, void *q_out, void *k_out, int64_t q_out_stride,
+                  int64_t k_out_stride, void *stream);
+
+/* dspark_rotary and dspark_kv_write in one: queries are normed, turned and written
+ * to q_out; keys are normed, turned and written into the cache at positions
+ * cache_len[b] + i, and values beside them as they are.  An 8-bit cache takes the
+ * keys straight from their float32 values, in the format of dspark_kv_write.
+ *   q           may be NULL with n_heads 0 (keys and values alone); otherwise as for
+ *               dspark_rotary.  The query rows of a request with a negative
+ *               cache_len are not written.
+ *   k, v, the cache, cache_len, page_table   as for dspark_kv_write */
+int dspark_kv_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, int dtype, const int32_t *row_offsets, int n_rows, const int32_t *cache_len,
+                     const int32_t *page_table, int B, int max_pages, int n_heads, int n_kv_heads, int head_dim,
+                     const float *inv_freq, int rotary_dim, int neighbours, const void *q_norm, const void *k_norm,
+                     int norm_dtype, float eps, void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+                     uint8_t *k_scale, uint8_t *v_scale, int cache_dtype, int n_pages, int page_size, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* Attention ([CE] 02: one causal forward over the block's positions)  */
@@ -501,6 +591,25 @@ int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int
                            const uint8_t *k_scale, const uint8_t *v_scale, int cache_dtype, int n_pages, int page_size,
                            float scale, int causal, void *out, float *lse_out, void *workspace, size_t workspace_bytes,
                            void *stream);
+
+/* Bytes of device workspace dspark_window_attention needs; 0 for invalid sizes. */
+size_t dspark_window_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim);
+
+/* dspark_paged_attention (causal) through a sliding window: the row at position
+ * p = cache_len[b] + i sees the tokens t <= p with p - t < window, and the first
+ * `sinks` tokens of its request (t <= p and t < sinks).  Any number of rows a
+ * request, from one (decoding) to chunks of a prompt of thousands.  Tokens that no
+ * row of a request sees are not read: their pages may be gone from page_table.
+ *   window      >= 1
+ *   sinks       >= 0
+ *   max_rows    >= 1: how many rows a request usually has at most; picks the kernel
+ *   everything else as for dspark_paged_attention */
+int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
+                            int max_rows, const int32_t *cache_len, const int32_t *page_table, int B, int max_pages,
+                            int n_heads, int n_kv_heads, int head_dim, const void *k_cache, const void *v_cache,
+                            const uint8_t *k_scale, const uint8_t *v_scale, int cache_dtype, int n_pages,
+                            int page_size, int window, int sinks, float scale, void *out, float *lse_out,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of device workspace dspark_prompt_attention needs; 0 for invalid sizes. */
 size_t dspark_prompt_attention_workspace_size(int B, int n_rows, int n_kv_rows, int n_heads, int n_kv_heads,

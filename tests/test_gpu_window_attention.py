@@ -1,0 +1,189 @@
+"""dspark_window_attention against its definition in 64 bits: windows and sinks of
+all sizes, one row to chunks, pages that are gone, values that must not reach a row."""
+import math
+
+import pytest
+import torch
+
+from attendkit import Paged, U, attend, check, offsets
+
+pytestmark = pytest.mark.gpu
+
+BF, FH, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+def _ds():
+    import draft_sampling_verification_02_amd as ds
+    ds.load_library()
+    return ds
+
+
+def _i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _sees(p, window, sinks):
+    return [t for t in range(p + 1) if t < sinks or p - t < window]
+
+
+def _probability(dtype, cache):
+    # what a probability is rounded to: float16 rows over an 8-bit cache carry it in two bfloat16 terms
+    return U[dtype] if cache != E4 else (U[BF] if dtype == BF else 2.0 ** -16)
+
+
+def _want(q, paged, rows, past, window, sinks, scale, lead, dtype, cache, width=None):
+    """(out, lse, tolerances); rows of no request, and of inactive ones, as the call leaves them."""
+    N, Hq, D = q.shape
+    out, lse = torch.zeros(N, Hq, D, dtype=torch.float64), torch.full((N, Hq), -math.inf, dtype=torch.float64)
+    tol, lse_tol = torch.zeros_like(out), torch.zeros_like(lse)
+    at = lead
+    for b, (r, p) in enumerate(zip(rows, past)):
+        for i in range(r):
+            if p < 0:
+                continue
+            t = [x for x in _sees(p + i, window, sinks) if width is None or x < width]
+            k, v = paged.tokens["k"][b][t], paged.tokens["v"][b][t]
+            # float16 probabilities are held at least 2^8 times as large (the least of the kernels' lifts, less a slack)
+            o, z, a, c = attend(q[at + i:at + i + 1].double(), k, v, [len(t)], scale, _probability(dtype, cache), U[dtype], lift=7)
+            out[at + i], lse[at + i], tol[at + i], lse_tol[at + i] = o[0], z[0], a[0], c[0]
+        at += r
+    return out, lse, tol, lse_tol
+
+
+def _run(dtype, cache, Hq, Hkv, D, page, rows, past, window, sinks, lead=0, tail=0, max_rows=None, gone=True, seed=0,
+         spoil=False):
+    ds = _ds()
+    print(f"window: {dtype} {cache} {Hq}/{Hkv} D={D} page={page} rows={rows} past={past} window={window} sinks={sinks} "
+          f"max_rows={max_rows}", flush=True)
+    g = torch.Generator().manual_seed(seed)
+    lens = [r + p if p >= 0 else 0 for r, p in zip(rows, past)]
+    paged = Paged(lens, Hkv, D, page, dtype, cache, seed + 1)
+    if gone:  # pages that no row of their request sees
+        for b, (r, p) in enumerate(zip(rows, past)):
+            for i in range(paged.width):
+                if p >= 0 and i * page >= sinks and (i + 1) * page <= p - window + 1:
+                    paged.table[b, i] = -1 if i % 2 else 1 << 30
+    if spoil:  # tokens that no row sees hold what is not finite
+        for b, (r, p) in enumerate(zip(rows, past)):
+            for t in range(sinks, max(p - window + 1, 0)):
+                pg = int(paged.table[b, t // page])
+                if 0 <= pg < paged.buf["k"].shape[0]:
+                    for n, x in (("k", math.inf), ("v", math.nan if t % 2 else -math.inf)):
+                        paged.buf[n][pg, :, t % page] = torch.full((), x).to(paged.buf[n].dtype)
+    n = lead + sum(rows) + tail
+    q = (torch.randn((n, Hq + 1, D), generator=g) * 1.5).to(dtype)
+    one_each = lead == tail == 0 and all(r == 1 for r in rows)
+    res = {"out": torch.full((n, Hq, D), 9.0, dtype=dtype, device="cuda"),
+           "lse": torch.full((n, Hq), 9.0, dtype=torch.float32, device="cuda")}
+    dev = paged.on("cuda")
+    scale = 0.8 * D ** -0.5
+    call = lambda res: ds.dspark_window_attention(
+        q.cuda()[:, :Hq], dev["k_cache"], dev["v_cache"], _i32(past), dev["page_table"], window, sinks=sinks,
+        row_offsets=None if one_each else offsets(rows, lead).cuda(), k_scale=dev.get("k_scale"),
+        v_scale=dev.get("v_scale"), scale=scale, lse=True, max_rows=max_rows, out=res)
+    r = call(res)
+    want, lse, tol, lse_tol = _want(q[:, :Hq], paged, rows, past, window, sinks, scale, lead, dtype, cache)
+    own = torch.zeros(n, dtype=torch.bool)
+    own[lead:lead + sum(rows)] = True
+    want[~own], lse[~own] = 9.0, 9.0
+    check("out", r["out"], want, tol)
+    check("lse", r["lse"], lse, lse_tol)
+    again = call({"out": torch.full_like(res["out"], 9.0), "lse": torch.full_like(res["lse"], 9.0)})
+    assert torch.equal(again["out"].view(torch.int16), r["out"].view(torch.int16)) and torch.equal(again["lse"], r["lse"])
+    return r
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4), (FH, E4)])
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 1, 64, 16), (6, 2, 128, 32), (8, 8, 128, 16), (4, 2, 256, 64)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 4), (64, 16), (100, 33), (1000, 5)])
+def test_decode_and_verify_rows(dtype, cache, Hq, Hkv, D, page, window, sinks):
+    _run(dtype, cache, Hq, Hkv, D, page, [1] * 7, [0, 3, 39, 40, 41, 130, 333], window, sinks)
+    _run(dtype, cache, Hq, Hkv, D, page, [3, 0, 6, 1, 5, 2], [200, 3, 0, -1, 97, -9], window, sinks, lead=1, tail=2)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4), (FH, E4)])
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(4, 1, 64, 16), (6, 2, 128, 32), (2, 2, 128, 16), (4, 2, 256, 64)])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (17, 0), (150, 20), (4000, 3)])
+def test_chunks_of_rows(dtype, cache, Hq, Hkv, D, page, window, sinks):
+    _run(dtype, cache, Hq, Hkv, D, page, [90, 1, 0, 200, 65], [310, 50, 7, 0, -1], window, sinks, lead=2, tail=1)
+    _run(dtype, cache, Hq, Hkv, D, page, [64, 33], [0, 129], window, sinks, max_rows=1)  # only a hint
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_texts_are_split_and_joined(dtype, cache, D):
+    _run(dtype, cache, 8, 2, D, 16, [1, 1], [5000, 2900], 2100, 70)
+    _run(dtype, cache, 8, 2, D, 64, [5, 2], [4000, 1900], 1500, 200, max_rows=5)
+    _run(dtype, cache, 4, 1, D, 16, [150], [3700], 2000, 40)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4)])
+@pytest.mark.parametrize("rows", [1, 4, 130])
+def test_what_no_row_sees_reaches_no_row(dtype, cache, rows):
+    for D in (64, 128, 256):
+        _run(dtype, cache, 4, 2, D, 16, [rows, rows], [333, 90], 50, 5, gone=False, spoil=True)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("rows,D", [(3, 128), (70, 64), (140, 128), (140, 256)])
+def test_infinities_reach_the_rows_that_see_them(dtype, rows, D):
+    # an infinity of V at tokens that some rows still see and later rows do not
+    ds = _ds()
+    Hq, Hkv, page, window, sinks, past = 4, 2, 16, 40, 3, 100
+    print(f"window: infinities {dtype} rows={rows} D={D}", flush=True)
+    paged = Paged([past + rows], Hkv, D, page, dtype, dtype, 5)
+    marks = [(past - 38, 0, 7, math.inf), (past + 1, 1, 0, -math.inf), (1, 0, 5, math.inf), (past + 2, 1, 9, math.nan)]
+    for t, h, c, x in marks:
+        paged.tokens["v"][0][t, h, c] = x
+        paged.buf["v"][int(paged.table[0, t // page]), h, t % page, c] = x
+    q = torch.randn((rows, Hq, D), generator=torch.Generator().manual_seed(1)).to(dtype)
+    dev = paged.on("cuda")
+    r = ds.dspark_window_attention(q.cuda(), dev["k_cache"], dev["v_cache"], _i32([past]), dev["page_table"], window,
+                                   sinks=sinks, row_offsets=_i32([0, rows]), max_rows=rows)["out"].cpu()
+    for i in range(rows):
+        sees = _sees(past + i, window, sinks)
+        for h in range(Hq):
+            for c in (0, 5, 7, 9, 11):
+                hit = [x for t, kh, cc, x in marks if cc == c and kh == h // (Hq // Hkv) and t in sees]
+                got = float(r[i, h, c])
+                if not hit:
+                    assert math.isfinite(got), (i, h, c)
+                else:
+                    assert got == hit[0] or (math.isnan(got) and math.isnan(hit[0])), (i, h, c, got)
+
+
+def test_a_window_of_everything_is_paged_attention():
+    ds = _ds()
+    for dtype, cache in ((BF, BF), (FH, FH), (BF, E4)):
+        rows, past = [4, 1, 7], [100, 600, 0]
+        paged = Paged([r + p for r, p in zip(rows, past)], 2, 128, 16, dtype, cache, 3)
+        dev, off = paged.on("cuda"), offsets(rows).cuda()
+        table = dev.pop("page_table")
+        q = torch.randn(sum(rows), 8, 128, device="cuda").to(dtype)
+        a = ds.dspark_paged_attention(q, dev["k_cache"], dev["v_cache"], _i32(past), table, row_offsets=off, lse=True,
+                                      max_rows=7, k_scale=dev.get("k_scale"), v_scale=dev.get("v_scale"))
+        for window, sinks in ((700, 0), (1, 700), (2 ** 31 - 1, 2 ** 31 - 1)):
+            b = ds.dspark_window_attention(q, dev["k_cache"], dev["v_cache"], _i32(past), table, window, sinks=sinks,
+                                           row_offsets=off, lse=True, max_rows=7, k_scale=dev.get("k_scale"),
+                                           v_scale=dev.get("v_scale"))
+            assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_rows_past_the_table_see_what_is_left():
+    # positions at and past the table's end: sinks, and window tokens that are in the table
+    ds = _ds()
+    D, page, width = 128, 16, 8
+    paged = Paged([128], 1, D, page, BF, BF, 9, width=width)
+    dev = paged.on("cuda")
+    q = torch.randn(3, 4, D).to(BF)
+    for past, window, sinks in ((126, 20, 4), (140, 20, 4), (500, 20, 4), (140, 20, 0), (1 << 30, 7, 3), (2 ** 31 - 1, 1 << 30, 5)):
+        r = ds.dspark_window_attention(q.cuda(), dev["k_cache"], dev["v_cache"], _i32([past]), dev["page_table"], window,
+                                       sinks=sinks, row_offsets=_i32([0, 3]), lse=True)
+        at = min(past, 1 << 30)  # tables end there
+        for i in range(3):
+            t = [x for x in range(width * page) if x < sinks or (x <= at + i and at + i - x < window)]
+            t = [x for x in t if x <= at + i]
+            out, lse, tol, lse_tol = attend(q[i:i + 1].double(), paged.tokens["k"][0][t], paged.tokens["v"][0][t], [len(t)],
+                                            D ** -0.5, U[BF], U[BF])
+            check("out", r["out"][i:i + 1], out, tol)
+            check("lse", r["lse"][i:i + 1], lse, lse_tol)

@@ -1,0 +1,193 @@
+"""Host-side checks of rotation, cache append, windowed attention and logit rules
+(no GPU needed): every refusal comes before anything is enqueued, and the binding
+names what is wrong with its tensors."""
+import ctypes
+
+import pytest
+import torch
+
+import draft_sampling_verification_02_amd as ds
+
+P = ctypes.c_void_p(0x10000)  # never dereferenced: validation fails first
+Q = ctypes.c_void_p(0x20000)
+ODD = ctypes.c_void_p(0x10008)  # not 16-byte aligned
+
+ARG, UNSUPPORTED, WORKSPACE = ds.DSPARK_ERR_ARG, ds.DSPARK_ERR_UNSUPPORTED, ds.DSPARK_ERR_WORKSPACE
+BF, I32 = torch.bfloat16, torch.int32
+
+
+def _rotary(**kw):
+    a = dict(q=P, k=P, qs=2048, ks=512, dtype=0, off=P, n=8, first=P, B=4, Hq=16, Hkv=4, D=128, freq=P, rot=128, nb=0,
+             qn=P, kn=P, ndt=0, eps=1e-6, qo=Q, ko=Q, qos=2048, kos=512)
+    a.update(kw)
+    return ds.load_library().dspark_rotary(
+        a["q"], a["k"], a["qs"], a["ks"], a["dtype"], a["off"], a["n"], a["first"], a["B"], a["Hq"], a["Hkv"], a["D"],
+        a["freq"], a["rot"], a["nb"], a["qn"], a["kn"], a["ndt"], a["eps"], a["qo"], a["ko"], a["qos"], a["kos"], None)
+
+
+def _append(**kw):
+    a = dict(q=P, k=P, v=P, qs=2048, ks=512, vs=512, dtype=0, off=P, n=8, len=P, table=P, B=4, max_pages=10, Hq=16, Hkv=4,
+             D=128, freq=P, rot=128, nb=0, qn=P, kn=P, ndt=0, eps=1e-6, qo=Q, qos=2048, kc=P, vc=P, ksc=None, vsc=None,
+             cdt=0, n_pages=50, ps=16)
+    a.update(kw)
+    return ds.load_library().dspark_kv_append(
+        a["q"], a["k"], a["v"], a["qs"], a["ks"], a["vs"], a["dtype"], a["off"], a["n"], a["len"], a["table"], a["B"],
+        a["max_pages"], a["Hq"], a["Hkv"], a["D"], a["freq"], a["rot"], a["nb"], a["qn"], a["kn"], a["ndt"], a["eps"],
+        a["qo"], a["qos"], a["kc"], a["vc"], a["ksc"], a["vsc"], a["cdt"], a["n_pages"], a["ps"], None)
+
+
+def _window(**kw):
+    a = dict(q=P, qs=2048, dtype=0, off=P, n=8, max_rows=2, len=P, table=P, B=4, max_pages=10, Hq=16, Hkv=4, D=128, kc=P,
+             vc=P, ksc=None, vsc=None, cdt=0, n_pages=50, ps=16, window=100, sinks=4, scale=0.1, out=P, lse=None, ws=P,
+             ws_bytes=1 << 40)
+    a.update(kw)
+    return ds.load_library().dspark_window_attention(
+        a["q"], a["qs"], a["dtype"], a["off"], a["n"], a["max_rows"], a["len"], a["table"], a["B"], a["max_pages"], a["Hq"],
+        a["Hkv"], a["D"], a["kc"], a["vc"], a["ksc"], a["vsc"], a["cdt"], a["n_pages"], a["ps"], a["window"], a["sinks"],
+        a["scale"], a["out"], a["lse"], a["ws"], a["ws_bytes"], None)
+
+
+def _rules(**kw):
+    a = dict(x=P, stride=1000, dtype=0, off=P, n=8, B=4, V=1000, hist=P, width=50, hlen=P, plen=P, drafts=P, gamma=5, rep=P,
+             freq=P, pres=P, boff=P, bid=P, bval=P, nb=10, masks=P, nm=3, words=32, index=P, out=Q, os=1000)
+    a.update(kw)
+    return ds.load_library().dspark_logit_rules(
+        a["x"], a["stride"], a["dtype"], a["off"], a["n"], a["B"], a["V"], a["hist"], a["width"], a["hlen"], a["plen"],
+        a["drafts"], a["gamma"], a["rep"], a["freq"], a["pres"], a["boff"], a["bid"], a["bval"], a["nb"], a["masks"],
+        a["nm"], a["words"], a["index"], a["out"], a["os"], None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(B=0), ARG), (dict(B=65537), ARG), (dict(n=-1), ARG), (dict(n=(1 << 24) + 1), ARG), (dict(off=None), ARG),
+    (dict(Hq=-1), ARG), (dict(Hq=1025), ARG), (dict(Hkv=1025), ARG), (dict(D=0), ARG), (dict(D=192), UNSUPPORTED),
+    (dict(rot=-16), ARG), (dict(rot=144), ARG), (dict(rot=24), UNSUPPORTED), (dict(eps=-1.0), ARG),
+    (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG), (dict(dtype=1), UNSUPPORTED), (dict(dtype=9), ARG),
+    (dict(ndt=2), UNSUPPORTED), (dict(freq=None), ARG), (dict(q=None), ARG), (dict(q=ODD), ARG), (dict(qo=None), ARG),
+    (dict(qo=ODD), ARG), (dict(qs=2040), ARG), (dict(qs=2052), ARG), (dict(qos=2040), ARG), (dict(qo=P, qos=2056), ARG),
+    (dict(qs=(1 << 24) + 8), ARG), (dict(k=None), ARG), (dict(ks=504), ARG)])
+def test_rotation_refusals(change, status):
+    assert _append(**change) == status
+    assert _rotary(**change) == status
+
+
+def test_refusals_of_one_of_the_two():
+    assert _rotary(ko=None) == ARG and _rotary(ko=ODD) == ARG and _rotary(kos=500) == ARG
+    assert _rotary(ko=P, kos=520) == ARG and _rotary(Hq=0, Hkv=0) == ARG
+    assert _append(Hkv=0) == ARG and _append(v=None) == ARG and _append(vs=516) == ARG and _append(len=None) == ARG
+    assert _append(table=None) == ARG and _append(kc=ODD) == ARG and _append(cdt=3) == ARG and _append(cdt=2) == UNSUPPORTED
+    assert _append(ps=48) == UNSUPPORTED and _append(max_pages=1 << 27) == ARG
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(B=0), ARG), (dict(n=-1), ARG), (dict(off=None), ARG), (dict(max_pages=0), ARG), (dict(n_pages=0), ARG),
+    (dict(Hkv=0), ARG), (dict(Hq=15), ARG), (dict(Hq=1028), ARG), (dict(D=96), UNSUPPORTED), (dict(dtype=1), UNSUPPORTED),
+    (dict(cdt=2), UNSUPPORTED), (dict(cdt=3), ARG), (dict(ps=8), UNSUPPORTED), (dict(window=0), ARG), (dict(window=-5), ARG),
+    (dict(sinks=-1), ARG), (dict(max_rows=0), ARG), (dict(scale=0.0), ARG), (dict(scale=2.4e38), ARG), (dict(q=None), ARG),
+    (dict(q=ODD), ARG), (dict(out=None), ARG), (dict(out=ODD), ARG), (dict(len=None), ARG), (dict(table=None), ARG),
+    (dict(kc=None), ARG), (dict(qs=2040), ARG), (dict(ws=None), WORKSPACE), (dict(ws_bytes=16), WORKSPACE),
+    (dict(ws=ODD), WORKSPACE)])
+def test_window_attention_refusals(change, status):
+    assert _window(**change) == status
+
+
+def test_window_workspaces():
+    for good in [(1, 16, 4, 128), (2000, 8, 8, 64), (5, 16, 1, 256)]:
+        assert ds.dspark_window_attention_workspace_size(*good) > 0
+    for bad in [(0, 16, 4, 128), (1, 15, 4, 128), (1, 16, 0, 128), (1, 16, 4, 100), (1, 2048, 4, 128)]:
+        assert ds.dspark_window_attention_workspace_size(*bad) == 0
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(B=0), ARG), (dict(n=-1), ARG), (dict(off=None), ARG), (dict(V=0), ARG), (dict(V=1 << 24, stride=1 << 24), ARG),
+    (dict(stride=999), ARG), (dict(os=999), ARG), (dict(stride=(1 << 24) + 1), ARG), (dict(dtype=3), UNSUPPORTED),
+    (dict(dtype=7), ARG), (dict(hlen=None), ARG), (dict(width=-1), ARG), (dict(gamma=-1), ARG), (dict(gamma=33), ARG),
+    (dict(nb=-1), ARG), (dict(bid=None), ARG), (dict(bval=None), ARG), (dict(nm=-1), ARG), (dict(words=31), ARG),
+    (dict(index=None), ARG), (dict(x=None), ARG), (dict(out=None), ARG), (dict(x=ctypes.c_void_p(0x10001)), ARG),
+    (dict(x=ctypes.c_void_p(0x10002), dtype=1), ARG), (dict(out=ctypes.c_void_p(0x10002)), ARG), (dict(out=P), ARG),
+    (dict(out=P, dtype=1, stride=1004), ARG),
+    (dict(B=65536, n=70000, V=600000, stride=600000, os=600000, words=20000), ARG)])
+def test_logit_rules_refusals(change, status):
+    assert _rules(**change) == status
+
+
+def test_no_rows_is_a_call_that_does_nothing():
+    for call in (_rotary, _append, _window, _rules):
+        assert call(n=0) == ds.DSPARK_OK
+
+
+# ---- the binding: CPU tensors stand for wrong ones; nothing reaches a device
+
+def _t(shape, dtype=BF):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def _good():
+    return dict(q=_t((4, 4, 64)), k=_t((4, 2, 64)), v=_t((4, 2, 64)), f=_t(32, torch.float32), kc=_t((6, 2, 16, 64)),
+                vc=_t((6, 2, 16, 64)), ln=_t(4, I32), pt=_t((4, 3), I32))
+
+
+def test_binding_refuses_host_tensors():
+    g = _good()
+    for call in (lambda: ds.dspark_rotary(g["q"], g["k"], g["f"], out={"q": g["q"], "k": g["k"]}),
+                 lambda: ds.dspark_kv_append(g["q"], g["k"], g["v"], g["f"], g["kc"], g["vc"], g["ln"], g["pt"], out={"q": g["q"]}),
+                 lambda: ds.dspark_window_attention(g["q"], g["kc"], g["vc"], g["ln"], g["pt"], 8),
+                 lambda: ds.dspark_logit_rules(_t((4, 100)))):
+        with pytest.raises(ValueError, match="HIP device"):
+            call()
+
+
+@pytest.mark.parametrize("kw,error,word", [
+    (dict(q=None, k=None), TypeError, "q/k"), (dict(q=_t((4, 4, 64), torch.float32)), TypeError, "q"),
+    (dict(k=_t((5, 2, 64))), ValueError, "k"), (dict(k=_t((4, 2, 64), torch.float16)), TypeError, "k"),
+    (dict(inv_freq=_t(32)), TypeError, "inv_freq"), (dict(inv_freq=3.0), TypeError, "inv_freq"),
+    (dict(q_norm=_t(32)), ValueError, "q_norm"), (dict(q_norm=_t(64), k_norm=_t(64, torch.float32)), TypeError, "k_norm"),
+    (dict(first=_t(5, I32)), ValueError, "first"), (dict(row_offsets=_t(3)), TypeError, "row_offsets"),
+    (dict(out={"q": _t((4, 4, 32)), "k": _t((4, 2, 64))}), ValueError, "q"),
+    (dict(q=_t((4, 64, 4)).transpose(1, 2)), ValueError, "dense")])
+def test_binding_names_what_is_wrong_with_a_rotation(kw, error, word):
+    g = _good()
+    a = dict(q=g["q"], k=g["k"], inv_freq=g["f"])
+    a.update(kw)
+    with pytest.raises(error, match=word):
+        ds.dspark_rotary(a.pop("q"), a.pop("k"), a.pop("inv_freq"), **a)
+
+
+@pytest.mark.parametrize("kw,error,word", [
+    (dict(q=_t((5, 4, 64))), ValueError, "q"), (dict(q=_t((4, 4, 32))), ValueError, "q"), (dict(v=_t((4, 1, 64))), ValueError, "v"),
+    (dict(k=_t((4, 2, 128)), v=_t((4, 2, 128))), ValueError, "k"), (dict(cache_len=_t(3, I32)), ValueError, "cache_len"),
+    (dict(page_table=_t((3, 3), I32)), ValueError, "row_offsets"), (dict(k_scale=_t((6, 2, 16), torch.uint8)), ValueError, "scale"),
+    (dict(k_norm=_t(65)), ValueError, "k_norm")])
+def test_binding_names_what_is_wrong_with_an_append(kw, error, word):
+    g = _good()
+    a = dict(q=g["q"], k=g["k"], v=g["v"], inv_freq=g["f"], k_cache=g["kc"], v_cache=g["vc"], cache_len=g["ln"],
+             page_table=g["pt"], out={"q": _t((4, 4, 64))})
+    a.update(kw)
+    with pytest.raises(error, match=word):
+        ds.dspark_kv_append(**a)
+
+
+@pytest.mark.parametrize("kw,error,word", [
+    (dict(q=_t((4, 4, 32))), ValueError, "q"), (dict(window=2.5), TypeError, "window"), (dict(sinks="4"), TypeError, "sinks"),
+    (dict(cache_len=_t(3, I32)), ValueError, "cache_len"), (dict(out={"out": _t((4, 4, 32))}), ValueError, "out"),
+    (dict(workspace=7), TypeError, "workspace")])
+def test_binding_names_what_is_wrong_with_a_windowed_call(kw, error, word):
+    g = _good()
+    a = dict(q=g["q"], k_cache=g["kc"], v_cache=g["vc"], cache_len=g["ln"], page_table=g["pt"], window=8)
+    a.update(kw)
+    with pytest.raises(error, match=word):
+        ds.dspark_window_attention(**a)
+
+
+@pytest.mark.parametrize("kw,error,word", [
+    (dict(logits=_t((4, 100), torch.float64)), TypeError, "logits"), (dict(logits=_t(100)), ValueError, "logits"),
+    (dict(logits=_t((100, 4)).t()), ValueError, "dense"), (dict(history=_t((4, 9), I32)), ValueError, "history_len"),
+    (dict(history=_t((3, 9), I32)), ValueError, "history"), (dict(drafts=_t((4, 5))), TypeError, "drafts"),
+    (dict(repetition=_t(3, torch.float32)), ValueError, "repetition"), (dict(bias_offsets=_t(5, I32)), TypeError, "bias_ids"),
+    (dict(bias_offsets=_t(5, I32), bias_ids=_t(6, I32), bias_values=_t(5, torch.float32)), ValueError, "bias_values"),
+    (dict(masks=_t((2, 4), I32)), ValueError, "mask_index"), (dict(masks=_t((2, 3), I32), mask_index=_t(4, I32)), ValueError, "masks"),
+    (dict(out=_t((4, 100))), TypeError, "out"), (dict(out=_t((4, 99), torch.float32)), ValueError, "out")])
+def test_binding_names_what_is_wrong_with_rules(kw, error, word):
+    a = dict(logits=_t((4, 100)))
+    a.update(kw)
+    with pytest.raises(error, match=word):
+        ds.dspark_logit_rules(a.pop("logits"), **a)
