@@ -23,7 +23,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")
 
 SOURCES = ["api.cpp", "schedule.cpp", "draft.hip", "verify.hip", "accept.hip", "rnn.hip", "sts.hip", "cache.hip", "paged.hip", "prompt.hip",
-           "window.hip", "rotary.hip", "rules.hip", "debug.hip"]
+           "window.hip", "window_rows.hip", "rotary.hip", "rules.hip", "debug.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Wshadow", "-Werror",
     "-Wno-unused-parameter", "-Wno-cuda-compat",

@@ -674,6 +674,12 @@ bool rotary_rows_ok(const void *in, const void *out, int64_t stride, int64_t out
            row_stride_ok(out_stride, heads, head_dim) && (in != out || stride == out_stride);
 }
 
+// Whether a windowed call goes by query blocks over 16-bit caches (prompt.hpp), or
+// row by row as paged attention does.
+bool window_in_chunks(int max_rows, int group, int head_dim, int cache_dtype) {
+    return cache_dtype != DSPARK_E4M3 && int64_t(max_rows) * group > (head_dim >= 256 ? 32 : 64);
+}
+
 // the kernels multiply by scale * log2(e), which has to be finite
 bool scale_ok(float scale) { return scale > 0.f && scale <= 2.3e38f; }
 
@@ -917,7 +923,14 @@ int dspark_paged_attention(const void *q, int64_t q_stride, int dtype, const int
 }
 
 size_t dspark_window_attention_workspace_size(int max_rows, int n_heads, int n_kv_heads, int head_dim) {
-    return dspark_paged_attention_workspace_size(max_rows, n_heads, n_kv_heads, head_dim);
+    const size_t rows = dspark_paged_attention_workspace_size(max_rows, n_heads, n_kv_heads, head_dim);
+    if (rows == 0) return 0;
+    size_t chunks = 0;
+    PromptPlan plan{};  // the most parts there are
+    plan.slots = kWindowParts / 2;
+    plan.nsplit = 2;
+    prompt_carve(nullptr, plan, 1, head_dim, &chunks);
+    return rows > chunks ? rows : chunks;
 }
 
 int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
@@ -937,6 +950,49 @@ int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const in
     if (!row_stride_ok(q_stride, n_heads, head_dim)) return DSPARK_ERR_ARG;
     st = cache_buffers(k_cache, v_cache, k_scale, v_scale, cache_dtype);
     if (st != DSPARK_OK) return st;
+    // no request has more tokens than these
+    window = window < DSPARK_MAX_CACHE_TOKENS ? window : DSPARK_MAX_CACHE_TOKENS;
+    sinks = sinks < DSPARK_MAX_CACHE_TOKENS ? sinks : DSPARK_MAX_CACHE_TOKENS;
+    // what a request of the usual number of rows walks at most: sinks and windows in whole tiles
+    const long long table = (long long)max_pages * page_size, walked = (long long)window + sinks + max_rows + 64;
+    size_t need = 0;
+    if (window_in_chunks(max_rows, n_heads / n_kv_heads, head_dim, cache_dtype) &&
+        prompt_launchable(B, n_rows, n_heads, n_kv_heads)) {
+        const PromptPlan plan = window_chunk_plan(B, n_rows, walked < table ? walked : table, n_heads, n_kv_heads, head_dim);
+        prompt_carve(nullptr, plan, n_kv_heads, head_dim, &need);
+        if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
+        const PromptWork w = prompt_carve(workspace, plan, n_kv_heads, head_dim, nullptr);
+        PromptArgs a{};
+        a.q = q;
+        a.k = k_cache;
+        a.v = v_cache;
+        a.q_stride = q_stride;
+        a.dtype = dtype;
+        a.q_offsets = row_offsets;
+        a.start = cache_len;
+        a.page_table = page_table;
+        a.B = B;
+        a.n_rows = n_rows;
+        a.max_pages = max_pages;
+        a.n_heads = n_heads;
+        a.n_kv_heads = n_kv_heads;
+        a.head_dim = head_dim;
+        a.n_pages = n_pages;
+        a.page_size = page_size;
+        a.scale = scale;
+        a.causal = 1;
+        a.window = window;
+        a.sinks = sinks;
+        a.out = out;
+        a.lse = lse_out;
+        return launch_window_chunks(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
+    }
+    const PagedSizes z{n_rows, B, walked < table ? walked : table, max_rows, n_heads, n_kv_heads, head_dim,
+                       cache_dtype == DSPARK_E4M3};
+    const PagedPlan plan = paged_plan(z);
+    paged_carve(nullptr, plan, head_dim, &need);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
+    const PagedWork w = paged_carve(workspace, plan, head_dim, nullptr);
     PagedArgs a{};
     a.q = q;
     a.q_stride = q_stride;
@@ -959,20 +1015,10 @@ int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const in
     a.page_size = page_size;
     a.scale = scale;
     a.causal = 1;
-    // no request has more tokens than this
-    a.window = window < DSPARK_MAX_CACHE_TOKENS ? window : DSPARK_MAX_CACHE_TOKENS;
-    a.sinks = sinks < DSPARK_MAX_CACHE_TOKENS ? sinks : DSPARK_MAX_CACHE_TOKENS;
+    a.window = window;
+    a.sinks = sinks;
     a.out = out;
     a.lse = lse_out;
-    // what a request of the usual number of rows walks at most: sinks and windows in whole tiles
-    const long long table = (long long)max_pages * page_size, walked = (long long)a.window + a.sinks + max_rows + 64;
-    const PagedSizes z{n_rows, B, walked < table ? walked : table, max_rows, n_heads, n_kv_heads, head_dim,
-                       cache_dtype == DSPARK_E4M3};
-    const PagedPlan plan = paged_plan(z);
-    size_t need = 0;
-    paged_carve(nullptr, plan, head_dim, &need);
-    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;
-    const PagedWork w = paged_carve(workspace, plan, head_dim, nullptr);
     return launch_window_rows(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
 }
 

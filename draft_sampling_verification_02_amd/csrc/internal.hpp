@@ -344,6 +344,9 @@ struct PromptArgs {
     int B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim;
     float scale;
     int causal;
+    // windowed calls: k and v are the pages of a cache
+    const int32_t *start, *page_table;
+    int max_pages, n_pages, page_size, window, sinks;
     void *out;
     float *lse;
 };
@@ -359,6 +362,10 @@ struct PromptWork {
 };
 PromptWork prompt_carve(void *ws, const PromptPlan &p, int n_kv_heads, int head_dim, size_t *bytes);
 hipError_t launch_prompt(const PromptArgs &a, const PromptPlan &p, const PromptWork &w, hipStream_t s);
+// Chunks of rows over a paged cache, behind a window; kv_tokens: what a request walks at most.
+constexpr int kWindowParts = 512;
+PromptPlan window_chunk_plan(int B, int n_rows, long long kv_tokens, int n_heads, int n_kv_heads, int head_dim);
+hipError_t launch_window_chunks(const PromptArgs &a, const PromptPlan &p, const PromptWork &w, hipStream_t s);
 
 // ---- rules on logits -----------------------------------------------------
 

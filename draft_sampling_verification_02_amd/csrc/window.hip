@@ -4,15 +4,41 @@
 // For row i of request b (position p = start_b + i) and head h:
 //   s_t = scale q . k_t over t <= p with p - t < window or t < sinks,
 //   out = sum_t exp(s_t - lse) v_t,  lse = log sum_t exp(s_t).
-// Few rows a request go through the kernel of paged attention (paged.hpp), whose
-// walk leaves out the tokens between the sinks and the first row's window: what
-// no row sees is not read, and its pages may be gone.
-#include "paged.hpp"
+// What no row sees is not read, and its pages may be gone.
+//
+// Few rows a request (decoding, verification) go through the kernel of paged
+// attention (paged.hpp, window_rows.hip): bound by memory; its walk leaves out the tokens between the
+// sinks and the first row's window.  Chunks of rows go through the kernel of prompt
+// attention (prompt.hpp): bound by the matrix units; each block of 128 queries
+// walks the sinks and its own window, the tiles that all its queries see whole in
+// the pipelined loop, and those where windows begin or end beside it; keys and
+// values come out of their pages by scalar loads of the page ids, one tile ahead.
+#include "prompt.hpp"
 
 namespace dspark {
 
-hipError_t launch_window_rows(const PagedArgs &a, const PagedPlan &plan, const PagedWork &w, hipStream_t s) {
-    return launch_paged_any<true>(a, plan, w, s);
+// As prompt_plan, with kv_tokens walked by every block.  No more than kWindowParts
+// parts are written, so that a workspace of one size does for all batches.
+PromptPlan window_chunk_plan(int B, int n_rows, long long kv_tokens, int n_heads, int n_kv_heads, int head_dim) {
+    PromptPlan p{};
+    p.slots = int((long long)n_rows * (n_heads / n_kv_heads) / kPromptQueries + B);
+    p.nsplit = 1;
+    const double units = (p.slots - 0.5 * B) * n_kv_heads;
+    const double tiles = double(kv_tokens) / kKeys, wide = head_dim / 128.0;
+    double best = 1e30;
+    for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+        if (s > 1 && (tiles < s * kMinTiles || (long long)p.slots * n_kv_heads * s > kWindowParts)) break;
+        const double cost = (0.4 + 0.8 * wide) * tiles / s * std::max(1.0, units * s / 512) + (s > 1 ? 5 + 0.033 * wide * units * s : 0.0);
+        if (cost < best) {
+            best = cost;
+            p.nsplit = s;
+        }
+    }
+    return p;
+}
+
+hipError_t launch_window_chunks(const PromptArgs &a, const PromptPlan &plan, const PromptWork &w, hipStream_t s) {
+    return launch_prompt_any<true>(a, plan, w, s);
 }
 
 }  // namespace dspark
