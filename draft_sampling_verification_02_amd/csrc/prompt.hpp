@@ -252,63 +252,78 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
             }
         }
     };
-    // Windowed calls: a tile's four runs of 16 tokens lie in a page each, whose ids are scalar loads; K of a tile is
-    // issued one tile before its V, so ids are read one tile ahead of K and kept for V.  A run without a page is
-    // filled with zeros (and its scores hidden).
+    // Windowed calls: a tile's four runs of 16 tokens lie in a page each, whose ids are scalar loads, read one tile ahead
+    // of K's issue; the rows of the cache that they make serve K and, a tile later, V.  A run without a page reads page
+    // 0, and its tokens are hidden.
     const TableInts table = WIN ? (TableInts)(a.page_table + (long long)request * a.max_pages) : (TableInts) nullptr;
-    struct Pages {
-        int id[4];
+    struct Runs {
+        uint32_t at[4];  // (all rows of a cache in memory fit 32 bits: a row has 128 bytes at least)
     };
-    Pages pk{}, pv{};  // of the tiles that K and V are issued for next
-    auto page_of = [&](int t) __device__ __attribute__((always_inline)) { return table[min(t >> p.pshift, a.max_pages - 1)]; };
-    auto fetch = [&](int j) __device__ __attribute__((always_inline)) {
-        const int t = tok(j);
-        Pages g;
+    Runs ids{}, rows_v{};  // page ids of the tile that K is issued for next (from token `ahead`), rows of V's
+    int ahead = 0;
+    auto fetch = [&](int t) __device__ __attribute__((always_inline)) {
+        Runs g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) g.id[i] = page_of(t + 16 * i);
+        for (int i = 0; i < 4; ++i) g.at[i] = uint32_t(table[min((t + 16 * i) >> p.pshift, a.max_pages - 1)]);
         return g;
     };
-    auto no_page = [&](int id) __device__ __attribute__((always_inline)) { return id < 0 || id >= a.n_pages; };
-    auto issue_paged = [&](const void *src, const uint32_t *off, uint32_t dst, int t, const Pages &g) __device__ __attribute__((always_inline)) {
+    auto no_page = [&](uint32_t id) __device__ __attribute__((always_inline)) { return id >= uint32_t(a.n_pages); };
+    auto rows_of = [&](const Runs &g, int t) __device__ __attribute__((always_inline)) {
+        Runs r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t id = no_page(g.at[i]) ? 0u : g.at[i];
+            r.at[i] = ((id * uint32_t(a.n_kv_heads) + uint32_t(kvh)) << p.pshift) + uint32_t((t + 16 * i) & ((1 << p.pshift) - 1));
+        }
+        return r;
+    };
+    constexpr int RPW = 64 / S::CPR;  // rows a wave's load covers
+    const uint32_t in_run = uint32_t(wave * RPW % 16 * S::RB);
+    auto issue_paged = [&](const void *src, const uint32_t *off, uint32_t dst, const Runs &r) __device__ __attribute__((always_inline)) {
+        const uint8_t *from = static_cast<const uint8_t *>(src) + in_run;
 #pragma unroll
         for (int j = 0; j < SH::LPT; ++j) {
-            const int row = j * RPL + wave * (64 / S::CPR);  // the wave's first row of this load
-            int id = g.id[j * RPL / 16 % 4];                 // (rows j RPL .. + RPL - 1 are in one run, or two)
-            if constexpr (RPL >= 32) id = row % 32 >= 16 ? g.id[(j * RPL / 16 + 1) % 4] : id;
-            if (no_page(id)) {
-                lds_write(dst + (j * NW + wave) * 1024 + lane * 16, u32x4v_t{0, 0, 0, 0});
-            } else {
-                const long long at = (((long long)id * a.n_kv_heads + kvh) << p.pshift) + ((t + row) & ((1 << p.pshift) - 1));
-                dma16(uniform(dst + (j * NW + wave) * 1024), off[j % OFFS], uniform(static_cast<const uint8_t *>(src) + at * S::RB));
-            }
+            // (the workgroup's rows j RPL .. + RPL - 1 are in one run, or two at D = 64)
+            uint32_t at = r.at[j * RPL / 16 % 4];
+            if constexpr (RPL >= 32) at = wave * RPW >= 16 ? r.at[(j * RPL / 16 + 1) % 4] : at;
+            dma16(uniform(dst + (j * NW + wave) * 1024), off[j % OFFS], uniform(from + uint64_t(at) * S::RB + j * RPL % 16 * S::RB));
         }
     };
     auto issue_k = [&](int j) __device__ __attribute__((always_inline)) {
-        if constexpr (WIN)
-            issue_paged(a.k, koff, lds0 + (j & 1) * S::BYTES, tok(j), pk);
-        else
-            issue(a.k, a.k_stride, kst, koff, lds0 + (j & 1) * S::BYTES, j * kKeys);
+        if constexpr (!WIN) issue(a.k, a.k_stride, kst, koff, lds0 + (j & 1) * S::BYTES, j * kKeys);
     };
     auto issue_v = [&](int j) __device__ __attribute__((always_inline)) {
-        if constexpr (WIN)
-            issue_paged(a.v, voff, lds0 + (2 + (j & 1)) * S::BYTES, tok(j), pv);
-        else
-            issue(a.v, a.v_stride, vst, voff, lds0 + (2 + (j & 1)) * S::BYTES, j * kKeys);
+        if constexpr (!WIN) issue(a.v, a.v_stride, vst, voff, lds0 + (2 + (j & 1)) * S::BYTES, j * kKeys);
     };
-    // the first K and V tiles
-    auto issue_first = [&]() __device__ __attribute__((always_inline)) {
-        if constexpr (WIN) pk = pv = fetch(0);
-        issue_k(0);
-        issue_v(0);
-    };
-    auto issue_second_k = [&]() __device__ __attribute__((always_inline)) {
-        if (ntile > 1) {
-            if constexpr (WIN) pk = pv = fetch(1);
-            issue_k(1);
+    // K of tile jk (windowed: that `ids` are of; they move on) and V of tile jv, those there are
+    auto issue_next = [&](int jk, int jv) __device__ __attribute__((always_inline)) {
+        if constexpr (WIN) {
+            const Runs rows_k = rows_of(ids, ahead);
+            if (jk < ntile) issue_paged(a.k, koff, lds0 + (jk & 1) * S::BYTES, rows_k);
+            if (jv < ntile) issue_paged(a.v, voff, lds0 + (2 + (jv & 1)) * S::BYTES, rows_v);
+            rows_v = rows_k;
+            if (jk + 1 < ntile) {
+                ahead = tok(jk + 1);
+                ids = fetch(ahead);
+            }
+        } else {
+            if (jk < ntile) issue_k(jk);
+            if (jv < ntile) issue_v(jv);
         }
-        if constexpr (WIN)
-            if (ntile > 2) pk = fetch(2);
     };
+    // K and V of the first tile (there is one), K of the second
+    auto issue_first = [&]() __device__ __attribute__((always_inline)) {
+        if constexpr (WIN) {
+            ahead = tok(0);
+            ids = fetch(ahead);
+            issue_next(0, ntile);
+            issue_paged(a.v, voff, lds0 + 2 * S::BYTES, rows_v);
+        } else {
+            issue_k(0);
+            issue_v(0);
+        }
+    };
+    auto issue_second_k = [&]() __device__ __attribute__((always_inline)) { issue_next(1, ntile); };
 
     // ---- read addresses ----------------------------------------------------
     // K fragment (32 tokens from row r0, step k): chunk 2 k + h of row r0 + n;
@@ -349,8 +364,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     if constexpr (WIN) {
         for (int i = tid; i < 4 * ntile; i += SH::NT) {
             const int t = tok(i >> 2) + 16 * (i & 3);
-            const int id = a.page_table[(long long)request * a.max_pages + min(t >> p.pshift, a.max_pages - 1)];
-            gone |= t < L && no_page(id);
+            gone |= t < L && no_page(uint32_t(a.page_table[(long long)request * a.max_pages + min(t >> p.pshift, a.max_pages - 1)]));
         }
     }
 
@@ -375,7 +389,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         issue_first();
         if constexpr (WIN)
             if (__any(gone) && lane == 0) found_gone = 1;
-        vm_wait<WIN ? 0 : SH::LPT>();  // (a run without a page takes no load: no count to wait by)
+        vm_wait<SH::LPT>();
 #pragma unroll
         for (int k = 0; k < KS; ++k) qf[k] = lds_read<V8>(qlds + (kread ^ (32 * k)));
         wg_barrier();  // K of tile 0 is in, every wave has its queries
@@ -401,15 +415,19 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) x[tb] = mma32(k_frag(kb, 32 * tb, k), qf[k], x[tb]);
     };
+    auto pageless = [&](int t) __device__ __attribute__((always_inline)) {  // a bit a run of the tile at token t without a page
+        int bits = 0;
+        if (any_gone) {
+            const Runs g = fetch(t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bits |= int(no_page(g.at[i])) << i;
+        }
+        return bits;
+    };
     auto hide = [&](int j, f32x16_t *x) __device__ __attribute__((always_inline)) {
         const int t = tok(j);
-        int without = 0;  // a bit a run of 16 tokens without a page
+        const int without = WIN ? pageless(t) : 0;
         if constexpr (WIN) {
-            if (any_gone) {
-                const Pages g = fetch(j);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) without |= int(no_page(g.id[i])) << i;
-            }
             if (t + kKeys <= wmin && (t >= wlow_max || t + kKeys <= a.sinks) && without == 0) return;
         } else {
             if (t + kKeys <= wmin) return;
@@ -465,12 +483,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     auto turn = [&](int j) __device__ __attribute__((always_inline)) {
         vm_wait<0>();
         wg_barrier();
-        if (j + 2 < ntile) issue_k(j + 2);
-        if (j + 1 < ntile) issue_v(j + 1);
-        if constexpr (WIN) {
-            pv = pk;
-            if (j + 3 < ntile) pk = fetch(j + 3);
-        }
+        issue_next(j + 2, j + 1);
     };
     // What is not finite in a tile of V: the queries that see it get their share
     // of it here, and then it leaves the tile.  The share's probability is taken
@@ -478,6 +491,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     // is called twice and holds the sums has to be inlined, or they go to memory.)
     auto give_bad_shares = [&](int t, uint32_t vbuf) __device__ __attribute__((always_inline)) {
         const float ms = reference();
+        const int without = WIN ? pageless(t) : 0;
 #pragma unroll 1
         for (int k = 0; k < kKeys; ++k) {
             // token k is s[k / 32][4 ((k / 8) % 4) + k % 4] of lane half (k / 4) % 2;
@@ -487,7 +501,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
 #pragma unroll
             for (int e = 0; e < 32; ++e) score = e == at ? s[e >> 4][e & 15] : score;
             const float pk = __shfl(fast_exp2(__builtin_fmaf(score, cs, -ms)), n + 32 * ((k >> 2) & 1));
-            const bool sees = !hidden(t + k);
+            const bool sees = WIN ? bool(int(!hidden(t + k)) & ~(without >> (k >> 4)) & 1) : !hidden(t + k);
 #pragma unroll
             for (int c = 0; c < CB; ++c)
 #pragma unroll
@@ -687,7 +701,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         wg_barrier();  // and every wave is done with the tiles
         if (found_nan) {
             issue_first();
-            vm_wait<WIN ? 0 : SH::LPT>();
+            vm_wait<SH::LPT>();
             wg_barrier();
             issue_second_k();
             begin();
