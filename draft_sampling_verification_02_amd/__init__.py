@@ -6,9 +6,9 @@ kernels (or, for the scheduler, its host C++).  Device arrays are torch
 tensors on the current HIP device, passed by pointer together with torch's
 current stream; host arrays (scheduler) are numpy arrays.  The functions
 carry the C entry points' names.  A missing or unloadable library raises
-immediately: there is no fallback path.  The cache and attention functions
-marshal through a compiled module (csrc/marshal.cpp) where they can, the others
-through ctypes.
+immediately: there is no fallback path.  The cache, rotation, attention and
+logit functions marshal through a compiled module (csrc/marshal.cpp) where they
+can, the others through ctypes.
 """
 from __future__ import annotations
 
@@ -567,7 +567,8 @@ def _load_marshal():
         raise RuntimeError(f"marshalling module not built at {MARSHAL_PATH}; run __graft_entry__.build()")
     module = importlib.import_module(__name__ + "._marshal")
     names = ("dspark_kv_write", "dspark_kv_read", "dspark_paged_attention_workspace_size", "dspark_paged_attention",
-             "dspark_prompt_attention_workspace_size", "dspark_prompt_attention")
+             "dspark_prompt_attention_workspace_size", "dspark_prompt_attention", "dspark_rotary", "dspark_kv_append",
+             "dspark_window_attention_workspace_size", "dspark_window_attention", "dspark_logit_rules")
     module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
                 torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
     _short = module
@@ -757,6 +758,12 @@ def dspark_rotary(q, k, inv_freq, *, row_offsets=None, first=None, q_norm=None, 
     the first rot channels.  Returns {"q", "k"}; pass ``out`` to reuse its rows, or
     {"q": q, "k": k} to turn them in place.  Rows of no request keep what ``out``
     holds (zeros in a new result)."""
+    if out is not None and stream is None and q is not None and k is not None:
+        st = (_short or _load_marshal()).rotary(q, k, inv_freq, row_offsets, first, q_norm, k_norm, eps, neighbours,
+                                                out["q"], out["k"])
+        if st is not None:
+            _check(st, "dspark_rotary")
+            return out
     lib = load_library()
     x = q if q is not None else k
     if x is None:
@@ -806,6 +813,13 @@ def dspark_kv_append(q, k, v, inv_freq, k_cache, v_cache, cache_len, page_table,
     and turned at positions cache_len[b] + i, the queries (None: no queries) come
     back as {"q"} (``out`` to reuse its rows, {"q": q} in place), keys and values go
     into the paged cache.  Arguments as for those two."""
+    if out is not None and stream is None and q is not None and "q" in out:
+        st = (_short or _load_marshal()).kv_append(q, k, v, inv_freq, k_cache, v_cache, cache_len, page_table,
+                                                     row_offsets, q_norm, k_norm, eps, neighbours, k_scale, v_scale,
+                                                     out["q"])
+        if st is not None:
+            _check(st, "dspark_kv_append")
+            return out
     lib = load_library()
     dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     dt = _row_dtype(k, "k")
@@ -928,6 +942,13 @@ def dspark_window_attention(q, k_cache, v_cache, cache_len, page_table, window: 
     p sees the `window` newest tokens, itself among them, and the first `sinks`
     tokens of its request.  Pages that no row of a request sees may be gone from
     page_table.  Everything else as for dspark_paged_attention."""
+    if out is not None and stream is None and (not lse or "lse" in out):
+        st = (_short or _load_marshal()).window_attention(
+            q, k_cache, v_cache, cache_len, page_table, window, sinks, row_offsets, k_scale, v_scale, scale, max_rows,
+            out["out"], out.get("lse"), workspace if workspace is not None else out.get("workspace"))
+        if st is not None:
+            _check(st, "dspark_window_attention")
+            return out
     lib = load_library()
     dev, cdt, n_pages, Hkv, ps, D = _cache(k_cache, v_cache, k_scale, v_scale)
     dt = _row_dtype(q, "q")
@@ -1020,6 +1041,13 @@ def dspark_logit_rules(logits, *, row_offsets=None, history=None, history_len=No
     1], bias_ids, bias_values: each request's biases; masks [n_masks, >= V / 32]
     int32 bits of what is allowed and mask_index [n], each row's mask (outside the
     table: none).  Rows of no request keep what ``out`` holds (zeros in a new result)."""
+    if out is not None and stream is None:
+        st = (_short or _load_marshal()).logit_rules(logits, row_offsets, history, history_len, prompt_len, drafts,
+                                                       repetition, frequency, presence, bias_offsets, bias_ids,
+                                                       bias_values, masks, mask_index, out)
+        if st is not None:
+            _check(st, "dspark_logit_rules")
+            return out
     torch = _torch()
     lib = load_library()
     if not isinstance(logits, torch.Tensor):

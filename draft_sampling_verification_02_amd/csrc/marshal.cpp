@@ -1,5 +1,5 @@
-// marshal.cpp -- the short way from torch tensors to the cache and attention
-// entry points, for calls whose kernels take a few microseconds.
+// marshal.cpp -- the short way from torch tensors to the cache, rotation,
+// attention and logit entry points, for calls whose kernels take a few microseconds.
 //
 // Each function checks its tensors (types, shapes, layouts, one device, which
 // is the current one), calls the C entry point on torch's current stream and
@@ -23,6 +23,11 @@ struct Entry {
     decltype(&dspark_paged_attention) paged;
     decltype(&dspark_prompt_attention_workspace_size) prompt_ws;
     decltype(&dspark_prompt_attention) prompt;
+    decltype(&dspark_rotary) rotary;
+    decltype(&dspark_kv_append) append;
+    decltype(&dspark_window_attention_workspace_size) window_ws;
+    decltype(&dspark_window_attention) window;
+    decltype(&dspark_logit_rules) rules;
 } entry{};
 PyObject *raw_stream = nullptr;  // device index -> hipStream_t of torch's current stream
 PyObject *current_device = nullptr;
@@ -279,14 +284,215 @@ PyObject *prompt_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                         D, scale, a[6] == Py_True, out, lse, ws, bytes, s));
 }
 
-// bind(addresses of the six entry points, raw_stream, current_device)
+// What a rotation takes beside its rows.
+struct Turn {
+    float *freq = nullptr, eps = 0.f;
+    void *q_norm = nullptr, *k_norm = nullptr;
+    int rot = 0, norm_dtype = 0;
+    bool neighbours = false;
+};
+Turn turn_of(Call &c, PyObject *freq, PyObject *qn, PyObject *kn, PyObject *eps, PyObject *neighbours, at::ScalarType type,
+             int64_t D) {
+    Turn t;
+    t.norm_dtype = type == at::kHalf ? DSPARK_F16 : DSPARK_BF16;
+    if (freq != Py_None) {
+        const at::Tensor *f = c.tensor(freq);
+        if (!c.ok || f->dim() != 1 || f->scalar_type() != at::kFloat || !f->is_contiguous() || f->size(0) > D) {
+            c.ok = false;
+            return t;
+        }
+        t.freq = static_cast<float *>(f->data_ptr());
+        t.rot = int(2 * f->size(0));
+    }
+    PyObject *first = qn != Py_None ? qn : kn;
+    if (first != Py_None) {
+        const at::Tensor *w = c.tensor(first);
+        if (!c.ok) return t;
+        const at::ScalarType kind = w->scalar_type() == at::kFloat ? at::kFloat : type;
+        if (kind == at::kFloat) t.norm_dtype = DSPARK_F32;
+        t.q_norm = c.at_dense_or_none(qn, kind, {D});
+        t.k_norm = c.at_dense_or_none(kn, kind, {D});
+    }
+    if (!PyFloat_Check(eps) || !PyBool_Check(neighbours)) {
+        c.ok = false;
+        return t;
+    }
+    t.eps = float(PyFloat_AS_DOUBLE(eps));
+    t.neighbours = neighbours == Py_True;
+    return t;
+}
+
+// rotary(q, k, inv_freq, row_offsets, first, q_norm, k_norm, eps, neighbours, q_out, k_out): q and k both there
+PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 11) Py_RETURN_NONE;
+    Call c;
+    int64_t qs = 0, ks = 0, qo = 0, ko = 0;
+    const at::Tensor *q = c.rows(a[0], qs), *k = c.rows(a[1], ks), *to_q = c.rows(a[9], qo), *to_k = c.rows(a[10], ko);
+    if (!c.ok || q->size(0) != k->size(0) || q->size(2) != k->size(2) || k->scalar_type() != q->scalar_type() ||
+        to_q->scalar_type() != q->scalar_type() || to_k->scalar_type() != q->scalar_type() || to_q->sizes() != q->sizes() ||
+        to_k->sizes() != k->sizes() || !fits_int(q->size(0)) || !fits_int(q->size(1)) || !fits_int(k->size(1)) ||
+        !fits_int(q->size(2)))
+        Py_RETURN_NONE;
+    int64_t B = q->size(0);
+    int32_t *off = nullptr;
+    if (a[3] != Py_None) {
+        const at::Tensor *t = c.tensor(a[3]);
+        if (!c.ok || t->dim() != 1 || t->size(0) < 2) Py_RETURN_NONE;
+        B = t->size(0) - 1;
+        off = c.at_dense<int32_t>(a[3], at::kInt, {B + 1});
+    }
+    if (!fits_int(B)) Py_RETURN_NONE;
+    int32_t *first = c.at_dense_or_none<int32_t>(a[4], at::kInt, {B});
+    const Turn t = turn_of(c, a[2], a[5], a[6], a[7], a[8], q->scalar_type(), q->size(2));
+    void *s = nullptr;
+    const int dt = dtype_of(*q);
+    if (dt < 0 || !c.stream(s)) Py_RETURN_NONE;
+    return PyLong_FromLong(entry.rotary(q->data_ptr(), k->data_ptr(), qs, ks, dt, off, int(q->size(0)), first, int(B),
+                                        int(q->size(1)), int(k->size(1)), int(q->size(2)), t.freq, t.rot, t.neighbours,
+                                        t.q_norm, t.k_norm, t.norm_dtype, t.eps, to_q->data_ptr(), to_k->data_ptr(), qo,
+                                        ko, s));
+}
+
+// kv_append(q, k, v, inv_freq, k_cache, v_cache, cache_len, page_table, row_offsets, q_norm, k_norm, eps, neighbours,
+//           k_scale, v_scale, q_out): q is there
+PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 16) Py_RETURN_NONE;
+    Call c;
+    int64_t qs = 0, ks = 0, vs = 0, qo = 0;
+    const at::Tensor *q = c.rows(a[0], qs), *k = c.rows(a[1], ks), *v = c.rows(a[2], vs), *to_q = c.rows(a[15], qo);
+    const Cache m = cache_of(c, a[4], a[5], a[13], a[14]);
+    if (!c.ok || k->sizes() != v->sizes() || k->scalar_type() != v->scalar_type() || k->scalar_type() != q->scalar_type() ||
+        k->size(1) != m.heads || k->size(2) != m.D || q->size(2) != m.D || q->size(0) != k->size(0) ||
+        to_q->sizes() != q->sizes() || to_q->scalar_type() != q->scalar_type() || !fits_int(q->size(1)) || a[6] == Py_None)
+        Py_RETURN_NONE;
+    const Requests r = requests_of(c, a[7], a[8], a[6], k->size(0));
+    const Turn t = turn_of(c, a[3], a[9], a[10], a[11], a[12], k->scalar_type(), m.D);
+    void *s = nullptr;
+    const int dt = dtype_of(*k);
+    if (dt < 0 || !c.stream(s)) Py_RETURN_NONE;
+    return PyLong_FromLong(entry.append(q->data_ptr(), k->data_ptr(), v->data_ptr(), qs, ks, vs, dt, r.offsets,
+                                        int(k->size(0)), r.lens, r.table, r.B, r.max_pages, int(q->size(1)), m.heads, m.D,
+                                        t.freq, t.rot, t.neighbours, t.q_norm, t.k_norm, t.norm_dtype, t.eps,
+                                        to_q->data_ptr(), qo, m.k->data_ptr(), m.v->data_ptr(), m.k_scale, m.v_scale,
+                                        m.dtype, m.n_pages, m.page_size, s));
+}
+
+// a whole number of at least 0 that fits an int
+bool count_of(PyObject *o, int &x) {
+    if (!PyLong_CheckExact(o)) return false;
+    int overflow = 0;
+    const long v = PyLong_AsLongAndOverflow(o, &overflow);
+    if (overflow || !fits_int(v)) return false;
+    x = int(v);
+    return true;
+}
+
+// window_attention(q, k_cache, v_cache, cache_len, page_table, window, sinks, row_offsets, k_scale, v_scale, scale,
+//                  max_rows, out, lse, workspace)
+PyObject *window_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 15) Py_RETURN_NONE;
+    Call c;
+    int64_t qs = 0;
+    const at::Tensor *q = c.rows(a[0], qs);
+    const Cache m = cache_of(c, a[1], a[2], a[8], a[9]);
+    float scale = 0.f;
+    int window = 0, sinks = 0;
+    if (!c.ok || q->size(2) != m.D || a[3] == Py_None || !fits_int(q->size(1)) || !scale_of(a[10], m.D, scale) ||
+        !count_of(a[5], window) || !count_of(a[6], sinks))
+        Py_RETURN_NONE;
+    const Requests r = requests_of(c, a[4], a[7], a[3], q->size(0));
+    if (!c.ok) Py_RETURN_NONE;
+    int max_rows = int((q->size(0) + r.B - 1) / r.B);
+    if (a[11] != Py_None && !count_of(a[11], max_rows)) Py_RETURN_NONE;
+    const int heads = int(q->size(1)), dt = dtype_of(*q);
+    void *out = c.at_dense(a[12], q->scalar_type(), q->sizes());
+    float *lse = c.at_dense_or_none<float>(a[13], at::kFloat, q->sizes().slice(0, 2));
+    size_t bytes = 0;
+    void *ws = workspace_of(c, a[14], entry.window_ws(max_rows, heads, m.heads, m.D), bytes);
+    void *s = nullptr;
+    if (dt < 0 || !c.stream(s)) Py_RETURN_NONE;
+    return PyLong_FromLong(entry.window(q->data_ptr(), qs, dt, r.offsets, int(q->size(0)), max_rows, r.lens, r.table, r.B,
+                                        r.max_pages, heads, m.heads, m.D, m.k->data_ptr(), m.v->data_ptr(), m.k_scale,
+                                        m.v_scale, m.dtype, m.n_pages, m.page_size, window, sinks, scale, out, lse, ws,
+                                        bytes, s));
+}
+
+// logit_rules(logits, row_offsets, history, history_len, prompt_len, drafts, repetition, frequency, presence,
+//             bias_offsets, bias_ids, bias_values, masks, mask_index, out)
+PyObject *logit_rules(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 15) Py_RETURN_NONE;
+    Call c;
+    auto padded = [&](PyObject *o, int64_t &stride) -> const at::Tensor * {
+        const at::Tensor *t = c.tensor(o);
+        if (!c.ok || t->dim() != 2 || t->size(0) == 0 || t->size(1) == 0 || t->stride(1) != 1) {
+            c.ok = false;
+            return nullptr;
+        }
+        stride = t->size(0) > 1 ? t->stride(0) : t->size(1);
+        return t;
+    };
+    int64_t stride = 0, out_stride = 0;
+    const at::Tensor *x = padded(a[0], stride), *out = padded(a[14], out_stride);
+    if (!c.ok || out->scalar_type() != at::kFloat || out->sizes() != x->sizes() || !fits_int(x->size(0)) ||
+        !fits_int(x->size(1)))
+        Py_RETURN_NONE;
+    const int dt = x->scalar_type() == at::kFloat ? DSPARK_F32 : dtype_of(*x);
+    if (dt < 0 || dt == DSPARK_E4M3) Py_RETURN_NONE;
+    const int64_t rows = x->size(0), V = x->size(1);
+    int64_t B = rows;
+    int32_t *off = nullptr;
+    if (a[1] != Py_None) {
+        const at::Tensor *t = c.tensor(a[1]);
+        if (!c.ok || t->dim() != 1 || t->size(0) < 2) Py_RETURN_NONE;
+        B = t->size(0) - 1;
+        off = c.at_dense<int32_t>(a[1], at::kInt, {B + 1});
+    }
+    if (!fits_int(B)) Py_RETURN_NONE;
+    auto table = [&](PyObject *o, int64_t lines, int64_t &width) -> int32_t * {
+        if (o == Py_None) return nullptr;
+        const at::Tensor *t = c.tensor(o);
+        if (!c.ok || t->dim() != 2 || !fits_int(t->size(1)) || (lines >= 0 && t->size(0) != lines) || !fits_int(t->size(0)) ||
+            t->scalar_type() != at::kInt || !t->is_contiguous()) {
+            c.ok = false;
+            return nullptr;
+        }
+        width = t->size(1);
+        return static_cast<int32_t *>(t->data_ptr());
+    };
+    int64_t width = 0, gamma = 0, words = 0, n_masks = 0, n_biases = 0;
+    int32_t *history = table(a[2], B, width), *drafts = table(a[5], B, gamma), *masks = table(a[12], -1, words);
+    int32_t *history_len = c.at_dense_or_none<int32_t>(a[3], at::kInt, {B});
+    int32_t *prompt_len = c.at_dense_or_none<int32_t>(a[4], at::kInt, {B});
+    float *rep = c.at_dense_or_none<float>(a[6], at::kFloat, {B}), *freq = c.at_dense_or_none<float>(a[7], at::kFloat, {B});
+    float *pres = c.at_dense_or_none<float>(a[8], at::kFloat, {B});
+    int32_t *bias_off = c.at_dense_or_none<int32_t>(a[9], at::kInt, {B + 1}), *ids = nullptr;
+    float *values = nullptr;
+    if (bias_off) {
+        const at::Tensor *t = c.tensor(a[10]);
+        if (!c.ok || !fits_int(t->numel())) Py_RETURN_NONE;
+        n_biases = t->numel();
+        ids = c.at_dense<int32_t>(a[10], at::kInt, {n_biases});
+        values = c.at_dense<float>(a[11], at::kFloat, {n_biases});
+    }
+    int32_t *index = c.at_dense_or_none<int32_t>(a[13], at::kInt, {rows});
+    if (!c.ok || (history && !history_len) || (masks && (!index || words < (V + 31) / 32))) Py_RETURN_NONE;
+    if (masks) n_masks = THPVariable_Unpack(a[12]).size(0);
+    void *s = nullptr;
+    if (!c.stream(s)) Py_RETURN_NONE;
+    return PyLong_FromLong(entry.rules(x->data_ptr(), stride, dt, off, int(rows), int(B), int(V), history, int(width),
+                                       history_len, prompt_len, drafts, int(gamma), rep, freq, pres, bias_off, ids, values,
+                                       int(n_biases), masks, int(n_masks), words, index,
+                                       static_cast<float *>(out->data_ptr()), out_stride, s));
+}
+
+// bind(addresses of the eleven entry points, raw_stream, current_device)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (n != 8) {
-        PyErr_SetString(PyExc_TypeError, "bind: six addresses and two functions");
+    if (n != 13) {
+        PyErr_SetString(PyExc_TypeError, "bind: eleven addresses and two functions");
         return nullptr;
     }
-    void *p[6];
-    for (int i = 0; i < 6; ++i) {
+    void *p[11];
+    for (int i = 0; i < 11; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (!p[i]) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null address");
@@ -299,10 +505,15 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     entry.paged = reinterpret_cast<decltype(entry.paged)>(p[3]);
     entry.prompt_ws = reinterpret_cast<decltype(entry.prompt_ws)>(p[4]);
     entry.prompt = reinterpret_cast<decltype(entry.prompt)>(p[5]);
-    Py_INCREF(a[6]);
-    Py_INCREF(a[7]);
-    Py_XSETREF(raw_stream, a[6]);
-    Py_XSETREF(current_device, a[7]);
+    entry.rotary = reinterpret_cast<decltype(entry.rotary)>(p[6]);
+    entry.append = reinterpret_cast<decltype(entry.append)>(p[7]);
+    entry.window_ws = reinterpret_cast<decltype(entry.window_ws)>(p[8]);
+    entry.window = reinterpret_cast<decltype(entry.window)>(p[9]);
+    entry.rules = reinterpret_cast<decltype(entry.rules)>(p[10]);
+    Py_INCREF(a[11]);
+    Py_INCREF(a[12]);
+    Py_XSETREF(raw_stream, a[11]);
+    Py_XSETREF(current_device, a[12]);
     Py_RETURN_NONE;
 }
 
@@ -320,7 +531,8 @@ PyObject *guarded(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 #define METHOD(name) \
     { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {METHOD(bind),           METHOD(kv_write), METHOD(kv_read), METHOD(paged_attention),
-                         METHOD(prompt_attention), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(prompt_attention), METHOD(rotary), METHOD(kv_append), METHOD(window_attention),
+                         METHOD(logit_rules), {nullptr, nullptr, 0, nullptr}};
 #undef METHOD
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
