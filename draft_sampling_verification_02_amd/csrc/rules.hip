@@ -27,27 +27,37 @@ struct RulesParams {
     int slices;
 };
 
-constexpr long long kManySlices = 512;        // slices of 4096 entries that fill the chip
 constexpr uint32_t kInPrompt = 0x80000000u;  // beside a token's count
 
-// Four entries of a row as floats.
+// W entries of a row as they come, and as floats.
+template <typename L, int W>
+struct Piece {
+    typedef L type __attribute__((ext_vector_type(W)));
+    static_assert(W == 4, "one entry is a type of its own");
+};
 template <typename L>
-__device__ __forceinline__ f32x4_t load4(const L *p) {
-    if constexpr (sizeof(L) == 4) {
-        return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t *>(p));
-    } else {
-        using T = typename std::conditional<std::is_same<L, __bf16>::value, TypeBf16, TypeF16>::type;
-        float f[4];
-        widen4<T>(__builtin_nontemporal_load(reinterpret_cast<const u32x2_t *>(p)), f);
-        return f32x4_t{f[0], f[1], f[2], f[3]};
-    }
+struct Piece<L, 1> {
+    typedef L type;
+};
+template <typename L, int W>
+__device__ __forceinline__ float piece_at(const typename Piece<L, W>::type &x, int w) {
+    if constexpr (W == 1)
+        return float(x);
+    else
+        return float(x[w]);
 }
 
 // A workgroup of NT threads, each with E entries of the slice: V4 four
 // neighbouring ones at a time (rows 16-byte aligned), else one at a time.
+//
+// What a row needs comes on the way one row ahead, and its mask two: the mask
+// says which entries are read.  (An entry that is not reads the slice's first one
+// instead, one line for all of them: a load without a branch, so that the ones
+// before it can be waited for by count.)
 template <typename L, int NT, int E, bool V4>
 __global__ __launch_bounds__(NT) void rules_kernel(RulesParams p) {
     constexpr int S = NT * E, W = V4 ? 4 : 1, N = E / W;  // entries of the slice, of a load, loads
+    using X = typename Piece<L, W>::type;
     __shared__ __attribute__((aligned(16))) uint32_t count[S];
     __shared__ __attribute__((aligned(16))) float bias[S];
     const RulesArgs &a = p.a;
@@ -61,20 +71,56 @@ __global__ __launch_bounds__(NT) void rules_kernel(RulesParams p) {
     }
     if (r0 >= r1) return;
 
+    // ---- what is on its way first: the text, the first rows' masks, the first row
     const float rho = a.repetition ? a.repetition[b] : 1.f;
     const float phi = a.frequency ? a.frequency[b] : 0.f, pi = a.presence ? a.presence[b] : 0.f;
     const bool counted = !(rho == 1.f && phi == 0.f && pi == 0.f);
+    const int32_t *text = a.history ? a.history + (long long)b * a.max_history : nullptr;
+    const int len = counted && text ? min(max(a.history_len[b], 0), a.max_history) : 0;
+    const int given = a.prompt_len ? a.prompt_len[b] : 0;
+    constexpr int FLY = 8;  // tokens of a thread under way
+    int tok[FLY];
+    auto read_text = [&](int t0, int *to) __device__ {  // (past the end the last token again: not looked at)
+#pragma unroll
+        for (int k = 0; k < FLY; ++k) to[k] = text[min(t0 + k * NT + tid, len - 1)];
+    };
+    auto entry = [&](int k) __device__ { return (k * NT + tid) * W; };  // first entry of load k
+    // which entries of row r the thread keeps, W bits a load (none of a row past the last one)
+    auto read_mask = [&](int r, uint32_t *keep) __device__ {
+        const int m = a.mask_index && r < r1 ? a.mask_index[r] : -1;
+        const bool masked = m >= 0 && m < a.n_masks;
+        const int32_t *bits = masked ? a.masks + (long long)m * a.mask_stride + v0 / 32 : nullptr;
+#pragma unroll
+        for (int k = 0; k < N; ++k) keep[k] = masked ? uint32_t(bits[min(entry(k), size - 1) / 32]) : r < r1 ? ~0u : 0u;
+    };
+    auto kept = [&](const uint32_t *keep, int k) __device__ {
+        return entry(k) < size ? keep[k] >> (entry(k) & 31) & ((1u << W) - 1) : 0u;
+    };
+    auto read_row = [&](int r, const uint32_t *keep, X *x) __device__ {
+        const L *row = static_cast<const L *>(a.logits) + min(r, r1 - 1) * a.stride + v0;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            x[k] = __builtin_nontemporal_load(reinterpret_cast<const X *>(row + (kept(keep, k) ? entry(k) : 0)));
+    };
+    uint32_t keep[N], keep_next[N];
+    X x[N], x_next[N];
+    if (len > 0) read_text(0, tok);
+    read_mask(r0, keep);
+    read_mask(r0 + 1, keep_next);
     int e0 = 0, e1 = 0;
     if (a.bias_offsets) {
         e0 = min(max(a.bias_offsets[b], 0), a.n_biases);
         e1 = min(max(a.bias_offsets[b + 1], 0), a.n_biases);
     }
     const bool biased = e0 < e1;
-    for (int i = tid; i < S; i += NT) {
-        count[i] = 0;
-        bias[i] = 0.f;
+    read_row(r0, keep, x);
+
+    if (counted || biased) {
+        for (int i = tid; i < S; i += NT) count[i] = 0;
+        if (biased)
+            for (int i = tid; i < S; i += NT) bias[i] = 0.f;
+        __syncthreads();
     }
-    __syncthreads();
     // ---- biases: NT of the list at a time; of those with one token the first is added first
     for (int e = e0; e < e1; e += NT) {
         int i = -1;
@@ -95,35 +141,30 @@ __global__ __launch_bounds__(NT) void rules_kernel(RulesParams p) {
         }
     }
     // ---- the text
-    if (counted && a.history) {
-        const int32_t *text = a.history + (long long)b * a.max_history;
-        const int len = min(max(a.history_len[b], 0), a.max_history);
-        const int given = a.prompt_len ? a.prompt_len[b] : 0;
-        constexpr int FLY = 8;
-        for (int t0 = 0; t0 < len; t0 += NT * FLY) {
-            int tok[FLY];
+    for (int t0 = 0; t0 < len; t0 += NT * FLY) {
+        int next[FLY];
+        read_text(t0 + NT * FLY, next);
 #pragma unroll
-            for (int k = 0; k < FLY; ++k) {
-                const int t = t0 + k * NT + tid;
-                tok[k] = t < len ? text[t] : -1;
+        for (int k = 0; k < FLY; ++k) {
+            // (ids outside the vocabulary are in no slice, negative ones far above all as unsigned numbers)
+            const uint32_t i = uint32_t(tok[k]) - uint32_t(v0);
+            const int t = t0 + k * NT + tid;
+            if (t < len && i < uint32_t(size)) {
+                if (t < given)
+                    atomicOr(&count[i], kInPrompt);
+                else
+                    atomicAdd(&count[i], 1u);
             }
-#pragma unroll
-            for (int k = 0; k < FLY; ++k) {
-                const int i = tok[k] < 0 ? -1 : tok[k] - v0;
-                if (unsigned(i) < unsigned(size)) {
-                    if (t0 + k * NT + tid < given)
-                        atomicOr(&count[i], kInPrompt);
-                    else
-                        atomicAdd(&count[i], 1u);
-                }
-            }
+            tok[k] = next[k];
         }
-        __syncthreads();
     }
+    if (counted || biased) __syncthreads();
 
     // ---- the rows
-    auto entry = [&](int k) __device__ { return (k * NT + tid) * W; };  // first entry of load k
     for (int r = r0; r < r1; ++r) {
+        uint32_t keep_later[N];
+        read_row(r + 1, keep_next, x_next);
+        read_mask(r + 2, keep_later);
         if (r > r0 && counted && a.drafts && r - r0 - 1 < a.gamma) {
             const int i = a.drafts[(long long)b * a.gamma + (r - r0 - 1)] - v0;
             if (unsigned(i) < unsigned(size)) {
@@ -132,61 +173,46 @@ __global__ __launch_bounds__(NT) void rules_kernel(RulesParams p) {
                 __syncthreads();
             }
         }
-        const L *row = static_cast<const L *>(a.logits) + r * a.stride + v0;
         float *out = a.out + r * a.out_stride + v0;
-        const int m = a.mask_index ? a.mask_index[r] : -1;
-        const bool masked = m >= 0 && m < a.n_masks;
-        const int32_t *bits = masked ? a.masks + (long long)m * a.mask_stride + v0 / 32 : nullptr;
-        uint32_t keep[N];
-        float z[N][W];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const int i = entry(k);
-            keep[k] = i < size ? (1u << W) - 1 : 0u;
-            if (masked && i < size) keep[k] &= uint32_t(bits[i / 32]) >> (i & 31);
+            if (i < size) {
+                float z[W];
+                uint32_t c[W] = {};
+#pragma unroll
+                for (int w = 0; w < W; ++w) z[w] = piece_at<L, W>(x[k], w);
+                if (counted) {
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) any |= c[w] = count[i + w];
+                    if (any) {
+#pragma unroll
+                        for (int w = 0; w < W; ++w)
+                            if (c[w]) {
+                                const float n = float(c[w] & ~kInPrompt);
+                                const float y = z[w] > 0.f ? z[w] / rho : z[w] * rho;
+                                z[w] = y - (phi * n + (n > 0.f ? pi : 0.f));
+                            }
+                    }
+                }
+                const uint32_t bits = kept(keep, k);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    if (biased) z[w] += bias[i + w];
+                    if (!((bits >> w) & 1)) z[w] = kNegInf;
+                }
+                if constexpr (V4)
+                    __builtin_nontemporal_store(f32x4_t{z[0], z[1], z[2], z[3]}, reinterpret_cast<f32x4_t *>(out + i));
+                else
+                    out[i] = z[0];
+            }
         }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-#pragma unroll
-            for (int w = 0; w < W; ++w) z[k][w] = 0.f;
-            if (keep[k]) {
-                if constexpr (V4) {
-                    const f32x4_t x = load4<L>(row + entry(k));
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) z[k][w] = x[w];
-                } else {
-                    z[k][0] = float(row[entry(k)]);
-                }
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i = entry(k);
-            if (i >= size) continue;
-            if (counted) {
-                uint32_t c[W], any = 0;
-#pragma unroll
-                for (int w = 0; w < W; ++w) any |= c[w] = count[i + w];
-                if (any) {
-#pragma unroll
-                    for (int w = 0; w < W; ++w)
-                        if (c[w]) {
-                            const float n = float(c[w] & ~kInPrompt);
-                            float x = z[k][w];
-                            x = x > 0.f ? x / rho : x * rho;
-                            z[k][w] = x - (phi * n + (n > 0.f ? pi : 0.f));
-                        }
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                if (biased) z[k][w] += bias[i + w];
-                if (!((keep[k] >> w) & 1)) z[k][w] = kNegInf;
-            }
-            if constexpr (V4)
-                __builtin_nontemporal_store(f32x4_t{z[k][0], z[k][1], z[k][2], z[k][3]}, reinterpret_cast<f32x4_t *>(out + i));
-            else
-                out[i] = z[k][0];
+            x[k] = x_next[k];
+            keep[k] = keep_next[k];
+            keep_next[k] = keep_later[k];
         }
     }
 }
@@ -201,12 +227,28 @@ void launch_rules_slices(RulesParams p, bool v4, hipStream_t s) {
         launch_kernel("logit_rules", rules_kernel<L, NT, E, false>, grid, dim3(NT), s, p);
 }
 
+// The slices.  Few entries in all take small slices, for more workgroups; long
+// texts, which every slice of a request reads, take more threads a workgroup and
+// larger slices.  Us a call of 1 to 6 bfloat16 rows a request, V = 129280, in 256
+// threads of 8 entries / 512 of 8 / 1024 of 4 / 256 of 4, > < the rule's:
+//   256 requests, texts up to  4096  >149< / 158  / 233  / 200
+//                             16384   178 />176< / 242  / 235
+//                             60000   259 />222< / 279  / 361
+//   16 requests, 600          >19.2< / 21.3 / 22.2 / 20.6
+//   8                          13.7 / 13.7 / 13.2 />12.3<
+//   1, one row                  5.5 /  5.9 /  6.3 /> 4.9<
+//   2, texts up to 16384       15.1 / 14.7 / 12.9 />11.8<
+//                  32768       18.5 / 15.9 />13.8</ 15.9
+constexpr long long kFewEntries = 1500000;
+constexpr int kLongText = 16384, kLongTextFew = 24576;
+
 template <typename L>
 void launch_rules_typed(const RulesParams &p, bool v4, hipStream_t s) {
-    if ((long long)p.a.B * p.a.V >= kManySlices * 4096LL)
-        launch_rules_slices<L, 512, 8>(p, v4, s);
+    const int text = p.a.history ? p.a.max_history : 0;
+    if ((long long)p.a.B * p.a.V >= kFewEntries)
+        text < kLongText ? launch_rules_slices<L, 256, 8>(p, v4, s) : launch_rules_slices<L, 512, 8>(p, v4, s);
     else
-        launch_rules_slices<L, 256, 4>(p, v4, s);
+        text < kLongTextFew ? launch_rules_slices<L, 256, 4>(p, v4, s) : launch_rules_slices<L, 1024, 4>(p, v4, s);
 }
 
 }  // namespace

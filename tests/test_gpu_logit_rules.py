@@ -124,6 +124,10 @@ SHAPES = [
     (4099, [2, 1, 1], 300, 1, 40, 2, 1, 2),
     (12928, [4] * 9, 700, 3, 5, 1, 0, 1),
     (50257, [1, 5], 3000, 4, 30, 2, 0, 0),
+    (20000, [2, 1], 30000, 3, 9, 2, 0, 0),
+    (20001, [2, 1], 25000, 3, 9, 2, 0, 1),
+    (151936, [2] * 10, 20000, 1, 7, 2, 0, 0),
+    (151937, [1] * 10, 700, 1, 7, 2, 0, 0),
     (33, [2, 2, 2], 9, 2, 3, 4, 0, 0),
     (1, [1, 2], 4, 1, 2, 1, 0, 0),
 ]
