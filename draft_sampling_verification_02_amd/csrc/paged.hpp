@@ -399,9 +399,11 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
         };
         clear();
 
-        // This wave's tiles, whose first is on its way (CAREFUL: with every one looked over).
-        auto walk = [&](auto careful_tag) __device__ __attribute__((always_inline)) {
+        // This wave's tiles, whose first is on its way (CAREFUL: with every one looked over), for the first NU
+        // blocks of queries: the others are empty.
+        auto walk = [&](auto careful_tag, auto used_tag) __device__ __attribute__((always_inline)) {
             constexpr bool CAREFUL = decltype(careful_tag)::value;
+            constexpr int NU = decltype(used_tag)::value;
             for (int i = 0; i < tiles; ++i) {
                 const int t = tile_at(i);
                 const int bad_now = int(bad_page(pa)) | int(bad_page(pb)) << 1;  // the tile's halves on pages outside the cache
@@ -414,11 +416,11 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                 // ---- scores: s[q][half][r] is token 16 half + 4 g + r, query n
                 vm_wait<SH::VL>();
                 const uint32_t kbase = fresh(ring + kread);
-                f32x4_t s[NQ][2];
+                f32x4_t s[NU][2];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) s[q][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    for (int q = 0; q < NU; ++q) s[q][hf] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int k = 0; k < KSTEP; ++k) {
                         const u32x4v_t x = lds_read<u32x4v_t>(kbase ^ (64 * k), 16 * hf * S::RB);
@@ -427,12 +429,12 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                             e4m3_to8(u32x2_t{x[0], x[1]}, lo);
                             e4m3_to8(u32x2_t{x[2], x[3]}, hi);
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(lo, qf[q][2 * k], s[q][hf]);
+                            for (int q = 0; q < NU; ++q) s[q][hf] = mma16(lo, qf[q][2 * k], s[q][hf]);
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q) s[q][hf] = mma16(hi, qf[q][2 * k + 1], s[q][hf]);
+                            for (int q = 0; q < NU; ++q) s[q][hf] = mma16(hi, qf[q][2 * k + 1], s[q][hf]);
                         } else {
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q)
+                            for (int q = 0; q < NU; ++q)
                                 s[q][hf] = mma16(__builtin_bit_cast(V8, x), qf[q][k], s[q][hf]);
                         }
                     }
@@ -448,7 +450,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                             const float ks = scale_of((kw >> (8 * r)) & 255);
                             vs[hf][r] = scale_of((vw >> (8 * r)) & 255);
 #pragma unroll
-                            for (int q = 0; q < NQ; ++q) s[q][hf][r] *= ks;
+                            for (int q = 0; q < NU; ++q) s[q][hf][r] *= ks;
                         }
                     }
                 }
@@ -458,9 +460,9 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                 // ---- running maximum, probabilities
                 const bool edge = WIN && t < low_max && t + kTokens > a.sinks;  // before the window of a query
                 const bool masked = t + kTokens > lim_min || bad_now != 0 || edge;
-                P8 pf[NQ], pr_rest[kTwoTerms<T, E4> ? NQ : 1];
+                P8 pf[NU], pr_rest[kTwoTerms<T, E4> ? NU : 1];
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
+                for (int q = 0; q < NU; ++q) {
                     if (masked) {
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf)
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                                 const uint32_t row = vbuf + k * S::RB + (E4 ? 4 * g : 8 * (g & 1));
                                 const int sw = S::v_swizzle(k);
 #pragma unroll
-                                for (int q = 0; q < NQ; ++q) {
+                                for (int q = 0; q < NU; ++q) {
                                     float pk = 1.f;
                                     if constexpr (!E4) {
                                         float score = 0.f;
@@ -596,7 +598,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                 for (int c = 0; c < CB; ++c) {
                     const P8 vf = v_frag(vbase, c);
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
+                    for (int q = 0; q < NU; ++q) {
                         o[q][c] = mma16(vf, pf[q], o[q][c]);
                         if constexpr (kTwoTerms<T, E4>) o[q][c] = mma16(vf, pr_rest[q], o[q][c]);
                     }
@@ -609,7 +611,10 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
                 nb = fb;
             }
         };
-        walk(std::false_type{});
+        if (NQ > 1 && nq_all - grp * QB <= QB / 2)
+            walk(std::false_type{}, std::integral_constant<int, NQ == 1 ? 1 : NQ / 2>{});
+        else
+            walk(std::false_type{}, std::integral_constant<int, NQ>{});
         // A small enough float16 probability is zero, and 0 * inf is NaN where the
         // row should be infinite.  A wave that finds NaN beside good sums walks its
         // tiles again, all of them looked over.  (bfloat16 has the range of the sums.)
@@ -624,7 +629,7 @@ __global__ __launch_bounds__(64 * NW, (PagedShape<E4, D, NQ, NW>::EU)) void page
             if (__any(nan)) {
                 issue_first();
                 clear();
-                walk(std::true_type{});
+                walk(std::true_type{}, std::integral_constant<int, NQ>{});
             }
         }
 
