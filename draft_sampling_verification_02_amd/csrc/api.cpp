@@ -674,10 +674,20 @@ bool rotary_rows_ok(const void *in, const void *out, int64_t stride, int64_t out
            row_stride_ok(out_stride, heads, head_dim) && (in != out || stride == out_stride);
 }
 
-// Whether a windowed call goes by query blocks over 16-bit caches (prompt.hpp), or
-// row by row as paged attention does.
-bool window_in_chunks(int max_rows, int group, int head_dim, int cache_dtype) {
-    return cache_dtype != DSPARK_E4M3 && int64_t(max_rows) * group > (head_dim >= 256 ? 32 : 64);
+// Whether a windowed call goes by query blocks (prompt.hpp), or row by row as paged
+// attention does (float16 rows over 8 bits always: their range there needs the
+// rows' kernel).  Us a call, rows / blocks (window 1000, four query heads a key
+// head; 64 requests of 8 key heads, D = 128: 16 rows 88 / 96, 20 138 / 85, 32 167 /
+// 117, 64 333 / 135; over 8 bits 16 rows 76 / 120, 32 141 / 142, 64 278 / 163; D = 64:
+// 32 rows 66 / 98, 48 98 / 103, 64 130 / 106, over 8 bits 32 83 / 114, 64 168 / 129;
+// 16 requests, D = 256: 16 rows 56 / 77, 20 86 / 78, 48 148 / 85, over 8 bits 32 88 /
+// 98, 64 179 / 159; one request, D = 128: 4 rows 15.2 / 15.0, 8 18.6 / 15.2, 16
+// 27 / 16).
+bool window_in_chunks(long long segments, int max_rows, int group, int head_dim, int dtype, int cache_dtype) {
+    const bool e4 = cache_dtype == DSPARK_E4M3;
+    if (e4 && dtype != DSPARK_BF16) return false;
+    const int64_t queries = int64_t(max_rows) * group;
+    return queries > (head_dim == 64 ? 192 : e4 ? 128 : 64) || (!e4 && queries > 16 && segments <= 16);
 }
 
 // the kernels multiply by scale * log2(e), which has to be finite
@@ -956,7 +966,7 @@ int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const in
     // what a request of the usual number of rows walks at most: sinks and windows in whole tiles
     const long long table = (long long)max_pages * page_size, walked = (long long)window + sinks + max_rows + 64;
     size_t need = 0;
-    if (window_in_chunks(max_rows, n_heads / n_kv_heads, head_dim, cache_dtype) &&
+    if (window_in_chunks((long long)B * n_kv_heads, max_rows, n_heads / n_kv_heads, head_dim, dtype, cache_dtype) &&
         prompt_launchable(B, n_rows, n_heads, n_kv_heads)) {
         const PromptPlan plan = window_chunk_plan(B, n_rows, walked < table ? walked : table, n_heads, n_kv_heads, head_dim);
         prompt_carve(nullptr, plan, n_kv_heads, head_dim, &need);
@@ -970,6 +980,8 @@ int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const in
         a.dtype = dtype;
         a.q_offsets = row_offsets;
         a.start = cache_len;
+        a.k_scale = k_scale;
+        a.v_scale = v_scale;
         a.page_table = page_table;
         a.B = B;
         a.n_rows = n_rows;
@@ -988,7 +1000,7 @@ int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const in
         return launch_window_chunks(a, plan, w, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
     }
     const PagedSizes z{n_rows, B, walked < table ? walked : table, max_rows, n_heads, n_kv_heads, head_dim,
-                       cache_dtype == DSPARK_E4M3};
+                       cache_dtype == DSPARK_E4M3, walked < table};
     const PagedPlan plan = paged_plan(z);
     paged_carve(nullptr, plan, head_dim, &need);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return DSPARK_ERR_WORKSPACE;

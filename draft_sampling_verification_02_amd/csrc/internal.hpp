@@ -307,6 +307,7 @@ struct PagedSizes {
     long long n_rows, requests, table_tokens;  // table_tokens: max_pages * page_size, the longest a request can be
     int max_rows, n_heads, n_kv_heads, head_dim;
     bool e4;
+    bool window = false;  // table_tokens are those that a window and the sinks leave
 };
 PagedPlan paged_plan(const PagedSizes &z);
 struct PagedWork {
@@ -344,7 +345,8 @@ struct PromptArgs {
     int B, n_rows, n_kv_rows, n_heads, n_kv_heads, head_dim;
     float scale;
     int causal;
-    // windowed calls: k and v are the pages of a cache
+    // windowed calls: k and v are the pages of a cache, of 8 bits with scales
+    const uint8_t *k_scale, *v_scale;
     const int32_t *start, *page_table;
     int max_pages, n_pages, page_size, window, sinks;
     void *out;

@@ -79,6 +79,13 @@ PagedPlan paged_plan(const PagedSizes &z) {
     p.waves = 4;
     p.grid = 256 * paged_per_cu(z.e4, z.head_dim, p.qblocks, 4);
     p.whole = z.table_tokens <= kWholeTokens;
+    // Walks behind a window are all about as long as it, so that whole segments
+    // load the chip evenly once there are enough.  Us a call, split / whole (8 key
+    // heads, D = 128; one row, bfloat16, window 1500: 4 requests 15.4 / 16.0, 16
+    // 26.5 / 20.3, 64 86.6 / 74.1; window 8000: 4 30.4 / 49.9, 16 106 / 100, 64 356 /
+    // 352; up to 6 rows over 8 bits, window 2048: 8 25.6 / 29.3, 16 31.5 / 30.2, 128
+    // 142 / 115; window 8000: 16 65 / 88, 32 120 / 135, 64 222 / 199).
+    if (z.window && z.requests * z.n_kv_heads >= (z.e4 && z.table_tokens > 4096 ? 512 : 128)) p.whole = 1;
     if (p.whole && z.table_tokens > kUnit && z.requests * z.n_kv_heads <= kFewSegments &&
         paged_per_cu(z.e4, z.head_dim, p.qblocks, 8) >= 1)
         p.waves = 8;

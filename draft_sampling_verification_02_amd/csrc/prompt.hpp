@@ -104,8 +104,10 @@ struct PromptShape {
 };
 
 // WIN: the keys are those of a paged cache, and the row at position i sees token
-// t <= i where i - t < a.window or t < a.sinks.
-template <typename T, int D, bool WIN>
+// t <= i where i - t < a.window or t < a.sinks.  E4 (bfloat16 rows): the cache holds
+// 8 bits; a tile comes through registers, where its values take their scale (which
+// is exact in bfloat16), and lies in LDS as one of 16 bits does.
+template <typename T, int D, bool WIN, bool E4 = false>
 __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_kernel(PromptParams p) {
     // (lambdas are inlined by force: one that is not takes what it captures, the sums among it, through memory)
     using SH = PromptShape<D>;
@@ -295,17 +297,71 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     auto issue_v = [&](int j) __device__ __attribute__((always_inline)) {
         if constexpr (!WIN) issue(a.v, a.v_stride, vst, voff, lds0 + (2 + (j & 1)) * S::BYTES, j * kKeys);
     };
-    // K of tile jk (windowed: that `ids` are of; they move on) and V of tile jv, those there are
+    // 8-bit tiles: 16 values a thread and load, and their row's scale, under way from one turn to the next
+    constexpr int LANES8 = D / 16, LOADS8 = E4 ? kKeys * LANES8 / SH::NT : 1, RPW8 = 64 / LANES8;
+    struct Raw {
+        u32x4v_t x[LOADS8];
+        uint32_t scale[LOADS8];
+    };
+    Raw raw_k{}, raw_v{};
+    auto load_raw = [&](const void *src, const uint8_t *scales, const Runs &r) __device__ __attribute__((always_inline)) {
+        Raw w;
+        const int ln = int(fresh(uint32_t(lane)));  // (registers are short: the places are made anew)
+#pragma unroll
+        for (int l = 0; l < LOADS8; ++l) {
+            const int row = l * (SH::NT / LANES8) + wave * RPW8;  // the wave's first row, of one run
+            const int run = row / 16;
+            const uint32_t at = (run & 2 ? (run & 1 ? r.at[3] : r.at[2]) : (run & 1 ? r.at[1] : r.at[0])) + uint32_t(row % 16);
+            const int mine = ln / LANES8;
+            w.x[l] = *reinterpret_cast<const u32x4v_t *>(static_cast<const uint8_t *>(src) + uint64_t(at) * D + (mine * D + ln % LANES8 * 16));
+            w.scale[l] = scales[uint64_t(at) + mine];
+        }
+        return w;
+    };
+    auto store_raw = [&](const Raw &w, uint32_t dst, auto swizzle) __device__ __attribute__((always_inline)) {
+        const int ln = int(fresh(uint32_t(lane)));
+#pragma unroll
+        for (int l = 0; l < LOADS8; ++l) {
+            const int row = l * (SH::NT / LANES8) + wave * RPW8 + ln / LANES8;
+            const float scale = scale_of(w.scale[l]);
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x[l][i], scale, false));
+                y[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x[l][i], scale, true));
+            }
+            const int c = ln % LANES8 * 2, sw = swizzle(row);
+            lds_write(dst + row * S::RB + ((c ^ sw) * 16), u32x4v_t{y[0], y[1], y[2], y[3]});
+            lds_write(dst + row * S::RB + (((c + 1) ^ sw) * 16), u32x4v_t{y[4], y[5], y[6], y[7]});
+        }
+    };
+    auto store_k = [&](int j) __device__ __attribute__((always_inline)) { store_raw(raw_k, lds0 + (j & 1) * S::BYTES, [](int r) __device__ __attribute__((always_inline)) { return S::k_swizzle(r); }); };
+    auto store_v = [&](int j) __device__ __attribute__((always_inline)) { store_raw(raw_v, lds0 + (2 + (j & 1)) * S::BYTES, [](int r) __device__ __attribute__((always_inline)) { return S::v_swizzle(r); }); };
+    // rows of the tile that `ids` are of, which move on to tile j + 1
+    auto take_rows = [&](int j) __device__ __attribute__((always_inline)) {
+        const Runs r = rows_of(ids, ahead);
+        if (j + 1 < ntile) {
+            ahead = tok(j + 1);
+            ids = fetch(ahead);
+        }
+        return r;
+    };
+    // K of tile jk (windowed: that `ids` are of) and V of tile jv, those there are; of an 8-bit cache what is under way
+    // goes to LDS, and the tiles after them get under way
     auto issue_next = [&](int jk, int jv) __device__ __attribute__((always_inline)) {
-        if constexpr (WIN) {
-            const Runs rows_k = rows_of(ids, ahead);
+        if constexpr (E4) {
+            if (jk < ntile) store_k(jk);
+            if (jv < ntile) store_v(jv);
+            if (jv + 1 < ntile) raw_v = load_raw(a.v, a.v_scale, rows_v);
+            if (jk + 1 < ntile) {
+                rows_v = take_rows(jk + 1);
+                raw_k = load_raw(a.k, a.k_scale, rows_v);
+            }
+        } else if constexpr (WIN) {
+            const Runs rows_k = take_rows(jk);
             if (jk < ntile) issue_paged(a.k, koff, lds0 + (jk & 1) * S::BYTES, rows_k);
             if (jv < ntile) issue_paged(a.v, voff, lds0 + (2 + (jv & 1)) * S::BYTES, rows_v);
             rows_v = rows_k;
-            if (jk + 1 < ntile) {
-                ahead = tok(jk + 1);
-                ids = fetch(ahead);
-            }
         } else {
             if (jk < ntile) issue_k(jk);
             if (jv < ntile) issue_v(jv);
@@ -316,14 +372,39 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         if constexpr (WIN) {
             ahead = tok(0);
             ids = fetch(ahead);
-            issue_next(0, ntile);
-            issue_paged(a.v, voff, lds0 + 2 * S::BYTES, rows_v);
+            rows_v = take_rows(0);
+            if constexpr (E4) {
+                raw_k = load_raw(a.k, a.k_scale, rows_v);
+                raw_v = load_raw(a.v, a.v_scale, rows_v);
+                store_k(0);
+                store_v(0);
+                if (ntile > 1) {
+                    rows_v = take_rows(1);
+                    raw_k = load_raw(a.k, a.k_scale, rows_v);
+                }
+            } else {
+                issue_paged(a.k, koff, lds0, rows_v);
+                issue_paged(a.v, voff, lds0 + 2 * S::BYTES, rows_v);
+            }
         } else {
             issue_k(0);
             issue_v(0);
         }
     };
-    auto issue_second_k = [&]() __device__ __attribute__((always_inline)) { issue_next(1, ntile); };
+    auto issue_second_k = [&]() __device__ __attribute__((always_inline)) {
+        if constexpr (E4) {
+            if (ntile > 1) {
+                store_k(1);
+                raw_v = load_raw(a.v, a.v_scale, rows_v);
+            }
+            if (ntile > 2) {
+                rows_v = take_rows(2);
+                raw_k = load_raw(a.k, a.k_scale, rows_v);
+            }
+        } else {
+            issue_next(1, ntile);
+        }
+    };
 
     // ---- read addresses ----------------------------------------------------
     // K fragment (32 tokens from row r0, step k): chunk 2 k + h of row r0 + n;
@@ -389,7 +470,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         issue_first();
         if constexpr (WIN)
             if (__any(gone) && lane == 0) found_gone = 1;
-        vm_wait<SH::LPT>();
+        vm_wait<E4 ? 0 : SH::LPT>();
 #pragma unroll
         for (int k = 0; k < KS; ++k) qf[k] = lds_read<V8>(qlds + (kread ^ (32 * k)));
         wg_barrier();  // K of tile 0 is in, every wave has its queries
@@ -481,7 +562,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     // K of tile j + 1 and V of tile j are in, and every wave is done with the
     // buffers that K of tile j + 2 and V of tile j + 1 go to
     auto turn = [&](int j) __device__ __attribute__((always_inline)) {
-        vm_wait<0>();
+        if constexpr (!E4) vm_wait<0>();
         wg_barrier();
         issue_next(j + 2, j + 1);
     };
@@ -785,21 +866,21 @@ __global__ __launch_bounds__(256) void prompt_join_kernel(PromptParams p) {
     store_row<T>(p.a.out, p.a.lse, (long long)(unit.y + row) * p.a.n_heads + kvh * p.G + (qi - row * p.G), c4, D, o, m, l);
 }
 
-template <bool WIN, typename T, int D>
+template <bool WIN, bool E4, typename T, int D>
 hipError_t launch_prompt_typed(const PromptParams &p, hipStream_t s) {
     const unsigned units = unsigned(p.slots) * p.a.n_kv_heads;
-    launch_kernel(WIN ? "window_chunks" : "prompt_attention", prompt_kernel<T, D, WIN>, dim3(units * p.nsplit), dim3(64 * kPromptWaves), s, p);
+    launch_kernel(WIN ? "window_chunks" : "prompt_attention", prompt_kernel<T, D, WIN, E4>, dim3(units * p.nsplit), dim3(64 * kPromptWaves), s, p);
     if (p.nsplit > 1)
         launch_kernel(WIN ? "window_join" : "prompt_join", prompt_join_kernel<T, D>, dim3(units, kPromptQueries * D / 1024), dim3(256), s, p);
     return hipGetLastError();
 }
 
-template <bool WIN, typename T>
+template <bool WIN, bool E4, typename T>
 hipError_t launch_prompt_dim(const PromptParams &p, hipStream_t s) {
     switch (p.a.head_dim) {
-        case 64: return launch_prompt_typed<WIN, T, 64>(p, s);
-        case 128: return launch_prompt_typed<WIN, T, 128>(p, s);
-        default: return launch_prompt_typed<WIN, T, 256>(p, s);
+        case 64: return launch_prompt_typed<WIN, E4, T, 64>(p, s);
+        case 128: return launch_prompt_typed<WIN, E4, T, 128>(p, s);
+        default: return launch_prompt_typed<WIN, E4, T, 256>(p, s);
     }
 }
 
@@ -813,7 +894,9 @@ hipError_t launch_prompt_any(const PromptArgs &a, const PromptPlan &plan, const 
     p.slots = plan.slots;
     p.pshift = WIN ? log2_of(a.page_size) : 0;
     p.c = a.scale * kLog2e;
-    return a.dtype == DSPARK_BF16 ? launch_prompt_dim<WIN, TypeBf16>(p, s) : launch_prompt_dim<WIN, TypeF16>(p, s);
+    if constexpr (WIN)
+        if (a.k_scale) return a.dtype == DSPARK_BF16 ? launch_prompt_dim<WIN, true, TypeBf16>(p, s) : hipErrorInvalidValue;
+    return a.dtype == DSPARK_BF16 ? launch_prompt_dim<WIN, false, TypeBf16>(p, s) : launch_prompt_dim<WIN, false, TypeF16>(p, s);
 }
 
 }  // namespace

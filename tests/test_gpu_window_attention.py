@@ -166,7 +166,11 @@ def test_a_window_of_everything_is_paged_attention():
             b = ds.dspark_window_attention(q, dev["k_cache"], dev["v_cache"], _i32(past), table, window, sinks=sinks,
                                            row_offsets=off, lse=True, max_rows=7, k_scale=dev.get("k_scale"),
                                            v_scale=dev.get("v_scale"))
-            assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+            # both are within their roundings of the one definition (which kernel takes a call is a matter of sizes)
+            want, lse, tol, lse_tol = _want(q.cpu(), paged, rows, past, window, sinks, 128 ** -0.5, 0, dtype, cache)
+            for r in (a, b):
+                check("out", r["out"], want, tol)
+                check("lse", r["lse"], lse, lse_tol)
 
 
 def test_rows_past_the_table_see_what_is_left():
