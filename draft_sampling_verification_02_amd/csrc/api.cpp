@@ -662,7 +662,7 @@ int rotary_geometry(int dtype, int n_rows, int n_heads, int n_kv_heads, int v_he
         !head_dim_supported(head_dim) || rotary_dim % 16 != 0)
         return DSPARK_ERR_UNSUPPORTED;
     // a launch holds fewer than 2^32 threads, 256 a workgroup
-    if (n_heads + n_kv_heads > 0 && rotary_plan(n_rows, n_heads + n_kv_heads + v_heads, head_dim).blocks >= (1 << 24))
+    if (n_heads + n_kv_heads > 0 && rotary_plan(n_rows, n_heads + n_kv_heads + v_heads, head_dim, false).blocks >= (1 << 24))
         return DSPARK_ERR_ARG;
     return DSPARK_OK;
 }
@@ -807,7 +807,7 @@ int dspark_rotary(const void *q, const void *k, int64_t q_stride, int64_t k_stri
     a.k_norm = k_norm;
     a.norm_dtype = norm_dtype;
     a.eps = eps;
-    const RotaryPlan plan = rotary_plan(n_rows, n_heads + n_kv_heads, head_dim);
+    const RotaryPlan plan = rotary_plan(n_rows, n_heads + n_kv_heads, head_dim, false);
     return launch_rotary(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
 }
 
@@ -863,7 +863,7 @@ int dspark_kv_append(const void *q, const void *k, const void *v, int64_t q_stri
     a.k_norm = k_norm;
     a.norm_dtype = norm_dtype;
     a.eps = eps;
-    const RotaryPlan plan = rotary_plan(n_rows, n_heads + 2 * n_kv_heads, head_dim);
+    const RotaryPlan plan = rotary_plan(n_rows, n_heads + 2 * n_kv_heads, head_dim, true);
     return launch_rotary(a, plan, static_cast<hipStream_t>(stream)) == hipSuccess ? DSPARK_OK : DSPARK_ERR_HIP;
 }
 

@@ -292,7 +292,7 @@ struct RotaryPlan {
     int per_row, per_block;
     bool many;
 };
-RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim);
+RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim, bool to_cache);
 hipError_t launch_rotary(const RotaryArgs &a, const RotaryPlan &p, hipStream_t s);
 
 // The split of a paged attention call.

@@ -475,8 +475,10 @@ PyObject *logit_rules(PyObject *, PyObject *const *a, Py_ssize_t n) {
         values = c.at_dense<float>(a[11], at::kFloat, {n_biases});
     }
     int32_t *index = c.at_dense_or_none<int32_t>(a[13], at::kInt, {rows});
-    if (!c.ok || (history && !history_len) || (masks && (!index || words < (V + 31) / 32))) Py_RETURN_NONE;
-    if (masks) n_masks = THPVariable_Unpack(a[12]).size(0);
+    // (an empty tensor has no address: what is there is told by the argument)
+    const bool masked = a[12] != Py_None;
+    if (!c.ok || (a[2] != Py_None && !history_len) || (masked && (!index || words < (V + 31) / 32))) Py_RETURN_NONE;
+    if (masked) n_masks = THPVariable_Unpack(a[12]).size(0);
     void *s = nullptr;
     if (!c.stream(s)) Py_RETURN_NONE;
     return PyLong_FromLong(entry.rules(x->data_ptr(), stride, dt, off, int(rows), int(B), int(V), history, int(width),

@@ -28,7 +28,8 @@ namespace dspark {
 namespace {
 
 constexpr int kTableFloats = 4096;  // cosines and sines of a workgroup's rows
-constexpr int kRotaryItems = 4;     // items of a thread when there are many
+constexpr int kRotaryItems = 2;     // items of a thread
+constexpr int kManyItems = 4;       // where many go into a cache
 
 struct RotaryParams {
     RotaryArgs a;
@@ -289,10 +290,9 @@ __global__ __launch_bounds__(kCacheThreads) void rotary_kernel(RotaryParams p) {
 template <typename T, int D, int MODE>
 void launch_rotary_items(const RotaryParams &p, bool many, int blocks, hipStream_t s) {
     const char *name = MODE == kToRows ? "rotary" : "kv_append";
-    if (many)
-        launch_kernel(name, rotary_kernel<T, D, MODE, kRotaryItems>, dim3(blocks), dim3(kCacheThreads), s, p);
-    else
-        launch_kernel(name, rotary_kernel<T, D, MODE, 1>, dim3(blocks), dim3(kCacheThreads), s, p);
+    if constexpr (MODE != kToRows)
+        if (many) return launch_kernel(name, rotary_kernel<T, D, MODE, kManyItems>, dim3(blocks), dim3(kCacheThreads), s, p);
+    launch_kernel(name, rotary_kernel<T, D, MODE, kRotaryItems>, dim3(blocks), dim3(kCacheThreads), s, p);
 }
 
 template <typename T, int D>
@@ -317,12 +317,17 @@ void launch_rotary_dim(const RotaryParams &p, bool many, int blocks, hipStream_t
 }  // namespace
 
 // A workgroup takes whole heads, and no more rows than its table of angles holds.
-RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim) {
+// Us a call in 1 / 2 / 4 items a thread (32/8 heads, D = 128, normed): rotation of 64
+// rows 5.3 / 4.8 / 6.3, 1000 7.6 / 6.9 / 8.2, 4000 22 / 19 / 21, 37,800 161 / 149 /
+// 149; appends to 8 bits and their reading back, 1000 rows 13.7 / 13.5 / 15.1, 2000
+// 22.5 / 22.6 / 20.5, 16,000 150 / 136 / 124; appends of rows of 16/4 heads, D = 64,
+// in float16, 4000 8.1 / 8.1 / 9.1, 16,000 25.9 / 26.4 / 24.9, 50,000 69 / 70-74 / 68.
+RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim, bool to_cache) {
     RotaryPlan p{};
     p.per_row = heads * (head_dim / 16);
     p.items = n_rows * p.per_row;
-    p.many = p.items >= 2048LL * kCacheThreads;
-    p.per_block = std::min(p.many ? kCacheThreads * kRotaryItems : kCacheThreads, (kTableFloats / head_dim - 1) * p.per_row);
+    p.many = to_cache && p.items >= 2048LL * kCacheThreads;
+    p.per_block = std::min(kCacheThreads * (p.many ? kManyItems : kRotaryItems), (kTableFloats / head_dim - 1) * p.per_row);
     p.blocks = (p.items + p.per_block - 1) / p.per_block;
     return p;
 }

@@ -483,7 +483,7 @@ int dspark_logit_rules(const void *logits, int64_t stride, int dtype, const int3
  * (otherwise DSPARK_ERR_UNSUPPORTED).  n_rows = 0 is valid and does nothing.
  * One launch takes all of a call: n_rows * n_heads is below 2^31, the K and V
  * of a write or read are below 256 GiB, the rows of a rotation or an append
- * below 512 GiB, and n_rows * n_heads / 128 + (B + 1) * n_kv_heads of a prompt
+ * too, and n_rows * n_heads / 128 + (B + 1) * n_kv_heads of a prompt
  * call is below 2^24 (otherwise DSPARK_ERR_ARG).  Calls
  * that may overlap in time, on two streams or in two captured graphs, need a
  * workspace each.

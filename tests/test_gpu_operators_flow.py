@@ -1,0 +1,239 @@
+"""Rotation, appends, windowed attention and logit rules together, as a target
+forward with a local layer uses them: prompts enter the cache in chunks, verify
+rows are appended and attend through the window, their logits keep to penalties and
+a grammar, and dspark_verify draws from them; the same captured and replayed."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from attendkit import U, U32, attend, check, dequantise, offsets, quantise
+from test_gpu_rotary import turned
+
+pytestmark = pytest.mark.gpu
+
+BF, FH, E4, I32 = torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.int32
+EPS = 1e-5
+
+
+def _ds():
+    import draft_sampling_verification_02_amd as ds
+    ds.load_library()
+    return ds
+
+
+class Layer:
+    """Rows of a fused projection by token, norms, frequencies, an output matrix."""
+    V, Hq, Hkv, D, R = 1000, 8, 2, 64, 16
+
+    def __init__(self, seed):
+        g = torch.Generator().manual_seed(seed)
+        r = lambda *s: torch.randn(s, generator=g)
+        self.qkv = r(self.V, self.Hq + 2 * self.Hkv, self.D).to(BF)
+        self.wq, self.wk = ((1 + 0.2 * r(self.D)).to(BF) for _ in range(2))
+        self.freq = (10000.0 ** (-torch.arange(0, 64, 2) / 64)).float()
+        self.out = r(self.V, self.Hq * self.D) * 0.3
+        self.W1, self.W2 = (r(self.V, self.R) * 0.3).to(BF), (r(self.V, self.R) * 0.3).to(BF)
+
+    def split(self, t):
+        return t[:, :self.Hq], t[:, self.Hq:self.Hq + self.Hkv], t[:, self.Hq + self.Hkv:]
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_chunks_of_prompts_then_verify_rounds(cache):
+    ds = _ds()
+    m, dev = Layer(3), "cuda"
+    Hq, Hkv, D, V = m.Hq, m.Hkv, m.D, m.V
+    window, sinks, page, gamma = 70, 5, 16, 4
+    g = torch.Generator().manual_seed(8)
+    lens = [200, 3, 131]
+    B = len(lens)
+    texts = [torch.randint(0, V, (n,), generator=g).tolist() for n in lens]
+    width = (max(lens) + 40) // page + 2
+    table = torch.randperm(B * width, generator=g).to(I32).reshape(B, width).to(dev)
+    kc, vc = (torch.full((B * width, Hkv, page, D), float("nan")).to(cache).to(dev) for _ in range(2))
+    sc = {} if cache == BF else {n: torch.zeros((B * width, Hkv, page), dtype=torch.uint8, device=dev) for n in ("k_scale", "v_scale")}
+    qkv = m.qkv.to(dev)
+    turn = dict(q_norm=m.wq.to(dev), k_norm=m.wk.to(dev), eps=EPS)
+    freq = m.freq.to(dev)
+
+    def step(tokens, past, max_rows):
+        off = offsets([len(t) for t in tokens]).to(dev)
+        rows = qkv[torch.tensor(sum(tokens, []), device=dev)]
+        q, k, v = m.split(rows)
+        ln = torch.tensor(past, dtype=I32, device=dev)
+        q = ds.dspark_kv_append(q, k, v, freq, kc, vc, ln, table, row_offsets=off, **sc, **turn)["q"]
+        r = ds.dspark_window_attention(q, kc, vc, ln, table, window, sinks=sinks, row_offsets=off, lse=True, max_rows=max_rows, **sc)
+        return q, r, off
+
+    def expect(tokens, past, q, r, off):
+        for b, new in enumerate(tokens):
+            text = torch.tensor(texts[b][:past[b]] + new)
+            _, k, v = m.split(m.qkv[text])
+            # keys as the cache holds them: what was read back stands for them, within the roundings that are tested elsewhere
+            back = ds.dspark_kv_read(kc, vc, table[b:b + 1], len(text), row_offsets=torch.tensor([0, len(text)], dtype=I32, device=dev), **sc)
+            want, mag = turned(k, torch.arange(len(text)), m.freq, m.wk, False)
+            step8 = 2.0 ** -4 * want.abs() + 2.0 ** -9 * want.abs().amax(-1, keepdim=True)
+            assert bool(((back["k"].cpu().double() - want).abs() <= (step8 if cache == E4 else 2.0 ** -8 * want.abs()) + 2.0 ** -12 * mag).all())
+            for i in range(len(new)):
+                p = past[b] + i
+                t = [x for x in range(p + 1) if x < sinks or p - x < window]
+                row = int(off[b]) + i
+                o, z, tol, lt = attend(q[row:row + 1].cpu().double(), back["k"][t].cpu().double(), back["v"][t].cpu().double(),
+                                       [len(t)], D ** -0.5, U[BF], U[BF])
+                check("out", r["out"][row:row + 1], o, tol)
+                check("lse", r["lse"][row:row + 1], z, lt)
+
+    # ---- the prompts, 64 rows at a time
+    done = [0] * B
+    while any(d < n for d, n in zip(done, lens)):
+        chunk = [texts[b][done[b]:done[b] + 64] for b in range(B)]
+        q, r, off = step(chunk, done, 64)
+        expect(chunk, done, q, r, off)
+        done = [d + len(c) for d, c in zip(done, chunk)]
+
+    # ---- rounds: drafts, target rows with rules, verification
+    anchor = torch.tensor([7, 8, 9], dtype=I32)
+    texts = [t + [int(a)] for t, a in zip(texts, anchor)]
+    history = torch.zeros((B, 400), dtype=I32)
+    allowed = torch.rand((3, 32 * 32), generator=g) < 0.5
+    allowed[:, V:] = False
+    bits = (allowed.reshape(3, 32, 32).long() << torch.arange(32)).sum(-1)
+    masks = torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(I32).to(dev)
+    rep, fre, pre = (torch.tensor(x, device=dev) for x in ([1.2, 1.0, 0.9], [0.0, 0.3, 0.2], [0.4, 0.0, -0.1]))
+    temperature = torch.tensor([1.0, 0.0, 1.0], device=dev)
+    W1, W2 = m.W1.to(dev), m.W2.to(dev)
+    for rnd in range(4):
+        U_logits = torch.randn((B, gamma, V), generator=g).to(dev)
+        ell = torch.randint(0, gamma + 1, (B,), generator=g).to(I32)
+        past = [len(t) - 1 for t in texts]  # the anchor is not in the cache yet
+        last = torch.tensor([t[-1] for t in texts], dtype=I32, device=dev)
+        d = ds.dspark_draft_sample(U_logits, W1, W2, last, temperature, 5, rnd)
+        x = d["x"].cpu()
+        rows = [[texts[b][-1]] + x[b, :int(ell[b])].tolist() for b in range(B)]
+        q, r, off = step(rows, past, gamma + 1)
+        expect(rows, past, q, r, off)
+        logits = (r["out"].float().reshape(len(q), -1) @ m.out.to(dev).t()).to(BF)
+        for b in range(B):
+            history[b, :len(texts[b])] = torch.tensor(texts[b], dtype=I32)
+        index = torch.tensor([b for b in range(B) for _ in rows[b]], dtype=I32)
+        target = ds.dspark_logit_rules(logits, row_offsets=off, history=history.to(dev),
+                                       history_len=torch.tensor([len(t) for t in texts], dtype=I32, device=dev),
+                                       prompt_len=torch.tensor(lens, dtype=I32, device=dev), drafts=d["x"], repetition=rep,
+                                       frequency=fre, presence=pre, masks=masks, mask_index=index.to(dev))
+        for b in range(B):
+            for j, row in enumerate(range(int(off[b]), int(off[b + 1]))):
+                z = logits[row].cpu().double()
+                said = texts[b][lens[b]:] + x[b, :j].tolist()
+                for t in set(texts[b] + said):
+                    z[t] = z[t] / float(rep[b]) if z[t] > 0 else z[t] * float(rep[b])
+                    if said.count(t):
+                        z[t] -= float(fre[b]) * said.count(t) + float(pre[b])
+                got = target[row].cpu().double()
+                keep = allowed[b, :V]
+                assert bool(torch.isinf(got[~keep]).all())
+                assert bool(((got - z).abs()[keep] <= 4 * U32 * (z.abs()[keep] * 1.3 + 3)).all())
+        v = ds.dspark_verify(target, ell.to(dev), U_logits, W1, W2, last, d["x"], d["lse"], d["qx"], temperature, 5, rnd,
+                             row_offsets=off)
+        for b in range(B):
+            n = int(v["n"][b])
+            new = v["tokens"][b, :n + 1].tolist()
+            assert all(allowed[b, t] for t in new), "a token that the grammar forbids was emitted"
+            texts[b] += new
+
+
+def test_a_captured_round_follows_its_inputs():
+    ds = _ds()
+    m, dev = Layer(5), "cuda"
+    B, page, width, window, sinks, gamma = 3, 16, 30, 50, 4, 3
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(1)).to(I32).reshape(B, width).to(dev)
+    freq, wk = m.freq.to(dev), m.wk.to(dev)
+    W = m.out.to(dev).t().contiguous()
+    for cache, chunk in ((BF, 4), (E4, 4), (BF, 70), (E4, 70)):
+        n = B * chunk
+        kc, vc = (torch.zeros((B * width, m.Hkv, page, m.D), device=dev).to(cache) for _ in range(2))
+        sc = {} if cache == BF else {s: torch.full((B * width, m.Hkv, page), 127, dtype=torch.uint8, device=dev) for s in ("k_scale", "v_scale")}
+        rows = torch.randn(n, m.Hq + 2 * m.Hkv, m.D, device=dev).to(BF)
+        off, ln = offsets([chunk] * B).to(dev), torch.tensor([100, 3, 0], dtype=I32, device=dev)
+        hist, hl = torch.randint(0, m.V, (B, 60), device=dev).to(I32), torch.tensor([60, 9, 0], dtype=I32, device=dev)
+        drafts = torch.randint(0, m.V, (B, gamma), device=dev).to(I32)
+        rep = torch.full((B,), 1.3, device=dev)
+        q, k, v = m.split(rows)
+        res = {"q": {"q": torch.empty_like(q)}, "at": {"out": torch.empty((n, m.Hq, m.D), dtype=BF, device=dev), "lse": torch.empty((n, m.Hq), device=dev)},
+               "z": torch.empty((n, m.V), device=dev)}
+
+        def round_(res):
+            ds.dspark_kv_append(q, k, v, freq, kc, vc, ln, table, row_offsets=off, k_norm=wk, out=res["q"], **sc)
+            ds.dspark_window_attention(res["q"]["q"], kc, vc, ln, table, window, sinks=sinks, row_offsets=off, lse=True,
+                                       max_rows=chunk, out=res["at"], **sc)
+            o = res["at"]["out"].float().reshape(n, -1)
+            ds.dspark_logit_rules(torch.mm(o, W), row_offsets=off, history=hist, history_len=hl, drafts=drafts, repetition=rep,
+                                  out=res["z"])
+
+        round_(res)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            round_(res)
+        for lens, layout in (([100, 3, 0], [chunk] * B), ([7, 300, 55], [chunk] * B), ([250, -1, 16], [chunk, 0, 2 * chunk]), ([0, 90, 200], [1, chunk, chunk])):
+            ln.copy_(torch.tensor(lens, dtype=I32))
+            off.copy_(offsets(layout))
+            rows.copy_(torch.randn(n, m.Hq + 2 * m.Hkv, m.D, device=dev).to(BF))
+            hl.copy_(torch.tensor([abs(x) % 61 for x in lens], dtype=I32))
+            kc.copy_(torch.zeros_like(kc.float()).to(cache)), vc.copy_(torch.zeros_like(vc.float()).to(cache))
+            for t in (res["q"]["q"], res["at"]["out"], res["at"]["lse"], res["z"]):
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in (res["q"]["q"], res["at"]["out"], res["at"]["lse"], res["z"], kc.view(torch.uint8), vc.view(torch.uint8))]
+            for t in (res["q"]["q"], res["at"]["out"], res["at"]["lse"], res["z"]):
+                t.zero_()
+            kc.copy_(torch.zeros_like(kc.float()).to(cache)), vc.copy_(torch.zeros_like(vc.float()).to(cache))
+            round_(res)
+            torch.cuda.synchronize()
+            for a, b in zip(got, (res["q"]["q"], res["at"]["out"], res["at"]["lse"], res["z"], kc.view(torch.uint8), vc.view(torch.uint8))):
+                assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_calls_on_two_streams_keep_apart():
+    ds = _ds()
+    m, dev = Layer(6), "cuda"
+    freq = m.freq.to(dev)
+    B, page, width = 4, 16, 80
+    side = [torch.cuda.Stream() for _ in range(2)]
+    inputs = []
+    for s in range(2):
+        g = torch.Generator().manual_seed(s)
+        rows = torch.randn((B * 30, m.Hq + 2 * m.Hkv, m.D), generator=g).to(BF).to(dev)
+        table = torch.randperm(B * width, generator=g).to(I32).reshape(B, width).to(dev)
+        caches = [torch.randn((B * width, m.Hkv, page, m.D), generator=g).to(BF).to(dev) for _ in range(2)]
+        ln = torch.randint(0, 1200, (B,), generator=g).to(I32).to(dev)
+        inputs.append((rows, table, caches, ln, offsets([30] * B).to(dev), torch.randn((B * 30, 5000), generator=g).to(dev)))
+    torch.cuda.synchronize()
+
+    def run(x, stream):
+        rows, table, (kc, vc), ln, off, z = x
+        q, k, v = m.split(rows)
+        kc, vc = kc.clone(), vc.clone()
+        q = ds.dspark_kv_append(q, k, v, freq, kc, vc, ln, table, row_offsets=off, stream=stream)["q"]
+        out = []
+        for max_rows in (30, 1):
+            out += list(ds.dspark_window_attention(q, kc, vc, ln, table, 700, sinks=3, row_offsets=off, lse=True, max_rows=max_rows,
+                                                   stream=stream)[n] for n in ("out", "lse"))
+        turned_ = ds.dspark_rotary(*m.split(rows)[:2], freq, row_offsets=off, first=ln, stream=stream)
+        return out + [kc, vc, q, turned_["q"], turned_["k"], ds.dspark_logit_rules(z, row_offsets=off, stream=stream)]
+
+    alone = []
+    for x in inputs:
+        alone.append(run(x, None))
+        torch.cuda.synchronize()
+    for _ in range(3):
+        both = []
+        for x, s in zip(inputs, side):
+            with torch.cuda.stream(s):
+                both.append(run(x, s))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            for t, u in zip(a, b):
+                assert torch.equal(t, u)
