@@ -8,10 +8,10 @@
 // over the pairs (i, j) = (m, m + rot / 2), or neighbours (2 m, 2 m + 1), m <
 // rot / 2; channels from rot on keep y.  Everything is in 32 bits and rounded
 // once, to the rows' type or to the 8-bit cache's (the scale then is that of the
-// 32-bit values).  An angle is far larger than what matters of it: p f / 2 pi is
-// taken in 64 bits, exact but for 2^-53 of it, and only its fraction is rounded
-// to 32 (an angle is off by 2^-53 p f + 2^-22).  A workgroup takes each angle
-// once, whatever the number of heads.
+// 32-bit values).  An angle is far larger than what matters of it: its turns p f /
+// 2 pi are taken in 64 bits, exact but for 2^-52 of them, and so are the cosine and
+// sine of their fraction.  A workgroup takes each angle once, whatever the number of
+// heads.
 //
 // Bound by memory: every row is read once and written once.  A work item is 16
 // values, two chunks of 8 that hold each other's pairs, so a rotation stays in
@@ -66,6 +66,28 @@ __device__ __forceinline__ float head_max(float x) {
     if constexpr (LANES >= 8) top(std::integral_constant<int, 0x141>{});
     if constexpr (LANES >= 16) top(std::integral_constant<int, 0x140>{});
     return x;
+}
+
+// Cosine and sine of an angle of -1/2 to 1/2 turns, off by half a step of float32 and
+// 2^-32: the Taylor series in 64 bits over an eighth of a turn to either side of the
+// nearest quarter, where what is left out is below x^13 / 13! = 7e-12 and x^12 / 12! =
+// 1.2e-10.  (In 32 bits the function's own error and that of its argument turn more
+// values of an 8-bit cache to the other neighbour.)
+__device__ __forceinline__ float2 cos_sin(double turn) {
+    const double q = rint(4. * turn), x = __builtin_fma(q, -0.25, turn) * 6.283185307179586, y = x * x;
+    double s = __builtin_fma(y, -1. / 39916800., 1. / 362880.);
+    s = __builtin_fma(y, s, -1. / 5040.);
+    s = __builtin_fma(y, s, 1. / 120.);
+    s = __builtin_fma(y, s, -1. / 6.);
+    s = __builtin_fma(x * y, s, x);
+    double c = __builtin_fma(y, -1. / 3628800., 1. / 40320.);
+    c = __builtin_fma(y, c, -1. / 720.);
+    c = __builtin_fma(y, c, 1. / 24.);
+    c = __builtin_fma(y, c, -1. / 2.);
+    c = __builtin_fma(y, c, 1.);
+    const int k = int(q) & 3;  // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
+    const float a = float(k & 1 ? s : c), b = float(k & 1 ? c : s);
+    return make_float2(k == 1 || k == 2 ? -a : a, k >= 2 ? -b : b);
 }
 
 template <typename T>
@@ -173,10 +195,9 @@ __global__ __launch_bounds__(kCacheThreads) void rotary_kernel(RotaryParams p) {
     for (int i = tid; i < rows * half; i += kCacheThreads) {
         const int r = int(unsigned(i) / unsigned(half)), m = i - r * half;
         const double turns = double(at[r]) * double(a.inv_freq[m]) * 0.15915494309189535;  // 1 / 2 pi
-        float s, co;
-        sincospif(2.f * float(turns - rint(turns)), &s, &co);
-        table[r * a.rot + m] = co;
-        table[r * a.rot + half + m] = s;
+        const float2 cs = cos_sin(turns - rint(turns));
+        table[r * a.rot + m] = cs.x;
+        table[r * a.rot + half + m] = cs.y;
     }
     __syncthreads();
 
@@ -317,11 +338,11 @@ void launch_rotary_dim(const RotaryParams &p, bool many, int blocks, hipStream_t
 }  // namespace
 
 // A workgroup takes whole heads, and no more rows than its table of angles holds.
-// Us a call in 1 / 2 / 4 items a thread (32/8 heads, D = 128, normed): rotation of 64
-// rows 5.3 / 4.8 / 6.3, 1000 7.6 / 6.9 / 8.2, 4000 22 / 19 / 21, 37,800 161 / 149 /
-// 149; appends to 8 bits and their reading back, 1000 rows 13.7 / 13.5 / 15.1, 2000
-// 22.5 / 22.6 / 20.5, 16,000 150 / 136 / 124; appends of rows of 16/4 heads, D = 64,
-// in float16, 4000 8.1 / 8.1 / 9.1, 16,000 25.9 / 26.4 / 24.9, 50,000 69 / 70-74 / 68.
+// Us a call in 2 / 4 items a thread: rotation (32/8 heads, D = 128, normed) of 64 rows
+// 5.3 / 6.3, 1000 7.0 / 8.3, 4000 19.9 / 20.8, 37,800 148 / 151 (one item 161); appends
+// of the same heads to 8 bits, with their reading back, 1000 rows 13.6 / 15.2, 2000
+// 22.5 / 20.6, 16,000 138 / 123; appends of 16/4 heads, D = 64, in float16, 4000 rows
+// 9.2 / 9.3, 16,000 26.6 / 24.6, 50,000 71 / 66.
 RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim, bool to_cache) {
     RotaryPlan p{};
     p.per_row = heads * (head_dim / 16);

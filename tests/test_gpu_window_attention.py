@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from attendkit import Paged, U, attend, check, offsets
+from attendkit import Paged, U, attend, check, far_inputs, far_tolerances, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -187,6 +187,79 @@ def test_rows_past_the_table_see_what_is_left():
         for i in range(3):
             t = [x for x in range(width * page) if x < sinks or (x <= at + i and at + i - x < window)]
             t = [x for x in t if x <= at + i]
+            out, lse, tol, lse_tol = attend(q[i:i + 1].double(), paged.tokens["k"][0][t], paged.tokens["v"][0][t], [len(t)],
+                                            D ** -0.5, U[BF], U[BF])
+            check("out", r["out"][i:i + 1], out, tol)
+            check("lse", r["lse"][i:i + 1], lse, lse_tol)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4), (FH, E4)])
+@pytest.mark.parametrize("rows,D", [(3, 128), (80, 64), (140, 128), (140, 256)])
+def test_pages_that_are_missing_are_left_out(dtype, cache, rows, D):
+    # pages inside the window and under the sinks, outside the cache on either side; page 0 holds NaN
+    ds = _ds()
+    Hq, Hkv, page, window, sinks, past = 4, 1, 16, 90, 40, 200
+    print(f"window: missing pages {dtype} {cache} rows={rows} D={D}", flush=True)
+    paged = Paged([past + rows], Hkv, D, page, dtype, cache, 5)
+    n_pages = paged.buf["k"].shape[0]
+    spare = next(x for x in range(1, n_pages) if x not in paged.table[0].tolist())
+    paged.table[paged.table == 0] = spare
+    for n in ("k", "v"):  # what lies in page 0 moves to a spare one
+        b = paged.buf[n].view(torch.uint8)
+        b[spare] = b[0]
+        paged.buf[n][0] = torch.full_like(paged.buf[n][0].float(), math.nan).to(paged.buf[n].dtype)
+        if paged.scale[n] is not None:
+            paged.scale[n][spare] = paged.scale[n][0]
+    missing = {0: -1, 8: n_pages, 12: -7, (past + rows - 1) // page: 1 << 30}
+    for i, x in missing.items():
+        paged.table[0, i] = x
+    q = torch.randn((rows, Hq, D), generator=torch.Generator().manual_seed(2)).to(dtype)
+    dev = paged.on("cuda")
+    r = ds.dspark_window_attention(q.cuda(), dev["k_cache"], dev["v_cache"], _i32([past]), dev["page_table"], window, sinks=sinks,
+                                   row_offsets=_i32([0, rows]), lse=True, max_rows=rows, k_scale=dev.get("k_scale"), v_scale=dev.get("v_scale"))
+    for i in range(rows):
+        t = [x for x in _sees(past + i, window, sinks) if x // page not in missing]
+        o, z, tol, lt = attend(q[i:i + 1].double(), paged.tokens["k"][0][t], paged.tokens["v"][0][t], [len(t)], D ** -0.5,
+                               _probability(dtype, cache), U[dtype], lift=7)
+        check("out", r["out"][i:i + 1], o, tol)
+        check("lse", r["lse"][i:i + 1], z, lt)
+
+
+@pytest.mark.parametrize("dtype", [BF, FH])
+@pytest.mark.parametrize("rows,D", [(4, 128), (100, 64), (100, 128)])
+def test_scores_far_from_zero(dtype, rows, D):
+    ds = _ds()
+    Hq, Hkv, page, window, sinks, past = 4, 2, 16, 60, 7, 90
+    print(f"window: far scores {dtype} rows={rows} D={D}", flush=True)
+    q, k, v, scale = far_inputs(rows, past + rows, Hq, Hkv, D, dtype, 4)
+    paged = Paged([past + rows], Hkv, D, page, dtype, dtype, 5)
+    for t in range(past + rows):
+        pg = int(paged.table[0, t // page])
+        paged.buf["k"][pg, :, t % page], paged.buf["v"][pg, :, t % page] = k[t], v[t]
+    dev = paged.on("cuda")
+    r = ds.dspark_window_attention(q.cuda(), dev["k_cache"], dev["v_cache"], _i32([past]), dev["page_table"], window, sinks=sinks,
+                                   row_offsets=_i32([0, rows]), lse=True, max_rows=rows, scale=scale)
+    for i in range(rows):
+        t = _sees(past + i, window, sinks)
+        out, lse, tol, lse_tol = attend(q[i:i + 1].double(), k[t].double(), v[t].double(), [len(t)], scale, U[dtype], U[dtype], lift=7)
+        if i % 3 == 0:
+            tol, lse_tol = far_tolerances(out, lse, tol, lse_tol, v[t].double(), U[dtype])
+        check("out", r["out"][i:i + 1], out, tol)
+        check("lse", r["lse"][i:i + 1], lse, lse_tol)
+
+
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_chunks_past_the_table_see_what_is_left(cache):
+    ds = _ds()
+    D, page, width, rows = 128, 16, 8, 70
+    paged = Paged([128], 1, D, page, BF, cache, 9, width=width)
+    dev = paged.on("cuda")
+    q = torch.randn((rows, 4, D), generator=torch.Generator().manual_seed(3)).to(BF)
+    for past, window, sinks in ((100, 20, 4), (140, 20, 70), (500, 20, 0), (90, 50, 0)):
+        r = ds.dspark_window_attention(q.cuda(), dev["k_cache"], dev["v_cache"], _i32([past]), dev["page_table"], window, sinks=sinks,
+                                       row_offsets=_i32([0, rows]), lse=True, k_scale=dev.get("k_scale"), v_scale=dev.get("v_scale"))
+        for i in range(rows):
+            t = [x for x in _sees(past + i, window, sinks) if x < width * page]
             out, lse, tol, lse_tol = attend(q[i:i + 1].double(), paged.tokens["k"][0][t], paged.tokens["v"][0][t], [len(t)],
                                             D ** -0.5, U[BF], U[BF])
             check("out", r["out"][i:i + 1], out, tol)
