@@ -255,13 +255,20 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         }
     };
     // Windowed calls: a tile's four runs of 16 tokens lie in a page each, whose ids are scalar loads, read one tile ahead
-    // of K's issue; the rows of the cache that they make serve K and, a tile later, V.  A run without a page reads page
-    // 0, and its tokens are hidden.
+    // of K's issue; the places in the cache that they make serve K and, a tile later, V.  A run without a page reads the
+    // last page, and its tokens are hidden.
     const TableInts table = WIN ? (TableInts)(a.page_table + (long long)request * a.max_pages) : (TableInts) nullptr;
     struct Runs {
-        uint32_t at[4];  // (all rows of a cache in memory fit 32 bits: a row has 128 bytes at least)
+        uint32_t at[4];  // page ids; rows of an 8-bit cache (all there can be in memory fit 32 bits: 64 bytes at least)
     };
-    Runs ids{}, rows_v{};  // page ids of the tile that K is issued for next (from token `ahead`), rows of V's
+    struct Places {
+        uint64_t at[4];  // bytes from the start of a 16-bit cache
+    };
+    using Rows = typename std::conditional<E4, Runs, Places>::type;
+    Runs ids{};  // of the tile that K is issued for next, from token `ahead` on
+    Rows rows_v{};
+    const uint32_t page_rows = uint32_t(a.n_kv_heads) << p.pshift, head_row = uint32_t(kvh) << p.pshift;
+    const uint32_t last_page = uint32_t(a.n_pages) - 1, in_page = (1u << p.pshift) - 1;
     int ahead = 0;
     auto fetch = [&](int t) __device__ __attribute__((always_inline)) {
         Runs g;
@@ -271,24 +278,27 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     };
     auto no_page = [&](uint32_t id) __device__ __attribute__((always_inline)) { return id >= uint32_t(a.n_pages); };
     auto rows_of = [&](const Runs &g, int t) __device__ __attribute__((always_inline)) {
-        Runs r;
+        Rows r;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t id = no_page(g.at[i]) ? 0u : g.at[i];
-            r.at[i] = ((id * uint32_t(a.n_kv_heads) + uint32_t(kvh)) << p.pshift) + uint32_t((t + 16 * i) & ((1 << p.pshift) - 1));
+            const uint32_t row = min(g.at[i], last_page) * page_rows + (head_row + (uint32_t(t + 16 * i) & in_page));
+            if constexpr (E4)
+                r.at[i] = row;
+            else
+                r.at[i] = uint64_t(row) * S::RB;
         }
         return r;
     };
     constexpr int RPW = 64 / S::CPR;  // rows a wave's load covers
     const uint32_t in_run = uint32_t(wave * RPW % 16 * S::RB);
-    auto issue_paged = [&](const void *src, const uint32_t *off, uint32_t dst, const Runs &r) __device__ __attribute__((always_inline)) {
+    auto issue_paged = [&](const void *src, const uint32_t *off, uint32_t dst, const Rows &r) __device__ __attribute__((always_inline)) {
         const uint8_t *from = static_cast<const uint8_t *>(src) + in_run;
 #pragma unroll
         for (int j = 0; j < SH::LPT; ++j) {
             // (the workgroup's rows j RPL .. + RPL - 1 are in one run, or two at D = 64)
-            uint32_t at = r.at[j * RPL / 16 % 4];
+            uint64_t at = r.at[j * RPL / 16 % 4];
             if constexpr (RPL >= 32) at = wave * RPW >= 16 ? r.at[(j * RPL / 16 + 1) % 4] : at;
-            dma16(uniform(dst + (j * NW + wave) * 1024), off[j % OFFS], uniform(from + uint64_t(at) * S::RB + j * RPL % 16 * S::RB));
+            dma16(uniform(dst + (j * NW + wave) * 1024), off[j % OFFS], uniform(from + at + j * RPL % 16 * S::RB));
         }
     };
     auto issue_k = [&](int j) __device__ __attribute__((always_inline)) {
@@ -304,14 +314,14 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         uint32_t scale[LOADS8];
     };
     Raw raw_k{}, raw_v{};
-    auto load_raw = [&](const void *src, const uint8_t *scales, const Runs &r) __device__ __attribute__((always_inline)) {
+    auto load_raw = [&](const void *src, const uint8_t *scales, const Rows &r) __device__ __attribute__((always_inline)) {
         Raw w;
         const int ln = int(fresh(uint32_t(lane)));  // (registers are short: the places are made anew)
 #pragma unroll
         for (int l = 0; l < LOADS8; ++l) {
             const int row = l * (SH::NT / LANES8) + wave * RPW8;  // the wave's first row, of one run
             const int run = row / 16;
-            const uint32_t at = (run & 2 ? (run & 1 ? r.at[3] : r.at[2]) : (run & 1 ? r.at[1] : r.at[0])) + uint32_t(row % 16);
+            const uint32_t at = uint32_t(run & 2 ? (run & 1 ? r.at[3] : r.at[2]) : (run & 1 ? r.at[1] : r.at[0])) + uint32_t(row % 16);
             const int mine = ln / LANES8;
             w.x[l] = *reinterpret_cast<const u32x4v_t *>(static_cast<const uint8_t *>(src) + uint64_t(at) * D + (mine * D + ln % LANES8 * 16));
             w.scale[l] = scales[uint64_t(at) + mine];
@@ -339,7 +349,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     auto store_v = [&](int j) __device__ __attribute__((always_inline)) { store_raw(raw_v, lds0 + (2 + (j & 1)) * S::BYTES, [](int r) __device__ __attribute__((always_inline)) { return S::v_swizzle(r); }); };
     // rows of the tile that `ids` are of, which move on to tile j + 1
     auto take_rows = [&](int j) __device__ __attribute__((always_inline)) {
-        const Runs r = rows_of(ids, ahead);
+        const Rows r = rows_of(ids, ahead);
         if (j + 1 < ntile) {
             ahead = tok(j + 1);
             ids = fetch(ahead);
@@ -358,7 +368,7 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
                 raw_k = load_raw(a.k, a.k_scale, rows_v);
             }
         } else if constexpr (WIN) {
-            const Runs rows_k = take_rows(jk);
+            const Rows rows_k = take_rows(jk);
             if (jk < ntile) issue_paged(a.k, koff, lds0 + (jk & 1) * S::BYTES, rows_k);
             if (jv < ntile) issue_paged(a.v, voff, lds0 + (2 + (jv & 1)) * S::BYTES, rows_v);
             rows_v = rows_k;
