@@ -191,8 +191,10 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
     const int base = past - a.window + 1;  // the first row's window starts here
     const int low = base + qrow, wlow_min = uniform(base + wq0 / p.G), wlow_max = uniform(base + wlast / p.G);
     WindowTiles wt;
+    int glow = 0;  // the first token of the workgroup's first window
     if constexpr (WIN) {
-        wt.make(a.sinks, base + block * SH::QB / p.G, base + glast / p.G, uniform(limit_of(block * SH::QB / p.G)),
+        glow = uniform(base + block * SH::QB / p.G);
+        wt.make(a.sinks, glow, base + glast / p.G, uniform(limit_of(block * SH::QB / p.G)),
                 uniform(limit_of(glast / p.G)));
         tiles = wt.count();
     }
@@ -450,12 +452,12 @@ __global__ __launch_bounds__(64 * kPromptWaves, PromptShape<D>::EU) void prompt_
         return join4<V8>(lds_read_tr16(at, r0 * S::RB), lds_read_tr16(at, (r0 + 8) * S::RB));
     };
 
-    // windowed calls: whether a run of the walk has no page
+    // windowed calls: whether a run that a query sees has no page
     bool gone = false;
     if constexpr (WIN) {
         for (int i = tid; i < 4 * ntile; i += SH::NT) {
             const int t = tok(i >> 2) + 16 * (i & 3);
-            gone |= t < L && no_page(uint32_t(a.page_table[(long long)request * a.max_pages + min(t >> p.pshift, a.max_pages - 1)]));
+            gone |= t < L && (t + 16 > glow || t < a.sinks) && no_page(uint32_t(a.page_table[(long long)request * a.max_pages + min(t >> p.pshift, a.max_pages - 1)]));
         }
     }
 
