@@ -980,8 +980,8 @@ int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const in
         a.dtype = dtype;
         a.q_offsets = row_offsets;
         a.start = cache_len;
-        a.k_scale = k_scale;
-        a.v_scale = v_scale;
+        a.k_scale = cache_dtype == DSPARK_E4M3 ? k_scale : nullptr;  // which tells the kernel the cache's type
+        a.v_scale = cache_dtype == DSPARK_E4M3 ? v_scale : nullptr;
         a.page_table = page_table;
         a.B = B;
         a.n_rows = n_rows;
@@ -1110,9 +1110,10 @@ int dspark_logit_rules(const void *logits, int64_t stride, int dtype, const int3
     if (int64_t(B) * ((V + 4095) / 4096) >= (1 << 23)) return DSPARK_ERR_ARG;  // a launch holds fewer than 2^32 threads
     if (dtype != DSPARK_BF16 && dtype != DSPARK_F16 && dtype != DSPARK_F32 && dtype != DSPARK_E4M3) return DSPARK_ERR_ARG;
     if (dtype == DSPARK_E4M3) return DSPARK_ERR_UNSUPPORTED;
-    if (history && (max_history < 0 || !history_len)) return DSPARK_ERR_ARG;
+    // (the kernel steps past the end of a text or a list by less than 2^14)
+    if (history && (max_history < 0 || max_history > DSPARK_MAX_CACHE_TOKENS || !history_len)) return DSPARK_ERR_ARG;
     if (drafts && (gamma < 0 || gamma > DSPARK_MAX_GAMMA)) return DSPARK_ERR_ARG;
-    if (n_biases < 0 || (bias_offsets && n_biases > 0 && (!bias_ids || !bias_values))) return DSPARK_ERR_ARG;
+    if (n_biases < 0 || n_biases > DSPARK_MAX_CACHE_TOKENS || (bias_offsets && n_biases > 0 && (!bias_ids || !bias_values))) return DSPARK_ERR_ARG;
     if (masks && (n_masks < 0 || mask_stride < (V + 31) / 32 || mask_stride > DSPARK_MAX_ROW_STRIDE || !mask_index))
         return DSPARK_ERR_ARG;
     if (n_rows == 0) return DSPARK_OK;

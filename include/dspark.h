@@ -427,7 +427,8 @@ int dspark_acceptance_rnn(const float *target, int n_target_rows, const int32_t 
  *               stands for no mask
  *   out         device [n_rows, V] float32, row stride out_stride (>= V): the logits
  *               themselves (float32, same stride), or rows that do not overlap them
- * Token ids outside [0, V) are passed over.  B * ceil(V / 4096) is below 2^23.
+ * Token ids outside [0, V) are passed over.  max_history and n_biases are at most
+ * DSPARK_MAX_CACHE_TOKENS, B * ceil(V / 4096) is below 2^23.
  * Counts are whole numbers and biases are added in their order: outputs are a pure
  * function of the inputs.  Lengths, offsets and indexes are read on the device, so
  * a captured call follows them as they change. */
@@ -603,7 +604,8 @@ size_t dspark_window_attention_workspace_size(int max_rows, int n_heads, int n_k
  *   window      >= 1
  *   sinks       >= 0
  *   max_rows    >= 1: how many rows a request usually has at most; picks the kernel
- *   everything else as for dspark_paged_attention */
+ *   everything else as for dspark_paged_attention (calls of many rows take the values
+ *   of an 8-bit cache in bfloat16: those past its largest, 3.39e38, are infinite) */
 int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
                             int max_rows, const int32_t *cache_len, const int32_t *page_table, int B, int max_pages,
                             int n_heads, int n_kv_heads, int head_dim, const void *k_cache, const void *v_cache,

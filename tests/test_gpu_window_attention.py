@@ -264,3 +264,34 @@ def test_chunks_past_the_table_see_what_is_left(cache):
                                             D ** -0.5, U[BF], U[BF])
             check("out", r["out"][i:i + 1], out, tol)
             check("lse", r["lse"][i:i + 1], lse, lse_tol)
+
+
+@pytest.mark.parametrize("rows", [2, 90])
+def test_scales_beside_a_16_bit_cache_are_not_looked_at(rows):
+    # the C entry point takes them as they come; the binding refuses them
+    ds = _ds()
+    paged = Paged([200 + rows], 2, 128, 16, BF, BF, 5)
+    dev = paged.on("cuda")
+    kc, vc, table = dev["k_cache"], dev["v_cache"], dev["page_table"]
+    q = torch.randn(rows, 4, 128, device="cuda").to(BF)
+    want = ds.dspark_window_attention(q, kc, vc, _i32([200]), table, 100, row_offsets=_i32([0, rows]), max_rows=rows, lse=True)
+    out, lse, off, ln = torch.zeros_like(q), torch.zeros(rows, 4, device="cuda"), _i32([0, rows]), _i32([200])
+    scales = torch.zeros(kc.shape[:3], dtype=torch.uint8, device="cuda")
+    ws = torch.empty(ds.dspark_window_attention_workspace_size(rows, 4, 2, 128), dtype=torch.uint8, device="cuda")
+    at = lambda t: t.data_ptr()
+    st = ds.load_library().dspark_window_attention(
+        at(q), 4 * 128, 0, at(off), rows, rows, at(ln), at(table), 1, table.shape[1], 4, 2, 128, at(kc), at(vc), at(scales),
+        at(scales), 0, kc.shape[0], 16, 100, 0, 128 ** -0.5, at(out), at(lse), at(ws), ws.numel(),
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == ds.DSPARK_OK and torch.equal(out, want["out"]) and torch.equal(lse, want["lse"])
+    with pytest.raises(ValueError, match="scale"):
+        ds.dspark_window_attention(q, kc, vc, ln, table, 100, row_offsets=off, k_scale=scales, v_scale=scales)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4)])
+def test_single_rows_by_the_kernel_of_chunks(dtype, cache):
+    # max_rows is a hint: one row a request without offsets, and few rows, where many are usual
+    _run(dtype, cache, 4, 2, 128, 16, [1] * 9, [0, 3, 63, 64, 65, 130, 333, -1, 20], 50, 5, max_rows=300)
+    _run(dtype, cache, 4, 2, 64, 32, [3, 0, 6, 1], [200, 3, 0, 500], 40, 70, lead=1, tail=2, max_rows=300)
+    _run(dtype, cache, 4, 1, 256, 16, [2, 1], [1500, 40], 900, 3, max_rows=300)

@@ -100,7 +100,7 @@ def test_window_workspaces():
 @pytest.mark.parametrize("change,status", [
     (dict(B=0), ARG), (dict(n=-1), ARG), (dict(off=None), ARG), (dict(V=0), ARG), (dict(V=1 << 24, stride=1 << 24), ARG),
     (dict(stride=999), ARG), (dict(os=999), ARG), (dict(stride=(1 << 24) + 1), ARG), (dict(dtype=3), UNSUPPORTED),
-    (dict(dtype=7), ARG), (dict(hlen=None), ARG), (dict(width=-1), ARG), (dict(gamma=-1), ARG), (dict(gamma=33), ARG),
+    (dict(dtype=7), ARG), (dict(hlen=None), ARG), (dict(width=-1), ARG), (dict(width=(1 << 30) + 1), ARG), (dict(nb=(1 << 30) + 1), ARG), (dict(gamma=-1), ARG), (dict(gamma=33), ARG),
     (dict(nb=-1), ARG), (dict(bid=None), ARG), (dict(bval=None), ARG), (dict(nm=-1), ARG), (dict(words=31), ARG),
     (dict(index=None), ARG), (dict(x=None), ARG), (dict(out=None), ARG), (dict(x=ctypes.c_void_p(0x10001)), ARG),
     (dict(x=ctypes.c_void_p(0x10002), dtype=1), ARG), (dict(out=ctypes.c_void_p(0x10002)), ARG), (dict(out=P), ARG),
