@@ -15,7 +15,7 @@
 // not depend on timing.  An entry that its mask forbids is not read.
 //
 // Measured (MI355X): 852 bfloat16 rows of 129,280 of 256 requests with texts up to
-// 4096, biases and masks 146-149 us (664 MB, 4.5 TB/s); one float16 row 4.9 us; 76
+// 4096, biases and masks 144-155 us (664 MB, 4.3 to 4.6 TB/s); one float16 row 4.9 us; 76
 // float32 rows of 50,257 with texts up to 60,000 27 us, of which the texts, read by
 // every slice's workgroup, take 9, five rows one after another 10.
 #include "dspark.h"
