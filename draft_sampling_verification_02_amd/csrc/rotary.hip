@@ -20,9 +20,9 @@
 // rows may be turned in place.
 //
 // Measured (MI355X, 32/8 heads, D = 128, bfloat16): 37,800 rows normed and turned
-// 146-158 us over cards (774 MB, 4.9 to 5.3 TB/s; a large copy reaches 4.75); 64 rows 3.6 us, 64 appended
-// 4.9; 853 normed rows of 256 requests into 8 bits 9.3 us; 50,000 rows of 16/4 heads,
-// D = 64, into a float16 cache 68 us (307 MB, 4.5 TB/s).
+// 146-158 us over cards (774 MB, 4.9 to 5.3 TB/s; a large copy reaches 4.75); 64 rows
+// 3.6 us, 64 appended 4.9; 853 normed rows of 256 requests into 8 bits 9.3 us; 50,000
+// rows of 16/4 heads, D = 64, into a float16 cache 68 us (307 MB, 4.5 TB/s).
 #include <algorithm>
 
 #include "dspark.h"
