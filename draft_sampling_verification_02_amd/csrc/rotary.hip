@@ -76,8 +76,7 @@ __device__ __forceinline__ float head_max(float x) {
 // Cosine and sine of an angle of -1/2 to 1/2 turns, off by half a step of float32 and
 // 2^-32: the Taylor series in 64 bits over an eighth of a turn to either side of the
 // nearest quarter, where what is left out is below x^13 / 13! = 7e-12 and x^12 / 12! =
-// 1.2e-10.  (In 32 bits the function's own error and that of its argument turn more
-// values of an 8-bit cache to the other neighbour.)
+// 1.2e-10.
 __device__ __forceinline__ float2 cos_sin(double turn) {
     const double q = rint(4. * turn), x = __builtin_fma(q, -0.25, turn) * 6.283185307179586, y = x * x;
     double s = __builtin_fma(y, -1. / 39916800., 1. / 362880.);

@@ -17,7 +17,7 @@
 // Measured (MI355X, 32/8 heads, D = 128): rows: 256 requests, window 1024, bfloat16
 // 193-202 us (1.07 GB, 5.3 to 5.5 TB/s); up to 6 rows of 128 requests, window 2048, 8 bits
 // 112-126 us (510 MB, 4.1 to 4.5 TB/s).  Chunks: eight of 300 to 2048 rows, window 4096
-// and 64 sinks, 577-612 us, 845 to 895 TFLOP/s of what rows see, over 8 bits 708-724;
+// and 64 sinks, 548-612 us, 845 to 940 TFLOP/s of what rows see, over 8 bits 708-724;
 // matrix units busy 46% of 1.8 GHz, a compute unit 90% of the call.
 #include "prompt.hpp"
 
