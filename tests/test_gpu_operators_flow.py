@@ -237,3 +237,42 @@ def test_calls_on_two_streams_keep_apart():
         for a, b in zip(alone, both):
             for t, u in zip(a, b):
                 assert torch.equal(t, u)
+
+
+@pytest.mark.parametrize("V", [1000, 997])
+def test_rows_under_a_grammar_are_minus_infinity_where_it_forbids(V):
+    # the sign counts: +inf there would make a forbidden token certain
+    ds = _ds()
+    m, dev = Layer(9), "cuda"
+    B, gamma = 3, 2
+    g = torch.Generator().manual_seed(6)
+    rows = [3, 1, 2]
+    off, index = offsets(rows).to(dev), torch.tensor([0, 0, 1, 2, 3, 3], dtype=I32)
+    allowed = torch.rand((4, 32 * 32), generator=g) < 0.3
+    allowed[:, V:] = False
+    bits = (allowed.reshape(4, 32, 32).long() << torch.arange(32)).sum(-1)
+    masks = torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(I32).to(dev)
+    logits = torch.randn((6, V), generator=g).to(BF)
+    for v in range(0, V, 7):  # what must not come through a mask
+        logits[v % 6, v] = (math.inf, -math.inf, math.nan)[v % 3] if not allowed[index[v % 6], v] else 1.0
+    ids = torch.arange(V, dtype=I32).repeat(B)
+    drafts = torch.tensor([[1, 2], [3, 4], [5, 6]], dtype=I32)
+    history = torch.randint(0, V, (B, 300), generator=g).to(I32)
+    f32 = lambda *v: torch.tensor(v, device=dev)
+    r = ds.dspark_logit_rules(logits.to(dev), row_offsets=off, history=history.to(dev), drafts=drafts.to(dev),
+                              history_len=torch.full((B,), 300, dtype=I32, device=dev), repetition=f32(0.5, 1.0, 3.0),
+                              frequency=f32(-0.5, 0.0, 0.2), presence=f32(-2.0, 0.0, 1.0), masks=masks, mask_index=index.to(dev),
+                              bias_offsets=torch.arange(B + 1, dtype=I32, device=dev) * V, bias_ids=ids.to(dev),
+                              bias_values=torch.full((B * V,), 4.0, device=dev))
+    keep = allowed[index.long(), :V]
+    assert bool((r.cpu()[~keep] == -math.inf).all()) and bool(torch.isfinite(r.cpu()[keep]).all())
+    U_logits = torch.randn((B, gamma, V), generator=g).to(dev)
+    W1, W2, t = m.W1[:V].contiguous().to(dev), m.W2[:V].contiguous().to(dev), torch.ones(B, device=dev)
+    last = torch.tensor([7, 8, 9], dtype=I32, device=dev)
+    for rnd in range(3):
+        d = ds.dspark_draft_sample(U_logits, W1, W2, last, t, 5, rnd)
+        v = ds.dspark_verify(r, torch.tensor([2, 0, 1], dtype=I32, device=dev), U_logits, W1, W2, last, d["x"], d["lse"], d["qx"],
+                             t, 5, rnd, row_offsets=off)
+        for b in range(B):
+            for j, token in enumerate(v["tokens"][b, :int(v["n"][b]) + 1].tolist()):
+                assert keep[int(off[b]) + j, token], (b, j, token)
