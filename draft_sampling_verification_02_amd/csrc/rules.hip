@@ -195,7 +195,7 @@ __global__ __launch_bounds__(NT) void rules_kernel(RulesParams p) {
                             if (c[w]) {
                                 const float n = float(c[w] & ~kInPrompt);
                                 const float y = z[w] > 0.f ? z[w] / rho : z[w] * rho;
-                                z[w] = y - (phi * n + (n > 0.f ? pi : 0.f));
+                                z[w] = n > 0.f ? y - (phi * n + pi) : y;  // (an infinite phi times none would be NaN)
                             }
                     }
                 }

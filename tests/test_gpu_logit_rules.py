@@ -234,3 +234,26 @@ def test_a_captured_call_follows_its_inputs():
         torch.cuda.synchronize()
         w, tol = want(cases[k], x[k])
         compare(out, w, tol)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_an_infinite_frequency_bans_what_was_generated_and_that_alone(dtype):
+    # c = 0 takes no part in frequency * c: tokens of the prompt keep what the repetition makes of them
+    V, off = 70, torch.tensor([0, 2], dtype=torch.int32).cuda()
+    history = torch.tensor([[3, 5, 5, 9, 11, -1, V, 69]], dtype=torch.int32).cuda()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()
+    f32 = lambda *v: torch.tensor(v).cuda()
+    x = torch.randn((2, V), generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[:, 3], x[:, 5], x[:, 9], x[0, 40] = 2.0, -3.0, -math.inf, math.inf
+    for sign in (1.0, -1.0):
+        r = _ds().dspark_logit_rules(x.cuda(), row_offsets=off, history=history, history_len=i32(8), prompt_len=i32(4),
+                                     drafts=i32(20).reshape(1, 1), repetition=f32(2.0), frequency=f32(sign * math.inf),
+                                     presence=f32(0.5)).cpu()
+        for j in range(2):
+            for t in range(V):
+                z = float(x[j, t])
+                if t in (3, 5, 9):
+                    z = z / 2 if z > 0 else z * 2
+                if t in (11, 69) or (t == 20 and j == 1):
+                    z = -sign * math.inf
+                assert float(r[j, t]) == z, (j, t, float(r[j, t]), z)
