@@ -257,3 +257,58 @@ def test_an_infinite_frequency_bans_what_was_generated_and_that_alone(dtype):
                 if t in (11, 69) or (t == 20 and j == 1):
                     z = -sign * math.inf
                 assert float(r[j, t]) == z, (j, t, float(r[j, t]), z)
+
+
+def _bias_call(V, B, ids, values, dtype=BF):
+    n = ids.numel()
+    off = (torch.arange(B + 1) * n).to(torch.int32).cuda()
+    dev = ids.repeat(B).cuda(), values.repeat(B).cuda()
+    x = torch.zeros((B, V), dtype=dtype, device="cuda")
+    return lambda: _ds().dspark_logit_rules(x, bias_offsets=off, bias_ids=dev[0], bias_values=dev[1])
+
+
+@pytest.mark.parametrize("V,B,text", [(2500, 2, 0), (2500, 2, 30000), (160000, 10, 0), (160000, 10, 20000)])
+@pytest.mark.parametrize("kinds", [1, 2, 40, 2000])
+def test_biases_of_few_tokens_are_added_in_the_order_of_their_list(V, B, text, kinds):
+    # of each choice of the slices; the repeated ones lie in one part of the list, in several, and next to each other
+    g = torch.Generator().manual_seed(kinds)
+    n = 3001
+    names = torch.randperm(V, generator=g)[:kinds]
+    ids = names[torch.randint(0, kinds, (n,), generator=g)].to(torch.int32)
+    ids[1000:1100], ids[5::97], ids[7::89] = int(names[0]), -1, V
+    values = torch.randn(n, generator=g) * torch.exp(3 * torch.randn(n, generator=g))
+    want = torch.zeros(V)
+    for t, x in zip(ids.tolist(), values):
+        if 0 <= t < V:
+            want[t] = want[t] + x
+    off = (torch.arange(B + 1) * n).to(torch.int32).cuda()
+    kw = {} if not text else dict(history=torch.zeros((B, text), dtype=torch.int32, device="cuda"),
+                                  history_len=torch.zeros(B, dtype=torch.int32, device="cuda"))
+    r = _ds().dspark_logit_rules(torch.zeros((B, V), device="cuda"), bias_offsets=off, bias_ids=ids.repeat(B).cuda(),
+                                 bias_values=values.repeat(B).cuda(), **kw).cpu()
+    for b in range(B):
+        assert torch.equal(r[b], want)
+
+
+def test_a_list_of_one_token_takes_about_as_long_as_one_of_many():
+    # a repeated token costs a pass over its part of the list, not a turn of the workgroup for each of its entries
+    V, n = 1000, 16384
+    g = torch.Generator().manual_seed(3)
+
+    def us(ids):
+        call = _bias_call(V, 1, ids.to(torch.int32), torch.ones(n))
+        best = math.inf
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            call()
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, 1000 * a.elapsed_time(b))
+        return best
+
+    many, one = us(torch.randint(0, V, (n,), generator=g) + V), us(torch.full((n,), 17))  # (ids past V: the scan alone)
+    print(f"biases: {n} of other tokens {many:.0f} us, of one token {one:.0f} us", flush=True)
+    # 64 parts of the list.  The scan of one: an exchange and two loads; its sums: at most 64 steps of two LDS reads and
+    # four sums beside that, 2 us at 2 GHz.  One entry a turn instead is 16384 turns of three barriers, more than 2 ms.
+    assert one < 8 * many + 200
