@@ -59,6 +59,7 @@ namespace {
 // 500: 17.6 / 12.6 / 12.1, 41.3 / 34.7 / 40.1 and 78.1 / 69.2 / 76.7.
 constexpr int kWholeTokens = 1024;
 constexpr int kFewSegments = 128;
+constexpr int kWindowWhole = 4096;  // tokens that a window and the sinks leave
 
 }  // namespace
 
@@ -79,13 +80,23 @@ PagedPlan paged_plan(const PagedSizes &z) {
     p.waves = 4;
     p.grid = 256 * paged_per_cu(z.e4, z.head_dim, p.qblocks, 4);
     p.whole = z.table_tokens <= kWholeTokens;
-    // Walks behind a window are all about as long as it, so that whole segments
-    // load the chip evenly once there are enough.  Us a call, split / whole (8 key
-    // heads, D = 128; one row, bfloat16, window 1500: 4 requests 15.4 / 16.0, 16
-    // 26.5 / 20.3, 64 86.6 / 74.1; window 8000: 4 30.4 / 49.9, 16 106 / 100, 64 356 /
-    // 352; up to 6 rows over 8 bits, window 2048: 8 25.6 / 29.3, 16 31.5 / 30.2, 128
-    // 142 / 115; window 8000: 16 65 / 88, 32 120 / 135, 64 222 / 199).
-    if (z.window && z.requests * z.n_kv_heads >= (z.e4 && z.table_tokens > 4096 ? 512 : 128)) p.whole = 1;
+    // Walks behind a window end at its length, so that whole segments may load the
+    // chip evenly once there are enough; but texts may be shorter, and a batch lasts
+    // as long as its longest segment then.  Us a call, split / whole, 8 key heads, of
+    // texts past the window; of 0 to 2 windows; one past it, the others up to 400:
+    //   one row, bfloat16, D = 128, window 1500
+    //     128 segments 27.3 / 17.6; 23.5 / 17.1; 15.0 / 15.7    512 65 / 64; 61 / 50; 24 / 25
+    //   3000    128 36.8 / 30.0; 30.3 / 25.5; 16.3 / 23.2       512 120 / 118; 116 / 97; 25 / 39
+    //   8000    128 85 / 79; 66 / 72; 23 / 49                   512 319 / 314; 260 / 249; 31 / 84
+    //   30,000  128 307 / 334; 275 / 326; 39 / 166              512 1251 / 1246; 969 / 989; 48 / 293
+    //   up to 6 rows over 8 bits, window 1500
+    //     128 segments 29.7 / 25.1; 24.2 / 24.0; 20.2 / 20.1    512 48 / 45; 69 / 43; 31 / 28
+    //   3000    128 31.6 / 40.8; 31.0 / 39.6; 20.1 / 38.6       512 78 / 74; 89 / 69; 28 / 47
+    //   8000    128 63 / 88; 53 / 85; 25 / 65                   512 191 / 180; 150 / 164; 38 / 136
+    //   the same, D = 256, window 1500
+    //     128 segments 47.1 / 53.2; 42.5 / 52.3; 29.2 / 39.7    512 109 / 106; 134 / 104; 61 / 78
+    if (z.window && z.table_tokens <= kWindowWhole)
+        p.whole |= z.requests * z.n_kv_heads >= (z.e4 && (z.table_tokens > 2048 || z.head_dim == 256) ? 512 : 128);
     if (p.whole && z.table_tokens > kUnit && z.requests * z.n_kv_heads <= kFewSegments &&
         paged_per_cu(z.e4, z.head_dim, p.qblocks, 8) >= 1)
         p.waves = 8;

@@ -295,3 +295,47 @@ def test_single_rows_by_the_kernel_of_chunks(dtype, cache):
     _run(dtype, cache, 4, 2, 128, 16, [1] * 9, [0, 3, 63, 64, 65, 130, 333, -1, 20], 50, 5, max_rows=300)
     _run(dtype, cache, 4, 2, 64, 32, [3, 0, 6, 1], [200, 3, 0, 500], 40, 70, lead=1, tail=2, max_rows=300)
     _run(dtype, cache, 4, 1, 256, 16, [2, 1], [1500, 40], 900, 3, max_rows=300)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (FH, FH), (BF, E4)])
+@pytest.mark.parametrize("window", [1500, 3900, 4500])
+def test_many_requests_of_which_few_are_long(dtype, cache, window):
+    # 128 walks (whole segments or parts of them, by the window's length), most of them far shorter than the window
+    past = [(37 * b) % 90 for b in range(64)]
+    past[5], past[60] = 5000, 4100
+    rows = [1 + b % 3 if cache == E4 else 1 for b in range(64)]
+    _run(dtype, cache, 4, 2, 64, 16, rows, past, window, 5, max_rows=3)
+
+
+@pytest.mark.parametrize("cache,n", [(BF, 16), (E4, 16), (E4, 64)])
+def test_one_long_text_of_many_is_shared_by_the_chip(cache, n):
+    # the n-th request, a short one, must not send the long one's heads to a workgroup each
+    ds = _ds()
+    Hq, Hkv, D, page, window = 32, 8, 128, 16, 30000
+    n_pages = window // page + 2
+    dev = dict(device="cuda")
+    if cache == E4:
+        kc, vc = (torch.randint(0, 100, (n_pages, Hkv, page, D), dtype=torch.uint8, **dev).view(E4) for _ in range(2))
+        sc = {n: torch.full((n_pages, Hkv, page), 120, dtype=torch.uint8, **dev) for n in ("k_scale", "v_scale")}
+    else:
+        kc, vc, sc = torch.randn((n_pages, Hkv, page, D), dtype=BF, **dev), torch.randn((n_pages, Hkv, page, D), dtype=BF, **dev), {}
+
+    def us(B):
+        q = torch.randn((B, Hq, D), dtype=BF, **dev)
+        table = torch.arange(n_pages, dtype=torch.int32, **dev).repeat(B, 2)  # room for texts of two windows
+        lens = _i32([window] + [100 + b for b in range(B - 1)])
+        out = ds.dspark_window_attention(q, kc, vc, lens, table, window, **sc)
+        best = math.inf
+        for _ in range(8):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                ds.dspark_window_attention(q, kc, vc, lens, table, window, out=out, **sc)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, 250 * a.elapsed_time(b))
+        return best
+
+    few, many = us(n - 1), us(n)
+    print(f"window: {cache} {n - 1} requests {few:.0f} us, {n} {many:.0f} us", flush=True)
+    assert many < 2 * few + 20  # the bytes are the same within a part in 200
