@@ -941,7 +941,9 @@ def dspark_window_attention(q, k_cache, v_cache, cache_len, page_table, window: 
     """dspark_paged_attention (causal) through a sliding window: the row at position
     p sees the `window` newest tokens, itself among them, and the first `sinks`
     tokens of its request.  Pages that no row of a request sees may be gone from
-    page_table.  Everything else as for dspark_paged_attention."""
+    page_table.  max_rows picks the kernel: where chunks stand beside single rows,
+    give the chunks' (the average would send them row by row).  Everything else as
+    for dspark_paged_attention."""
     if out is not None and stream is None and (not lse or "lse" in out):
         st = (_short or _load_marshal()).window_attention(
             q, k_cache, v_cache, cache_len, page_table, window, sinks, row_offsets, k_scale, v_scale, scale, max_rows,

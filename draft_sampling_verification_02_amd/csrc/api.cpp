@@ -676,8 +676,9 @@ bool rotary_rows_ok(const void *in, const void *out, int64_t stride, int64_t out
 
 // Whether a windowed call goes by query blocks (prompt.hpp), or row by row as paged
 // attention does (float16 rows over 8 bits always: their range there needs the
-// rows' kernel).  Us a call, rows / blocks (window 1000, four query heads a key
-// head; 64 requests of 8 key heads, D = 128: 16 rows 88 / 96, 20 138 / 85, 32 167 /
+// rows' kernel, though a chunk's blocks all walk from its first window to its last
+// row: 2000 rows behind 1024 tokens 363 us, 67 for bfloat16 rows).  Us a call, rows / blocks (window 1000, four query heads a key
+// head; 255 single rows beside a chunk of 2000, window 1024, 715 / 270; 64 requests of 8 key heads, D = 128: 16 rows 88 / 96, 20 138 / 85, 32 167 /
 // 117, 64 333 / 135; over 8 bits 16 rows 76 / 120, 32 141 / 142, 64 278 / 163; D = 64:
 // 32 rows 66 / 98, 48 98 / 103, 64 130 / 106, over 8 bits 32 83 / 114, 64 168 / 129;
 // 16 requests, D = 256: 16 rows 56 / 77, 20 86 / 78, 48 148 / 85, over 8 bits 32 88 /

@@ -9,8 +9,8 @@
 // rot / 2; channels from rot on keep y.  Everything is in 32 bits and rounded
 // once, to the rows' type or to the 8-bit cache's (the scale then is that of the
 // 32-bit values).  An angle is far larger than what matters of it: its turns p f /
-// 2 pi are taken in 64 bits, exact but for 2^-52 of them, and so are the cosine and
-// sine of their fraction.  A workgroup takes each angle once, whatever the number of
+// 2 pi are taken in 64 bits, off by 2^-51 of them at most (two products and a
+// constant, each rounded), and so are the cosine and sine of their fraction.  A workgroup takes each angle once, whatever the number of
 // heads.
 //
 // Bound by memory: every row is read once and written once.  A work item is 16
@@ -342,11 +342,11 @@ void launch_rotary_dim(const RotaryParams &p, bool many, int blocks, hipStream_t
 }  // namespace
 
 // A workgroup takes whole heads, and no more rows than its table of angles holds.
-// Us a call in 2 / 4 items a thread: rotation (32/8 heads, D = 128, normed) of 64 rows
-// 5.3 / 6.3, 1000 7.0 / 8.3, 4000 19.9 / 20.8, 37,800 148 / 151 (one item 161); appends
-// of the same heads to 8 bits, with their reading back, 1000 rows 13.6 / 15.2, 2000
-// 22.5 / 20.6, 16,000 138 / 123; appends of 16/4 heads, D = 64, in float16, 4000 rows
-// 9.2 / 9.3, 16,000 26.6 / 24.6, 50,000 71 / 66.
+// Us a call in 2 / 4 items a thread, captured (packed rows of 64 requests, normed):
+// rotation (32/8 heads, D = 128) of 64 rows 5.0 / 6.4, 1000 7.3 / 8.4, 4000 19.8 / 21.0,
+// 37,800 147 / 150 (one item 161); appends of the same heads to 8 bits, 1000 rows 8.0 /
+// 9.5, 2000 15.0 / 13.2, 16,000 81.7 / 76.3; appends of 16/4 heads, D = 64, in float16,
+// 4000 rows 8.1 / 9.6, 16,000 26.6 / 24.7, 50,000 68.6 / 64.6.
 RotaryPlan rotary_plan(long long n_rows, int heads, int head_dim, bool to_cache) {
     RotaryPlan p{};
     p.per_row = heads * (head_dim / 16);

@@ -17,8 +17,16 @@
 // Measured (MI355X, 32/8 heads, D = 128): rows: 256 requests, window 1024, bfloat16
 // 193-202 us (1.07 GB, 5.3 to 5.5 TB/s); up to 6 rows of 128 requests, window 2048, 8 bits
 // 112-126 us (510 MB, 4.1 to 4.5 TB/s).  Chunks: eight of 300 to 2048 rows, window 4096
-// and 64 sinks, 548-612 us, 845 to 940 TFLOP/s of what rows see, over 8 bits 708-724;
-// matrix units busy 46% of 1.8 GHz, a compute unit 90% of the call.
+// and 64 sinks, 548-612 us, 845 to 940 TFLOP/s of what rows see, over 8 bits 678-724;
+// matrix units busy 46% of 1.8 GHz, a compute unit 90% of the call.  float16 rows of the
+// same sizes: rows 200 us, over 8 bits 115 (one row, 256 requests) and 123 (up to 6,
+// 128); chunks 609, over 8 bits, where the rows' kernel takes them, 2152.
+//
+// Probabilities are rounded to 16 bits for the product with V (the operand of the matrix
+// instructions), sums and maxima are not.  Errors against 64 bits, relative and root mean
+// square: bfloat16 rows 0.0020, chunks 0.0024 (whose largest share need not be 1, so that
+// it is rounded too), where the outputs' own rounding alone makes 0.0017; float16 0.00026
+// and 0.00029 of 0.00021, over 8 bits, in two bfloat16 terms, no more than that.
 #include "prompt.hpp"
 
 namespace dspark {

@@ -519,8 +519,8 @@ int dspark_kv_read(const void *k_cache, const void *v_cache, const uint8_t *k_sc
  * neighbours (2 m, 2 m + 1) where `neighbours` is not 0; channels from rotary_dim
  * on keep y.  Row i of request b stands at position first[b] + i (first NULL = 0; a
  * negative first[b] takes the request out: its rows are not written, nor are rows
- * of no request).  Computed in float32, angles to 2^-53 of their size and 2^-21,
- * and rounded once.
+ * of no request).  Computed in float32, angles to 2^-51 of their size, and rounded
+ * once (a head whose squares sum past float32's range is normed to zeros).
  *   q, k        device rows of `dtype` (DSPARK_BF16 or DSPARK_F16), row strides
  *               q_stride and k_stride; one of the two may be absent (NULL, 0 heads)
  *   inv_freq    device [rotary_dim / 2] float32 (may be NULL where rotary_dim is 0)
@@ -603,9 +603,11 @@ size_t dspark_window_attention_workspace_size(int max_rows, int n_heads, int n_k
  * row of a request sees are not read: their pages may be gone from page_table.
  *   window      >= 1
  *   sinks       >= 0
- *   max_rows    >= 1: how many rows a request usually has at most; picks the kernel
- *   everything else as for dspark_paged_attention (calls of many rows take the values
- *   of an 8-bit cache in bfloat16: those past its largest, 3.39e38, are infinite) */
+ *   max_rows    >= 1: how many rows a request usually has at most (where chunks stand
+ *               beside single rows: the chunks'); picks the kernel
+ *   everything else as for dspark_paged_attention, the rounding of the probabilities
+ *   too (calls of many rows take the values of an 8-bit cache in bfloat16: those past
+ *   its largest, 3.39e38, are infinite) */
 int dspark_window_attention(const void *q, int64_t q_stride, int dtype, const int32_t *row_offsets, int n_rows,
                             int max_rows, const int32_t *cache_len, const int32_t *page_table, int B, int max_pages,
                             int n_heads, int n_kv_heads, int head_dim, const void *k_cache, const void *v_cache,
